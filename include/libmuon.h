@@ -256,6 +256,130 @@ float muon_lr_cooldown_floor(int64_t step, int64_t main_iterations, float cooldo
  * momentum = (1 - frac) start + frac end ([P3]: 500 steps, 0.85 -> 0.95). */
 float muon_momentum_warmup(int64_t step, int64_t warmup_steps, float start, float end);
 
+/* ---- layer operators ------------------------------------------------------
+ * The pass that makes the gradients muon_step reads, for the weight matrices
+ * its table holds: the linear layer (matrix product with bias, activation and
+ * residual in its epilogue) with its two gradients, and layer norm with its
+ * backward pass. Library plumbing, not defined by the pages.
+ *
+ * These calls take no handle and keep no state: everything they need is in
+ * their arguments, and they only enqueue kernels on `stream` of the current
+ * device (they may be captured into a graph, and calls on different streams
+ * may run at once as long as they share neither outputs nor workspace). Device
+ * pointers belong to the current device. Row strides are in elements; 0 means
+ * the row length. Sizes 0 of tokens / rows are allowed (the gradients of
+ * weights are then 0, or unchanged when accumulating, and tensors without
+ * elements may be NULL). Outputs may not overlap inputs, other outputs or the
+ * workspace, except that y / dx may be the very tensor of `add` (same address
+ * and stride): the sum then replaces it. Elements between rows (stride beyond
+ * the row length) are left as they were. Products and sums are held in fp32
+ * and rounded once to each output's type; no atomics are used, so the same
+ * call gives the same bits. Errors are muon_status codes, with the detail in
+ * muon_op_last_error; validation comes before any HIP call. */
+
+enum { MUON_TYPE_BF16 = 0, MUON_TYPE_FP16 = 1, MUON_TYPE_FP32 = 2 };
+enum {
+    MUON_WEIGHT_IN_OUT = 0, /* W [in_features, out_features], as the body's c_fc [d, 4d] */
+    MUON_WEIGHT_OUT_IN = 1  /* W [out_features, in_features] */
+};
+enum {
+    MUON_ACT_NONE = 0,
+    MUON_ACT_RELU = 1,
+    MUON_ACT_RELU2 = 2,     /* max(z, 0)^2 */
+    MUON_ACT_GELU = 3,      /* z (1 + erf(z / sqrt 2)) / 2 */
+    MUON_ACT_GELU_TANH = 4, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    MUON_ACT_SILU = 5       /* z / (1 + e^-z) */
+};
+enum { MUON_LINEAR_FORWARD = 0, MUON_LINEAR_GRAD_INPUT = 1, MUON_LINEAR_GRAD_WEIGHT = 2 };
+
+/* One linear layer on one batch. dtype (bf16 or fp16) is the type of X, W, Y
+ * and of their gradients dX, dY; bias and the weight gradients are float32.
+ * tokens < 2^24, features and strides at most 2^21. */
+typedef struct muon_linear {
+    int64_t tokens;
+    int64_t in_features;
+    int64_t out_features;
+    int64_t ld_x; /* X, dX [tokens, in_features] */
+    int64_t ld_w; /* W, dW in weight_layout */
+    int64_t ld_y; /* Y, dY [tokens, out_features] */
+    int32_t dtype;
+    int32_t weight_layout;
+} muon_linear;
+
+/* What happens to a product before its one rounding. */
+typedef struct muon_epilogue {
+    int32_t activation;
+    int32_t reserved;  /* must be 0 */
+    const float* bias; /* forward: [out_features], or NULL */
+    const void* add;   /* forward: residual [tokens, out_features]; grad input: another gradient of X
+                          [tokens, in_features]; or NULL */
+    int64_t ld_add;
+    void* z;           /* forward: where the pre-activation X W + bias goes, rounded [tokens, out_features], or
+                          NULL; grad input: read, the pre-activation [tokens, in_features] whose activation X
+                          was (NULL with MUON_ACT_NONE) */
+    int64_t ld_z;
+} muon_epilogue;
+
+/* Bytes of device workspace (256-byte aligned) the call `op` needs; often 0,
+ * and NULL is then accepted. a, b: the addresses of its two operands (forward:
+ * x, w; grad input: dy, w; grad weight: x, dy), of which only the alignment is
+ * looked at: operands whose rows do not start 16-byte aligned or whose length
+ * is no multiple of 8 are first copied to aligned rows in the workspace.
+ * Host-only. */
+muon_status muon_linear_workspace_bytes(const muon_linear* d, int32_t op, const void* a, const void* b,
+                                        size_t* out_bytes);
+
+/* Y = act(X W + bias) + add; e NULL: Y = X W. The activation is taken of the
+ * unrounded sum. */
+muon_status muon_linear_forward(const muon_linear* d, const void* x, const void* w, const muon_epilogue* e, void* y,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/* dX = (dY W^T) * act'(z) + add: with an activation this is the gradient of
+ * the previous layer's pre-activation, in one pass. act'(0) = 0 for relu. */
+muon_status muon_linear_grad_input(const muon_linear* d, const void* dy, const void* w, const muon_epilogue* e,
+                                   void* dx, void* workspace, size_t ws_bytes, void* stream);
+
+/* dW (+)= the product of X and dY over the tokens, in the weight's layout and
+ * float32: `dw` may point into the flat gradient buffer of muon_step. dbias
+ * [out_features] (+)= the sum of dY over the tokens, or NULL. accumulate != 0
+ * adds to what is there. */
+muon_status muon_linear_grad_weight(const muon_linear* d, const void* x, const void* dy, float* dw, float* dbias,
+                                    int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
+
+/* One layer norm on one batch of rows. dtype (any of the three) is the type
+ * of x, y and of their gradients; weight, bias, their gradients and the row
+ * statistics are float32. rows < 2^24, cols and strides at most 2^21. */
+typedef struct muon_layernorm {
+    int64_t rows;
+    int64_t cols;
+    int64_t ld_x;   /* x */
+    int64_t ld_y;   /* y, dy */
+    int64_t ld_dx;  /* dx */
+    int64_t ld_add; /* add */
+    int32_t dtype;
+    float eps;
+} muon_layernorm;
+
+/* y = (x - mean) rstd weight + bias per row, rstd = 1 / sqrt(var + eps) with
+ * the variance over the row (its elements' number as divisor). weight, bias
+ * [cols] or NULL (1, 0); mean, rstd [rows] are written. */
+muon_status muon_layernorm_forward(const muon_layernorm* d, const void* x, const float* weight, const float* bias,
+                                   void* y, float* mean, float* rstd, void* stream);
+
+/* Bytes of device workspace muon_layernorm_backward needs when it reduces a
+ * weight or bias gradient. Host-only. */
+muon_status muon_layernorm_workspace_bytes(const muon_layernorm* d, size_t* out_bytes);
+
+/* dx = the gradient of x from dy, + add (or NULL); dweight, dbias [cols] (+)=
+ * the sums over rows of dy (x - mean) rstd and of dy, each or NULL (with both
+ * NULL no workspace is needed). mean, rstd as the forward pass wrote them. */
+muon_status muon_layernorm_backward(const muon_layernorm* d, const void* dy, const void* x, const float* weight,
+                                    const float* mean, const float* rstd, const void* add, void* dx, float* dweight,
+                                    float* dbias, int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
+
+/* Detail of the last failed layer operator call on this thread ("" if none). */
+const char* muon_op_last_error(void);
+
 /* ---- measurement (benchmarks) -------------------------------------------
  * Library plumbing, not defined by the pages. */
 

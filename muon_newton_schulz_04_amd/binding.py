@@ -53,6 +53,22 @@ MUON_KERNEL_NS_PANEL = 7
 MUON_KERNEL_COUNT = 8
 KERNEL_NAMES = ["momentum", "gram", "poly", "update", "normuon", "apply", "ns_small", "ns_panel"]
 
+# layer operators
+MUON_TYPE_BF16 = 0
+MUON_TYPE_FP16 = 1
+MUON_TYPE_FP32 = 2
+MUON_WEIGHT_IN_OUT = 0
+MUON_WEIGHT_OUT_IN = 1
+MUON_ACT_NONE = 0
+MUON_ACT_RELU = 1
+MUON_ACT_RELU2 = 2
+MUON_ACT_GELU = 3
+MUON_ACT_GELU_TANH = 4
+MUON_ACT_SILU = 5
+MUON_LINEAR_FORWARD = 0
+MUON_LINEAR_GRAD_INPUT = 1
+MUON_LINEAR_GRAD_WEIGHT = 2
+
 
 class muon_matrix(ctypes.Structure):
     _fields_ = [
@@ -110,6 +126,44 @@ class muon_work(ctypes.Structure):
     ]
 
 
+class muon_linear(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64),
+        ("in_features", ctypes.c_int64),
+        ("out_features", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("ld_w", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("weight_layout", ctypes.c_int32),
+    ]
+
+
+class muon_epilogue(ctypes.Structure):
+    _fields_ = [
+        ("activation", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("bias", ctypes.c_void_p),
+        ("add", ctypes.c_void_p),
+        ("ld_add", ctypes.c_int64),
+        ("z", ctypes.c_void_p),
+        ("ld_z", ctypes.c_int64),
+    ]
+
+
+class muon_layernorm(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64),
+        ("ld_dx", ctypes.c_int64),
+        ("ld_add", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
 _P = ctypes.c_void_p
 _SIGS = {
     "muon_hparams_default": (None, [ctypes.POINTER(muon_hparams)]),
@@ -131,6 +185,20 @@ _SIGS = {
     "muon_profile_enable": (ctypes.c_int, [_P, ctypes.c_int32]),
     "muon_profile_read": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64),
                                          ctypes.POINTER(ctypes.c_double)]),
+    "muon_linear_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(muon_linear), ctypes.c_int32, _P, _P,
+                                                   ctypes.POINTER(ctypes.c_size_t)]),
+    "muon_linear_forward": (ctypes.c_int, [ctypes.POINTER(muon_linear), _P, _P, ctypes.POINTER(muon_epilogue), _P, _P,
+                                           ctypes.c_size_t, _P]),
+    "muon_linear_grad_input": (ctypes.c_int, [ctypes.POINTER(muon_linear), _P, _P, ctypes.POINTER(muon_epilogue), _P,
+                                              _P, ctypes.c_size_t, _P]),
+    "muon_linear_grad_weight": (ctypes.c_int, [ctypes.POINTER(muon_linear), _P, _P, _P, _P, ctypes.c_int32, _P,
+                                               ctypes.c_size_t, _P]),
+    "muon_layernorm_forward": (ctypes.c_int, [ctypes.POINTER(muon_layernorm), _P, _P, _P, _P, _P, _P, _P]),
+    "muon_layernorm_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(muon_layernorm),
+                                                      ctypes.POINTER(ctypes.c_size_t)]),
+    "muon_layernorm_backward": (ctypes.c_int, [ctypes.POINTER(muon_layernorm), _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                               ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "muon_op_last_error": (ctypes.c_char_p, []),
     "muon_lr_wsd": (ctypes.c_float, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
     "muon_lr_cooldown_floor": (ctypes.c_float, [ctypes.c_int64, ctypes.c_int64, ctypes.c_float, ctypes.c_float]),
     "muon_momentum_warmup": (ctypes.c_float, [ctypes.c_int64, ctypes.c_int64, ctypes.c_float, ctypes.c_float]),
@@ -271,6 +339,52 @@ def muon_profile_read(h, kernel: int, clear: int = 0) -> tuple:
     ms = ctypes.c_double(0.0)
     s = load().muon_profile_read(h, kernel, clear, ctypes.byref(n), ctypes.byref(ms))
     return s, n.value, ms.value
+
+
+# --- layer operators (tensors in layers.py; here the C calls as they are) -----
+
+def muon_linear_workspace_bytes(d: muon_linear, op: int, a_ptr: int, b_ptr: int) -> tuple:
+    out = ctypes.c_size_t(0)
+    s = load().muon_linear_workspace_bytes(d, op, a_ptr, b_ptr, out)
+    return s, out.value
+
+
+def muon_linear_forward(d: muon_linear, x_ptr: int, w_ptr: int, e: Optional[muon_epilogue], y_ptr: int,
+                        workspace_ptr: int, ws_bytes: int, stream_ptr: int) -> int:
+    return load().muon_linear_forward(d, x_ptr, w_ptr, e, y_ptr, workspace_ptr, ws_bytes, stream_ptr)
+
+
+def muon_linear_grad_input(d: muon_linear, dy_ptr: int, w_ptr: int, e: Optional[muon_epilogue], dx_ptr: int,
+                           workspace_ptr: int, ws_bytes: int, stream_ptr: int) -> int:
+    return load().muon_linear_grad_input(d, dy_ptr, w_ptr, e, dx_ptr, workspace_ptr, ws_bytes, stream_ptr)
+
+
+def muon_linear_grad_weight(d: muon_linear, x_ptr: int, dy_ptr: int, dw_ptr: int, dbias_ptr: int, accumulate: int,
+                            workspace_ptr: int, ws_bytes: int, stream_ptr: int) -> int:
+    return load().muon_linear_grad_weight(d, x_ptr, dy_ptr, dw_ptr, dbias_ptr, accumulate, workspace_ptr, ws_bytes,
+                                          stream_ptr)
+
+
+def muon_layernorm_forward(d: muon_layernorm, x_ptr: int, weight_ptr: int, bias_ptr: int, y_ptr: int, mean_ptr: int,
+                           rstd_ptr: int, stream_ptr: int) -> int:
+    return load().muon_layernorm_forward(d, x_ptr, weight_ptr, bias_ptr, y_ptr, mean_ptr, rstd_ptr, stream_ptr)
+
+
+def muon_layernorm_workspace_bytes(d: muon_layernorm) -> tuple:
+    out = ctypes.c_size_t(0)
+    s = load().muon_layernorm_workspace_bytes(d, out)
+    return s, out.value
+
+
+def muon_layernorm_backward(d: muon_layernorm, dy_ptr: int, x_ptr: int, weight_ptr: int, mean_ptr: int, rstd_ptr: int,
+                            add_ptr: int, dx_ptr: int, dweight_ptr: int, dbias_ptr: int, accumulate: int,
+                            workspace_ptr: int, ws_bytes: int, stream_ptr: int) -> int:
+    return load().muon_layernorm_backward(d, dy_ptr, x_ptr, weight_ptr, mean_ptr, rstd_ptr, add_ptr, dx_ptr,
+                                          dweight_ptr, dbias_ptr, accumulate, workspace_ptr, ws_bytes, stream_ptr)
+
+
+def muon_op_last_error() -> str:
+    return load().muon_op_last_error().decode()
 
 
 class MuonError(RuntimeError):

@@ -1,0 +1,447 @@
+// The linear layer's products on gfx950: C[M, N] = sum_k A(m, k) B(k, n) over
+// bf16 or fp16 operands with fp32 accumulation, and an epilogue on the fp32
+// sums that is rounded once (see Epilogue).
+//
+//  * One kernel for the three products of a layer (forward, input gradient,
+//    weight gradient, in either weight layout): each operand may have its k
+//    index contiguous (AKC, BKC) or its other index; the latter are read from
+//    LDS with the transposing read.
+//  * A workgroup of 4 waves (one per SIMD at T = 256) computes a T x T tile,
+//    each wave a quarter, T/2 x T/2, as blocks of 32x32x16 matrix
+//    instructions. At T = 256 a wave's 128 x 128 block takes 16 products from
+//    8 fragment reads, so the tile's LDS traffic (reads and the incoming
+//    slices) is 96 bytes a clock at the matrix peak, of the 128 that LDS
+//    gives; eight waves of 128 x 64 would need all of it.
+//  * K goes by in slices of 32 through a ring of four LDS buffers filled by
+//    direct-to-LDS loads, three slices ahead of their use, with one barrier a
+//    slice. Loads past K, past a split's end or past the matrix go out with an
+//    offset beyond the buffer resource's range and land as zeros, so the loop
+//    has no tail and reads nothing outside the operands.
+//  * splits > 1: each split writes its fp32 tile to the workspace and a second
+//    kernel adds them in order and does the epilogue (the same bits every run).
+
+#include "layer_device.hpp"
+
+namespace muon {
+
+namespace {
+
+constexpr int BK = kGemmSlice;
+constexpr int NBUF = 4;
+constexpr int DIST = NBUF - 1;     // slices a load goes out ahead of its use
+constexpr int KROWB = 2 * BK;      // bytes of a row of a k-contiguous tile
+constexpr uint32_t OUT = 0x80000000u;  // an offset beyond every resource's range
+
+template <typename T>
+__device__ __forceinline__ f32x16 mfma(typename V8<T>::type a, typename V8<T>::type b, f32x16 c);
+template <>
+__device__ __forceinline__ f32x16 mfma<bf16>(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x16 mfma<f16>(f16x8 a, f16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// s_waitcnt vmcnt(n), the other counters left alone
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
+
+// How one operand's tile is loaded and read. KC: T rows of KROWB bytes, chunk
+// c (16 bytes) of row r stored at c ^ ((r >> 2) & 3), so that the 16 rows of a
+// phase of ds_read_b128 fall in 16 distinct 16-byte slots. Otherwise BK rows
+// of 2T bytes, chunk c of row r at c ^ (4 (r & 3)), so that the 4 rows x 64
+// bytes of a half-wave's transposing read fall in 4 distinct 64-byte windows.
+template <typename T, int TILE, bool KC>
+struct Operand {
+    static constexpr int XCH = TILE / 8;  // 16-byte chunks of a row (not KC)
+    static constexpr int NLD = TILE * BK * 2 / 4096;  // load instructions a wave issues per slice
+    static constexpr int BLK = TILE / 64;             // 32-wide fragment blocks of a wave
+    const char* base;  // KC: first row of the tile; else row 0, first column of the tile
+    int64_t step;      // bytes per slice (not KC)
+    uint32_t range;    // KC: bytes of the tile's valid rows; else bytes of one row's remainder
+    uint32_t rowb;     // row stride in bytes
+    int kend;          // k at which this split ends
+    int kch;           // KC: the lane's first k within a slice
+    uint32_t off[NLD];
+    int lds_row;       // wave's first LDS byte of a load instruction
+    int rd[BLK == 4 ? 4 : 2];  // fragment read offsets: KC uses [0], [1] per k16 half
+
+    __device__ __forceinline__ void init(const void* p, int ld, int i0, int n, int kp, int kend_, int wave, int lane,
+                                         int wblk) {
+        rowb = (uint32_t)ld * 2u;
+        kend = kend_;
+        if constexpr (KC) {
+            // 16 rows of 4 chunks per instruction
+            const int rows = n - i0 < TILE ? n - i0 : TILE;
+            base = static_cast<const char*>(p) + (int64_t)i0 * rowb;
+            range = (uint32_t)(rows - 1) * rowb + (uint32_t)kp * 2u;
+            const int r = wave * 16 + (lane >> 2);
+            const int c = (lane & 3) ^ ((r >> 2) & 3);
+            kch = c * 8;
+#pragma unroll
+            for (int q = 0; q < NLD; ++q) {
+                const int row = r + q * 64;
+                off[q] = row < rows ? (uint32_t)row * rowb + (uint32_t)c * 16u : OUT;
+            }
+            lds_row = wave * 16 * KROWB;
+            const int l32 = lane & 31, hi = lane >> 5;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+                rd[ks] = (wblk * (TILE / 2) + l32) * KROWB + 16 * ((2 * ks + hi) ^ ((l32 >> 2) & 3));
+        } else {
+            base = static_cast<const char*>(p) + (int64_t)i0 * 2;
+            step = (int64_t)BK * rowb;
+            const int cols = n - i0 < TILE ? n - i0 : TILE;
+            range = (uint32_t)cols * 2u;
+            constexpr int RPI = 64 / XCH;  // rows per instruction
+            const int r = wave * RPI + lane / XCH;
+            const int c = (lane % XCH) ^ (4 * (r & 3));
+#pragma unroll
+            for (int q = 0; q < NLD; ++q)
+                off[q] = c * 8 < cols ? (uint32_t)(r + q * 4 * RPI) * rowb + (uint32_t)c * 16u : OUT;
+            lds_row = wave * 1024;
+            const int g = lane >> 4, s = lane & 15;
+            const int row = 8 * (g >> 1) + (s >> 2);
+#pragma unroll
+            for (int f = 0; f < BLK; ++f) {
+                const int e = wblk * (TILE / 2) + 32 * f + 16 * (g & 1) + 4 * (s & 3);
+                rd[f] = row * (2 * TILE) + 16 * ((e >> 3) ^ (4 * (row & 3))) + 2 * (e & 7);
+            }
+        }
+    }
+
+    // what a slice's loads need besides off[]: the resource, the scalar offset
+    // and (KC) whether the lane's chunk lies before the end of k
+    struct Slice {
+        u32x4 r;
+        int soff;
+        uint32_t dead;
+    };
+    __device__ __forceinline__ Slice slice(int k0) const {
+        Slice s;
+        const int left = kend - k0;
+        if constexpr (KC) {
+            s.r = rsrc(base, range);
+            s.soff = left > 0 ? k0 * 2 : 0;
+            s.dead = kch < left ? 0u : OUT;
+        } else {
+            const int rows = left < 0 ? 0 : left < BK ? left : BK;
+            s.r = rsrc(rows > 0 ? base + (int64_t)k0 * rowb : base, rows > 0 ? (uint32_t)(rows - 1) * rowb + range : 0u);
+            s.soff = 0;
+            s.dead = 0u;
+        }
+        return s;
+    }
+    __device__ __forceinline__ void load(const Slice& s, char* S, int q) const {
+        dma16(s.r, S + lds_row + q * 4096, (int)(KC ? (off[q] | s.dead) : off[q]), s.soff);
+    }
+    // fragment block f of k16 half ks
+    __device__ __forceinline__ typename V8<T>::type read(const char* S, int ks, int f) const {
+        if constexpr (KC) {
+            return *reinterpret_cast<const typename V8<T>::type*>(S + rd[ks] + f * 32 * KROWB);
+        } else {
+            const bf16x4 lo = tr_read(S + rd[f] + (16 * ks) * (2 * TILE));
+            const bf16x4 up = tr_read(S + rd[f] + (16 * ks + 4) * (2 * TILE));
+            return __builtin_bit_cast(typename V8<T>::type, __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7));
+        }
+    }
+};
+
+// blockIdx -> (tile row, tile column, split). Workgroups go round-robin over
+// the 8 XCDs, so each XCD takes one contiguous run of the order in which
+// tiles of 8 tile rows at a time walk down the columns: the tiles an XCD
+// works on at once share their operand panels in its L2.
+__device__ __forceinline__ void tile_of(int b, int total, int tm, int tn, int& ti, int& tj, int& sp) {
+    const int x = b & 7, i = b >> 3, q = total >> 3, r = total & 7;
+    int l = x * q + (x < r ? x : r) + i;
+    const int tiles = tm * tn;
+    sp = l / tiles;
+    l -= sp * tiles;
+    const int per = 8 * tn;
+    const int grp = l / per;
+    const int rows = tm - grp * 8 < 8 ? tm - grp * 8 : 8;
+    l -= grp * per;
+    ti = grp * 8 + l % rows;
+    tj = l / rows;
+}
+
+template <typename T, int TILE, bool AKC, bool BKC>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, TILE == 256 ? 1 : 2))) void k_gemm(
+    const GemmArgs g) {
+    constexpr int STAGE = 2 * TILE * KROWB;
+    constexpr int BOFF = TILE * KROWB;  // the B tile within a stage
+    constexpr int BLK = TILE / 64;
+    constexpr int WT = TILE / 2;
+    constexpr int SROW = WT * 4 + 16;  // bytes of a staged epilogue row
+    static_assert(4 * 32 * SROW <= NBUF * STAGE, "epilogue staging");
+    __shared__ __attribute__((aligned(16))) char smem[NBUF * STAGE];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wi = wave >> 1, wj = wave & 1;
+    int ti, tj, sp;
+    tile_of(blockIdx.x, gridDim.x, g.tiles_m, g.tiles_n, ti, tj, sp);
+    const int i0 = ti * TILE, j0 = tj * TILE;
+    const int kmax = AKC || BKC ? g.kp : g.K;
+    const int kb = sp * g.slices * BK;
+    int ke = kb + g.slices * BK;
+    ke = ke < kmax ? ke : kmax;
+    const int nk = ke > kb ? (ke - kb + BK - 1) / BK : 0;
+
+    Operand<T, TILE, AKC> A;
+    Operand<T, TILE, BKC> B;
+    A.init(g.a, g.ld_a, i0, AKC ? g.M : g.mp, g.kp, AKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wi);
+    B.init(g.b, g.ld_b, j0, BKC ? g.N : g.np, g.kp, BKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wj);
+    constexpr int NLD = Operand<T, TILE, AKC>::NLD;
+
+    auto buf = [&](int k) { return smem + (k & (NBUF - 1)) * STAGE; };
+    auto dma_stage = [&](int kt) {
+        const auto sa = A.slice(kb + kt * BK);
+        const auto sb = B.slice(kb + kt * BK);
+        char* S = buf(kt);
+#pragma unroll
+        for (int q = 0; q < NLD; ++q) A.load(sa, S, q);
+#pragma unroll
+        for (int q = 0; q < NLD; ++q) B.load(sb, S + BOFF, q);
+    };
+
+    f32x16 acc[BLK][BLK];
+#pragma unroll
+    for (int a = 0; a < BLK; ++a)
+#pragma unroll
+        for (int b = 0; b < BLK; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
+
+    typename V8<T>::type pf[2][BLK], qf[2][BLK];
+    auto read_frags = [&](const char* S, int ks) {
+#pragma unroll
+        for (int f = 0; f < BLK; ++f) pf[ks][f] = A.read(S, ks, f);
+#pragma unroll
+        for (int f = 0; f < BLK; ++f) qf[ks][f] = B.read(S + BOFF, ks, f);
+    };
+    auto products = [&](int ks, int f0, int f1) {
+#pragma unroll
+        for (int fi = f0; fi < f1; ++fi)
+#pragma unroll
+            for (int fj = 0; fj < BLK; ++fj) acc[fi][fj] = mfma<T>(qf[ks][fj], pf[ks][fi], acc[fi][fj]);
+    };
+
+    if (nk > 0) {
+#pragma unroll
+        for (int k = 0; k < DIST; ++k) dma_stage(k);
+        wait_vm<(DIST - 1) * 2 * NLD>();
+        __syncthreads();
+        read_frags(buf(0), 0);
+        for (int kt = 0; kt < nk; ++kt) {
+            const char* S = buf(kt);
+            // slice kt + 3 into the buffer of slice kt - 1, which every wave
+            // had read before the last barrier
+            dma_stage(kt + DIST);
+            read_frags(S, 1);
+            products(0, 0, BLK);
+            products(1, 0, BLK / 2);
+            wait_vm<(DIST - 1) * 2 * NLD>();  // slice kt + 1 has landed
+            __syncthreads();
+            read_frags(buf(kt + 1), 0);
+            products(1, BLK / 2, BLK);
+        }
+        wait_vm0();  // the loads past the end
+    }
+    __syncthreads();
+
+    // ---- epilogue: lane holds C[i][j .. j+3], i = l32, j = 8 g + 4 hi; each
+    // wave stages 32 rows at a time in its own LDS region and leaves with 8
+    // consecutive columns a lane ----
+    char* W = smem + wave * 32 * SROW;
+    const int l32 = lane & 31, hi = lane >> 5;
+    constexpr int CPR = WT / 8;      // chunks of 8 per staged row
+    constexpr int RPI = 64 / CPR;    // rows per pass of the wave
+    const int ch = lane % CPR, rr = lane / CPR;
+    const int col = j0 + wj * WT + ch * 8;
+    const int ncol = g.N - col;
+    float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (g.epi.bias && ncol > 0) load8(g.epi.bias + col, ncol, false, bias);
+#pragma unroll
+    for (int fi = 0; fi < BLK; ++fi) {
+#pragma unroll
+        for (int fj = 0; fj < BLK; ++fj)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                f32x4 v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = acc[fi][fj][4 * q + e];
+                *reinterpret_cast<f32x4*>(W + l32 * SROW + 4 * (32 * fj + 8 * q + 4 * hi)) = v;
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 2
+        for (int it = 0; it < 32 / RPI; ++it) {
+            const int row = i0 + wi * WT + 32 * fi + it * RPI + rr;
+            const f32x4* s = reinterpret_cast<const f32x4*>(W + (it * RPI + rr) * SROW + 32 * ch);
+            const f32x4 lo = s[0], up = s[1];
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], up[0], up[1], up[2], up[3]};
+            if (row < g.M && ncol > 0) {
+                if (g.splits > 1) {
+                    // ld_p is N rounded up to 8: whole chunks
+                    float* p = g.partial + ((int64_t)sp * g.M + row) * g.ld_p + col;
+                    *reinterpret_cast<f32x4*>(p) = lo;
+                    *reinterpret_cast<f32x4*>(p + 4) = up;
+                } else {
+                    epilogue8<T>(g.epi, row, col, ncol, v, bias);
+                }
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// The splits' partial tiles added in order, then the epilogue.
+template <typename T>
+__global__ __launch_bounds__(256) void k_gemm_reduce(const GemmArgs g) {
+    const int cpr = g.ld_p / 8;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t row = id / cpr;
+    if (row >= g.M) return;
+    const int col = (int)(id - row * cpr) * 8;
+    const float* p = g.partial + row * g.ld_p + col;
+    const int64_t stride = (int64_t)g.M * g.ld_p;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < g.splits; ++s) {
+        float t[8];
+        load8(p + s * stride, 8, true, t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += t[e];
+    }
+    float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (g.epi.bias) load8(g.epi.bias + col, g.N - col, false, bias);
+    epilogue8<T>(g.epi, row, col, g.N - col, v, bias);
+}
+
+// Rows of any alignment and length to 16-byte aligned, zero-padded ones: one
+// 16-byte chunk per thread.
+__global__ __launch_bounds__(256) void k_pack(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
+                                              uint4* __restrict__ dst, int64_t chunks) {
+    const int64_t n = rows * chunks;
+    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < n; id += (int64_t)gridDim.x * 256) {
+        const int64_t r = id / chunks, c = (id - r * chunks) * 8;
+        const uint16_t* p = src + r * ld + c;
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = c + e < cols ? p[e] : 0u;
+        dst[id] = uint4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+    }
+}
+
+// Column sums of a 16-bit matrix whose rows are 16-byte aligned and a
+// multiple of 8 long: a block takes 256 columns (32 lanes x 8) of a run of
+// rows, 8 rows at a time, and writes one partial row.
+template <typename T>
+__global__ __launch_bounds__(256) void k_colsum(const T* __restrict__ dy, int64_t ld, int64_t rows, int cols,
+                                                int64_t per, float* __restrict__ part) {
+    __shared__ float red[8][32][9];
+    const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int c = blockIdx.x * 256 + lane * 8;
+    const int64_t r0 = blockIdx.y * per;
+    const int64_t r1 = r0 + per < rows ? r0 + per : rows;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (c < cols) {
+#pragma unroll 4
+        for (int64_t r = r0 + rl; r < r1; r += 8) {
+            float t[8];
+            load8(dy + r * ld + c, 8, true, t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += t[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) red[rl][lane][e] = v[e];
+    __syncthreads();
+    const int l = threadIdx.x >> 3, e = threadIdx.x & 7;
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += red[k][l][e];
+    const int cc = blockIdx.x * 256 + l * 8 + e;
+    if (cc < cols) part[(int64_t)blockIdx.y * cols + cc] = s;
+}
+
+__global__ __launch_bounds__(256) void k_colsum_join(const float* __restrict__ part, int blocks, int cols, int n,
+                                                     float* __restrict__ db, int accumulate) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= n) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int b = 0; b < blocks; ++b) s += part[(int64_t)b * cols + c];
+    db[c] = accumulate ? db[c] + s : s;
+}
+
+template <typename T, int TILE>
+hipError_t gemm_t(const GemmArgs& g, bool a_kc, bool b_kc, hipStream_t st) {
+    const int grid = g.tiles_m * g.tiles_n * g.splits;
+    if (a_kc && b_kc)
+        k_gemm<T, TILE, true, true><<<grid, 256, 0, st>>>(g);
+    else if (a_kc)
+        k_gemm<T, TILE, true, false><<<grid, 256, 0, st>>>(g);
+    else
+        k_gemm<T, TILE, false, false><<<grid, 256, 0, st>>>(g);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gemm(const GemmArgs& g, int tile, bool a_kc, bool b_kc, int dtype, hipStream_t st) {
+    if (dtype == 0) return tile == 256 ? gemm_t<bf16, 256>(g, a_kc, b_kc, st) : gemm_t<bf16, 128>(g, a_kc, b_kc, st);
+    return tile == 256 ? gemm_t<f16, 256>(g, a_kc, b_kc, st) : gemm_t<f16, 128>(g, a_kc, b_kc, st);
+}
+
+hipError_t launch_gemm_reduce(const GemmArgs& g, int dtype, hipStream_t st) {
+    const int64_t n = (int64_t)g.M * (g.ld_p / 8);
+    const unsigned grid = (unsigned)((n + 255) / 256);
+    if (dtype == 0)
+        k_gemm_reduce<bf16><<<grid, 256, 0, st>>>(g);
+    else
+        k_gemm_reduce<f16><<<grid, 256, 0, st>>>(g);
+    return hipGetLastError();
+}
+
+hipError_t launch_pack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t cols_pad,
+                       hipStream_t st) {
+    if (rows == 0) return hipSuccess;
+    const int64_t n = rows * (cols_pad / 8);
+    const int64_t blocks = (n + 255) / 256;
+    k_pack<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(static_cast<const uint16_t*>(src), ld, rows,
+                                                                        cols, static_cast<uint4*>(dst), cols_pad / 8);
+    return hipGetLastError();
+}
+
+int colsum_blocks(int64_t rows, int64_t cols) {
+    // about 1024 blocks in all, each at least 64 rows
+    const int64_t cb = (cols + 255) / 256;
+    int64_t b = (1024 + cb - 1) / cb;
+    const int64_t most = (rows + 63) / 64;
+    if (b > most) b = most;
+    return (int)(b < 1 ? 1 : b);
+}
+
+hipError_t launch_colsum(const void* dy, int64_t ld, int64_t rows, int64_t cols, int dtype, float* part, float* db,
+                         int accumulate, hipStream_t st) {
+    const int64_t cp = (cols + 7) / 8 * 8;
+    const int blocks = colsum_blocks(rows, cols);
+    const int64_t per = (rows + blocks - 1) / blocks;
+    const dim3 grid((unsigned)((cp + 255) / 256), (unsigned)blocks);
+    if (dtype == 0)
+        k_colsum<bf16><<<grid, 256, 0, st>>>(static_cast<const bf16*>(dy), ld, rows, (int)cp, per, part);
+    else
+        k_colsum<f16><<<grid, 256, 0, st>>>(static_cast<const f16*>(dy), ld, rows, (int)cp, per, part);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    k_colsum_join<<<(unsigned)((cols + 255) / 256), 256, 0, st>>>(part, blocks, (int)cp, (int)cols, db, accumulate);
+    return hipGetLastError();
+}
+
+}  // namespace muon

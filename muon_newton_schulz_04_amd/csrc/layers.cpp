@@ -1,0 +1,496 @@
+// C ABI of the layer operators (include/libmuon.h): argument checks, operand
+// packing and workspace layout, the choice of tile and K split, and the
+// launches on the caller's stream.
+
+#include <hip/hip_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstring>
+#include <exception>
+#include <new>
+#include <string>
+
+#include "../../include/libmuon.h"
+#include "layers.hpp"
+
+namespace {
+
+thread_local std::string g_error;
+
+muon_status fail(muon_status s, const char* msg) noexcept {
+    try {
+        g_error = msg;
+    } catch (...) {
+    }
+    return s;
+}
+
+// No exception crosses the ABI.
+template <typename F>
+muon_status guarded(F&& body) noexcept {
+    try {
+        return body();
+    } catch (const std::bad_alloc&) {
+        return fail(MUON_E_HOST, "out of host memory");
+    } catch (const std::exception& ex) {
+        return fail(MUON_E_HOST, ex.what());
+    } catch (...) {
+        return fail(MUON_E_HOST, "unknown exception");
+    }
+}
+
+muon_status hip_status(hipError_t e, const char* where) {
+    if (e == hipSuccess) return MUON_OK;
+    return fail(MUON_E_HIP, (std::string(where) + ": " + hipGetErrorString(e)).c_str());
+}
+
+// The current device must be a gfx950; asked once per device.
+muon_status check_device() {
+    constexpr int kMax = 64;
+    static std::atomic<int> known[kMax];
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0) {
+        (void)hipGetLastError();
+        return fail(MUON_E_NO_DEVICE, "no HIP device");
+    }
+    if (dev < kMax && known[dev].load(std::memory_order_relaxed) == 1) return MUON_OK;
+    hipDeviceProp_t prop;
+    hipError_t e = hipGetDeviceProperties(&prop, dev);
+    if (e != hipSuccess) return hip_status(e, "hipGetDeviceProperties");
+    if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
+        return fail(MUON_E_NO_DEVICE, (std::string("device is ") + prop.gcnArchName + ", need gfx950").c_str());
+    if (dev < kMax) known[dev].store(1, std::memory_order_relaxed);
+    return MUON_OK;
+}
+
+constexpr int64_t kMaxRows = (int64_t)1 << 24;
+constexpr int64_t kMaxCols = (int64_t)1 << 21;
+
+// A [rows, cols] tensor with a row stride, and the bytes from its first to
+// its last element.
+struct Tensor {
+    const void* p;
+    int64_t rows, cols, ld;
+    int size;
+    int64_t bytes() const { return rows == 0 ? 0 : ((rows - 1) * ld + cols) * size; }
+};
+
+bool overlap(const Tensor& a, const Tensor& b) {
+    const int64_t na = a.bytes(), nb = b.bytes();
+    if (!a.p || !b.p || na == 0 || nb == 0) return false;
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+bool same_tensor(const Tensor& a, const Tensor& b) { return a.p == b.p && (a.ld == b.ld || a.rows <= 1); }
+
+// `out` against every input, other output and the workspace; `may` is the one
+// input it may coincide with.
+muon_status check_disjoint(const Tensor& out, std::initializer_list<Tensor> others, const Tensor* may) {
+    for (const Tensor& o : others) {
+        if (!overlap(out, o)) continue;
+        if (may && o.p == may->p && same_tensor(out, o)) continue;
+        return fail(MUON_E_INVALID_ARG, "an output overlaps another tensor or the workspace");
+    }
+    return MUON_OK;
+}
+
+muon_status check_align(const void* p, int size, const char* what) {
+    if ((uintptr_t)p % (uintptr_t)size == 0) return MUON_OK;
+    return fail(MUON_E_LAYOUT, (std::string(what) + " is not aligned to its element size").c_str());
+}
+
+muon_status check_ld(int64_t ld, int64_t cols, const char* what) {
+    if (ld == 0 || (ld >= cols && ld <= kMaxCols)) return MUON_OK;
+    return fail(MUON_E_LAYOUT, (std::string(what) + " must be 0 or from the row length to 2^21").c_str());
+}
+
+muon_status check_workspace(const void* ws, size_t have, size_t need) {
+    if (need == 0) return MUON_OK;
+    if (!ws) return fail(MUON_E_WORKSPACE, "null workspace");
+    if ((uintptr_t)ws % 256 != 0) return fail(MUON_E_WORKSPACE, "workspace not 256-byte aligned");
+    if (have < need)
+        return fail(MUON_E_WORKSPACE, ("workspace too small: need " + std::to_string(need) + " bytes").c_str());
+    return MUON_OK;
+}
+
+#define TRY(expr)                          \
+    do {                                   \
+        const muon_status s_ = (expr);     \
+        if (s_ != MUON_OK) return s_;      \
+    } while (0)
+
+bool aligned16(const void* p, int64_t ld, int size) { return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0; }
+int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+muon_status check_linear(const muon_linear* d) {
+    if (!d) return fail(MUON_E_INVALID_ARG, "null descriptor");
+    if (d->dtype != MUON_TYPE_BF16 && d->dtype != MUON_TYPE_FP16)
+        return fail(MUON_E_INVALID_ARG, "linear: dtype must be bf16 or fp16");
+    if (d->weight_layout != MUON_WEIGHT_IN_OUT && d->weight_layout != MUON_WEIGHT_OUT_IN)
+        return fail(MUON_E_INVALID_ARG, "linear: bad weight_layout");
+    if (d->tokens < 0 || d->tokens >= kMaxRows) return fail(MUON_E_SHAPE, "linear: tokens must be in [0, 2^24)");
+    if (d->in_features < 1 || d->in_features > kMaxCols || d->out_features < 1 || d->out_features > kMaxCols)
+        return fail(MUON_E_SHAPE, "linear: features must be in [1, 2^21]");
+    TRY(check_ld(d->ld_x, d->in_features, "ld_x"));
+    TRY(check_ld(d->ld_w, d->weight_layout == MUON_WEIGHT_IN_OUT ? d->out_features : d->in_features, "ld_w"));
+    TRY(check_ld(d->ld_y, d->out_features, "ld_y"));
+    return MUON_OK;
+}
+
+Tensor tensor_x(const muon_linear& d, const void* p) {
+    return {p, d.tokens, d.in_features, d.ld_x ? d.ld_x : d.in_features, 2};
+}
+Tensor tensor_y(const muon_linear& d, const void* p) {
+    return {p, d.tokens, d.out_features, d.ld_y ? d.ld_y : d.out_features, 2};
+}
+Tensor tensor_w(const muon_linear& d, const void* p, int size) {
+    const bool io = d.weight_layout == MUON_WEIGHT_IN_OUT;
+    const int64_t r = io ? d.in_features : d.out_features, c = io ? d.out_features : d.in_features;
+    return {p, r, c, d.ld_w ? d.ld_w : c, size};
+}
+
+// The tile and the number of K splits for an M x N x K product.
+muon::GemmPlan choose_plan(int64_t M, int64_t N, int64_t K) {
+    const int64_t slices = (K + muon::kGemmSlice - 1) / muon::kGemmSlice;
+    muon::GemmPlan best{128, 1, (int)(slices > 0 ? slices : 1)};
+    double best_t = 1e300;
+    for (int tile : {256, 128}) {
+        const int64_t tiles = ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
+        // one 256 tile fills a CU; two 128 tiles share one. Clocks: a slice's
+        // matrix work, and what a workgroup spends outside its main loop
+        const double slots = tile == 256 ? 256 : 512, per_slice = tile == 256 ? 1400 : 900,
+                     fixed = tile == 256 ? 14000 : 7000;
+        for (int s = 1; s <= 64; ++s) {
+            if (s > 1 && (s > slices || tiles * s > 2 * slots)) break;
+            const int64_t per = (slices + s - 1) / s;
+            if (s > 1 && (slices + per - 1) / per != s) continue;  // every split has work
+            double t = std::ceil((double)tiles * s / slots) * ((double)per * per_slice + fixed);
+            // partial tiles out and in (float32, about 1700 bytes a clock) and one more launch
+            if (s > 1) t += 8.0 * (double)M * (double)N * s / 1700.0 + 6000.0;
+            if (t < best_t) {
+                best_t = t;
+                best = {tile, s, (int)(per > 0 ? per : 1)};
+            }
+        }
+    }
+    return best;
+}
+
+// One product: operands, where packed copies and partial sums go, and the plan.
+struct Product {
+    int64_t M, N, K;
+    Tensor a, b;
+    bool a_kc, b_kc;  // k is the contiguous index
+    bool pack_a, pack_b;
+    muon::GemmPlan plan;
+    size_t off_a, off_b, off_part, off_cols, bytes;
+};
+
+bool needs_pack(const Tensor& t) { return t.rows > 0 && (!aligned16(t.p, t.ld, 2) || t.cols % 8 != 0); }
+
+muon_status plan_product(const muon_linear& d, int op, const void* pa, const void* pb, bool dbias, Product* P) {
+    const bool io = d.weight_layout == MUON_WEIGHT_IN_OUT;
+    if (op == MUON_LINEAR_FORWARD) {
+        *P = {d.tokens, d.out_features, d.in_features, tensor_x(d, pa), tensor_w(d, pb, 2), true, !io};
+    } else if (op == MUON_LINEAR_GRAD_INPUT) {
+        *P = {d.tokens, d.in_features, d.out_features, tensor_y(d, pa), tensor_w(d, pb, 2), true, io};
+    } else {
+        const Tensor x = tensor_x(d, pa), dy = tensor_y(d, pb);
+        if (io)
+            *P = {d.in_features, d.out_features, d.tokens, x, dy, false, false};
+        else
+            *P = {d.out_features, d.in_features, d.tokens, dy, x, false, false};
+    }
+    P->pack_a = needs_pack(P->a);
+    P->pack_b = needs_pack(P->b);
+    P->plan = choose_plan(P->M, P->N, P->K);
+    const int64_t T = P->plan.tile;
+    if (((P->M + T - 1) / T) * ((P->N + T - 1) / T) >= (int64_t)1 << 23)
+        return fail(MUON_E_SHAPE, "linear: output too large");
+    size_t o = 0;
+    P->off_a = o;
+    if (P->pack_a) o = up256(o + (size_t)P->a.rows * up8(P->a.cols) * 2);
+    P->off_b = o;
+    if (P->pack_b) o = up256(o + (size_t)P->b.rows * up8(P->b.cols) * 2);
+    P->off_part = o;
+    if (P->plan.splits > 1) o = up256(o + (size_t)P->plan.splits * P->M * up8(P->N) * 4);
+    P->off_cols = o;
+    if (dbias) o = up256(o + (size_t)muon::colsum_blocks(d.tokens, d.out_features) * up8(d.out_features) * 4);
+    P->bytes = o;
+    return MUON_OK;
+}
+
+muon_status run_product(Product& P, int dtype, muon::Epilogue& E, char* ws, hipStream_t st) {
+    for (int k = 0; k < 2; ++k) {
+        Tensor& t = k ? P.b : P.a;
+        if (!(k ? P.pack_b : P.pack_a)) continue;
+        char* dst = ws + (k ? P.off_b : P.off_a);
+        TRY(hip_status(muon::launch_pack(t.p, t.ld, t.rows, t.cols, dst, up8(t.cols), st), "pack kernel"));
+        t.p = dst;
+        t.ld = up8(t.cols);
+    }
+    const int T = P.plan.tile;
+    muon::GemmArgs g{};
+    g.a = P.a.p;
+    g.b = P.b.p;
+    g.ld_a = (int)P.a.ld;
+    g.ld_b = (int)P.b.ld;
+    g.M = (int)P.M;
+    g.N = (int)P.N;
+    g.K = (int)P.K;
+    g.kp = (int)((P.a_kc || P.b_kc) ? up8(P.K) : P.K);
+    g.mp = (int)up8(P.M);
+    g.np = (int)up8(P.N);
+    g.tiles_m = (int)((P.M + T - 1) / T);
+    g.tiles_n = (int)((P.N + T - 1) / T);
+    g.splits = P.plan.splits;
+    g.slices = P.plan.slices;
+    g.partial = reinterpret_cast<float*>(ws + P.off_part);
+    g.ld_p = (int)up8(P.N);
+    g.epi = E;
+    TRY(hip_status(muon::launch_gemm(g, T, P.a_kc, P.b_kc, dtype, st), "product kernel"));
+    if (g.splits > 1) TRY(hip_status(muon::launch_gemm_reduce(g, dtype, st), "split join kernel"));
+    return MUON_OK;
+}
+
+// forward and grad input
+muon_status run_layer(const muon_linear* d, int op, const void* a, const void* w, const muon_epilogue* e, void* y,
+                      void* ws, size_t ws_bytes, void* stream) {
+    TRY(check_linear(d));
+    const bool fwd = op == MUON_LINEAR_FORWARD;
+    const int64_t out_cols = fwd ? d->out_features : d->in_features;
+    muon_epilogue none{};
+    if (!e) e = &none;
+    if (e->activation < MUON_ACT_NONE || e->activation > MUON_ACT_SILU)
+        return fail(MUON_E_INVALID_ARG, "epilogue: unknown activation");
+    if (e->reserved != 0) return fail(MUON_E_INVALID_ARG, "epilogue: reserved must be 0");
+    if (!fwd && e->bias) return fail(MUON_E_INVALID_ARG, "grad input: takes no bias");
+    TRY(check_ld(e->ld_add, out_cols, "ld_add"));
+    TRY(check_ld(e->ld_z, out_cols, "ld_z"));
+    if (d->tokens == 0) return MUON_OK;
+    if (!a || !w || !y) return fail(MUON_E_INVALID_ARG, "null tensor");
+    if (!fwd && e->activation != MUON_ACT_NONE && !e->z)
+        return fail(MUON_E_INVALID_ARG, "grad input: an activation needs its pre-activation z");
+    const bool use_z = e->z && (fwd || e->activation != MUON_ACT_NONE);
+    const Tensor A = fwd ? tensor_x(*d, a) : tensor_y(*d, a), W = tensor_w(*d, w, 2);
+    const Tensor Y = fwd ? tensor_y(*d, y) : tensor_x(*d, y);
+    const Tensor R{e->add, d->tokens, out_cols, e->ld_add ? e->ld_add : out_cols, 2};
+    const Tensor Z{use_z ? e->z : nullptr, d->tokens, out_cols, e->ld_z ? e->ld_z : out_cols, 2};
+    const Tensor Bi{e->bias, 1, d->out_features, d->out_features, 4};
+    for (const Tensor& t : {A, W, Y, R, Z}) TRY(check_align(t.p, 2, "a 16-bit tensor"));
+    TRY(check_align(e->bias, 4, "bias"));
+    Product P;
+    TRY(plan_product(*d, op, a, w, false, &P));
+    TRY(check_workspace(ws, ws_bytes, P.bytes));
+    const Tensor S{ws, 1, (int64_t)P.bytes, (int64_t)P.bytes, 1};
+    TRY(check_disjoint(Y, {A, W, R, Z, Bi, S}, &R));
+    if (fwd) TRY(check_disjoint(Z, {A, W, R, Bi, S}, nullptr));
+    for (const Tensor& t : {A, W, R, Z, Bi})
+        if (overlap(S, t)) return fail(MUON_E_INVALID_ARG, "the workspace overlaps a tensor");
+    TRY(check_device());
+    muon::Epilogue E{};
+    E.mode = fwd ? muon::EPI_FORWARD : muon::EPI_GRAD_INPUT;
+    E.act = e->activation;
+    E.bias = e->bias;
+    E.add = e->add;
+    E.z = use_z ? e->z : nullptr;
+    E.y = y;
+    E.ld_add = R.ld;
+    E.ld_z = Z.ld;
+    E.ld_y = Y.ld;
+    E.vec_add = aligned16(R.p, R.ld, 2);
+    E.vec_z = aligned16(Z.p, Z.ld, 2);
+    E.vec_y = aligned16(Y.p, Y.ld, 2);
+    return run_product(P, d->dtype, E, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
+}
+
+muon_status check_norm(const muon_layernorm* d) {
+    if (!d) return fail(MUON_E_INVALID_ARG, "null descriptor");
+    if (d->dtype < MUON_TYPE_BF16 || d->dtype > MUON_TYPE_FP32)
+        return fail(MUON_E_INVALID_ARG, "layernorm: dtype must be bf16, fp16 or fp32");
+    if (d->rows < 0 || d->rows >= kMaxRows) return fail(MUON_E_SHAPE, "layernorm: rows must be in [0, 2^24)");
+    if (d->cols < 1 || d->cols > kMaxCols) return fail(MUON_E_SHAPE, "layernorm: cols must be in [1, 2^21]");
+    if (!(d->eps >= 0.f) || !std::isfinite(d->eps))
+        return fail(MUON_E_INVALID_ARG, "layernorm: eps must be finite and not negative");
+    TRY(check_ld(d->ld_x, d->cols, "ld_x"));
+    TRY(check_ld(d->ld_y, d->cols, "ld_y"));
+    TRY(check_ld(d->ld_dx, d->cols, "ld_dx"));
+    TRY(check_ld(d->ld_add, d->cols, "ld_add"));
+    return MUON_OK;
+}
+
+muon::NormArgs norm_args(const muon_layernorm& d) {
+    muon::NormArgs n{};
+    n.rows = d.rows;
+    n.cols = (int)d.cols;
+    n.ld_x = d.ld_x ? d.ld_x : d.cols;
+    n.ld_y = d.ld_y ? d.ld_y : d.cols;
+    n.ld_dx = d.ld_dx ? d.ld_dx : d.cols;
+    n.ld_r = d.ld_add ? d.ld_add : d.cols;
+    n.eps = d.eps;
+    return n;
+}
+
+size_t norm_workspace(const muon_layernorm& d) {
+    return up256((size_t)muon::norm_backward_blocks(d.rows, d.cols) * 2 * (size_t)d.cols * 4);
+}
+
+}  // namespace
+
+extern "C" {
+
+const char* muon_op_last_error(void) { return g_error.c_str(); }
+
+muon_status muon_linear_workspace_bytes(const muon_linear* d, int32_t op, const void* a, const void* b,
+                                        size_t* out_bytes) {
+    return guarded([&]() -> muon_status {
+        if (!out_bytes) return fail(MUON_E_INVALID_ARG, "null out_bytes");
+        TRY(check_linear(d));
+        if (op < MUON_LINEAR_FORWARD || op > MUON_LINEAR_GRAD_WEIGHT)
+            return fail(MUON_E_INVALID_ARG, "unknown linear operation");
+        *out_bytes = 0;
+        if (d->tokens == 0 && op != MUON_LINEAR_GRAD_WEIGHT) return MUON_OK;
+        Product P;
+        TRY(plan_product(*d, op, a, b, op == MUON_LINEAR_GRAD_WEIGHT, &P));
+        *out_bytes = P.bytes;
+        return MUON_OK;
+    });
+}
+
+muon_status muon_linear_forward(const muon_linear* d, const void* x, const void* w, const muon_epilogue* e, void* y,
+                                void* workspace, size_t ws_bytes, void* stream) {
+    return guarded([&]() { return run_layer(d, MUON_LINEAR_FORWARD, x, w, e, y, workspace, ws_bytes, stream); });
+}
+
+muon_status muon_linear_grad_input(const muon_linear* d, const void* dy, const void* w, const muon_epilogue* e,
+                                   void* dx, void* workspace, size_t ws_bytes, void* stream) {
+    return guarded([&]() { return run_layer(d, MUON_LINEAR_GRAD_INPUT, dy, w, e, dx, workspace, ws_bytes, stream); });
+}
+
+muon_status muon_linear_grad_weight(const muon_linear* d, const void* x, const void* dy, float* dw, float* dbias,
+                                    int32_t accumulate, void* workspace, size_t ws_bytes, void* stream) {
+    return guarded([&]() -> muon_status {
+        TRY(check_linear(d));
+        if (!dw || (d->tokens > 0 && (!x || !dy))) return fail(MUON_E_INVALID_ARG, "null tensor");
+        const Tensor X = tensor_x(*d, x), Y = tensor_y(*d, dy), W = tensor_w(*d, dw, 4);
+        const Tensor Bi{dbias, 1, d->out_features, d->out_features, 4};
+        TRY(check_align(x, 2, "x"));
+        TRY(check_align(dy, 2, "dy"));
+        TRY(check_align(dw, 4, "dw"));
+        TRY(check_align(dbias, 4, "dbias"));
+        Product P;
+        TRY(plan_product(*d, MUON_LINEAR_GRAD_WEIGHT, x, dy, dbias != nullptr, &P));
+        TRY(check_workspace(workspace, ws_bytes, P.bytes));
+        const Tensor S{workspace, 1, (int64_t)P.bytes, (int64_t)P.bytes, 1};
+        TRY(check_disjoint(W, {X, Y, Bi, S}, nullptr));
+        TRY(check_disjoint(Bi, {X, Y, S}, nullptr));
+        if (overlap(S, X) || overlap(S, Y)) return fail(MUON_E_INVALID_ARG, "the workspace overlaps a tensor");
+        TRY(check_device());
+        char* ws = static_cast<char*>(workspace);
+        hipStream_t st = static_cast<hipStream_t>(stream);
+        muon::Epilogue E{};
+        E.mode = muon::EPI_GRAD_WEIGHT;
+        E.y = dw;
+        E.ld_y = W.ld;
+        E.vec_y = aligned16(dw, W.ld, 4);
+        E.accumulate = accumulate != 0;
+        TRY(run_product(P, d->dtype, E, ws, st));
+        if (dbias) {
+            // dy as the product read it (packed or in place)
+            const Tensor& t = d->weight_layout == MUON_WEIGHT_IN_OUT ? P.b : P.a;
+            TRY(hip_status(muon::launch_colsum(t.p, t.ld, d->tokens, d->out_features, d->dtype,
+                                               reinterpret_cast<float*>(ws + P.off_cols), dbias, accumulate != 0, st),
+                           "bias gradient kernels"));
+        }
+        return MUON_OK;
+    });
+}
+
+muon_status muon_layernorm_forward(const muon_layernorm* d, const void* x, const float* weight, const float* bias,
+                                   void* y, float* mean, float* rstd, void* stream) {
+    return guarded([&]() -> muon_status {
+        TRY(check_norm(d));
+        if (d->rows == 0) return MUON_OK;
+        if (!x || !y || !mean || !rstd) return fail(MUON_E_INVALID_ARG, "null tensor");
+        const int size = d->dtype == MUON_TYPE_FP32 ? 4 : 2;
+        muon::NormArgs n = norm_args(*d);
+        const Tensor X{x, d->rows, d->cols, n.ld_x, size}, Y{y, d->rows, d->cols, n.ld_y, size};
+        const Tensor W{weight, 1, d->cols, d->cols, 4}, Bi{bias, 1, d->cols, d->cols, 4};
+        const Tensor M{mean, 1, d->rows, d->rows, 4}, S{rstd, 1, d->rows, d->rows, 4};
+        for (const Tensor& t : {X, Y}) TRY(check_align(t.p, size, "x or y"));
+        for (const Tensor& t : {W, Bi, M, S}) TRY(check_align(t.p, 4, "a float32 tensor"));
+        TRY(check_disjoint(Y, {X, W, Bi, M, S}, nullptr));
+        TRY(check_disjoint(M, {X, W, Bi, S}, nullptr));
+        TRY(check_disjoint(S, {X, W, Bi}, nullptr));
+        TRY(check_device());
+        n.x = x;
+        n.weight = weight;
+        n.bias = bias;
+        n.y = y;
+        n.mean = mean;
+        n.rstd = rstd;
+        n.vec = aligned16(x, n.ld_x, size) && aligned16(y, n.ld_y, size);
+        n.vec_w = aligned16(weight, 0, 4) && aligned16(bias, 0, 4);
+        return hip_status(muon::launch_norm_forward(n, d->dtype, static_cast<hipStream_t>(stream)),
+                          "layer norm kernel");
+    });
+}
+
+muon_status muon_layernorm_workspace_bytes(const muon_layernorm* d, size_t* out_bytes) {
+    return guarded([&]() -> muon_status {
+        if (!out_bytes) return fail(MUON_E_INVALID_ARG, "null out_bytes");
+        TRY(check_norm(d));
+        *out_bytes = norm_workspace(*d);
+        return MUON_OK;
+    });
+}
+
+muon_status muon_layernorm_backward(const muon_layernorm* d, const void* dy, const void* x, const float* weight,
+                                    const float* mean, const float* rstd, const void* add, void* dx, float* dweight,
+                                    float* dbias, int32_t accumulate, void* workspace, size_t ws_bytes, void* stream) {
+    return guarded([&]() -> muon_status {
+        TRY(check_norm(d));
+        if (d->rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return fail(MUON_E_INVALID_ARG, "null tensor");
+        const int size = d->dtype == MUON_TYPE_FP32 ? 4 : 2;
+        muon::NormArgs n = norm_args(*d);
+        const Tensor DY{dy, d->rows, d->cols, n.ld_y, size}, X{x, d->rows, d->cols, n.ld_x, size},
+            DX{dx, d->rows, d->cols, n.ld_dx, size}, R{add, d->rows, d->cols, n.ld_r, size};
+        const Tensor W{weight, 1, d->cols, d->cols, 4}, DW{dweight, 1, d->cols, d->cols, 4},
+            DB{dbias, 1, d->cols, d->cols, 4};
+        const Tensor M{mean, 1, d->rows, d->rows, 4}, S{rstd, 1, d->rows, d->rows, 4};
+        for (const Tensor& t : {DY, X, DX, R}) TRY(check_align(t.p, size, "dy, x, dx or add"));
+        for (const Tensor& t : {W, DW, DB, M, S}) TRY(check_align(t.p, 4, "a float32 tensor"));
+        const bool sums = dweight || dbias;
+        const size_t need = sums ? norm_workspace(*d) : 0;
+        TRY(check_workspace(workspace, ws_bytes, need));
+        const Tensor K{workspace, 1, (int64_t)need, (int64_t)need, 1};
+        TRY(check_disjoint(DX, {DY, X, R, W, DW, DB, M, S, K}, &R));
+        TRY(check_disjoint(DW, {DY, X, R, W, DB, M, S, K}, nullptr));
+        TRY(check_disjoint(DB, {DY, X, R, W, M, S, K}, nullptr));
+        TRY(check_disjoint(K, {DY, X, R, W, M, S}, nullptr));
+        if (d->rows == 0 && (!sums || accumulate)) return MUON_OK;
+        TRY(check_device());
+        n.dy = dy;
+        n.x = x;
+        n.weight = weight;
+        n.mean = const_cast<float*>(mean);
+        n.rstd = const_cast<float*>(rstd);
+        n.add = add;
+        n.dx = dx;
+        n.dweight = dweight;
+        n.dbias = dbias;
+        n.accumulate = accumulate != 0;
+        n.part = sums ? static_cast<float*>(workspace) : nullptr;
+        n.blocks = muon::norm_backward_blocks(d->rows, d->cols);
+        n.vec = aligned16(dy, n.ld_y, size) && aligned16(x, n.ld_x, size) && aligned16(dx, n.ld_dx, size) &&
+                aligned16(add, n.ld_r, size);
+        n.vec_w = aligned16(weight, 0, 4);
+        return hip_status(muon::launch_norm_backward(n, d->dtype, static_cast<hipStream_t>(stream)),
+                          "layer norm gradient kernels");
+    });
+}
+
+}  // extern "C"

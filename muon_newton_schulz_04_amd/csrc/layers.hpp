@@ -1,0 +1,92 @@
+// Internal interface of the layer operators: the linear layer (matrix product
+// with bias, activation and residual in its epilogue, and its gradients) and
+// layer norm. Plain data shared by the host entry points and the kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace muon {
+
+// What the epilogue of a product does with its fp32 accumulators.
+enum EpiMode {
+    EPI_FORWARD = 0,     // y = act(v + bias) + add; z = v + bias if asked
+    EPI_GRAD_INPUT = 1,  // y = v act'(z) + add
+    EPI_GRAD_WEIGHT = 2  // w (+)= v, float32
+};
+
+struct Epilogue {
+    int32_t mode, act;
+    const float* bias;  // [N] or null
+    const void* add;    // [M, N] of the 16-bit type, or null
+    void* z;            // forward: written if not null; grad input: read if act != none
+    void* y;            // 16-bit output, or float32 for the weight gradient
+    int64_t ld_add, ld_z, ld_y;
+    int32_t accumulate;                // weight gradient: add to what is there
+    int32_t vec_add, vec_z, vec_y;     // rows start 16-byte aligned: chunks of 8 move as vectors
+};
+
+// C[M, N] = sum_k A(m, k) B(k, n) over 16-bit operands, each stored with its k
+// index contiguous ([M, K], [N, K]) or its other index contiguous ([K, M],
+// [K, N]). Every operand's rows start 16-byte aligned and hold a multiple of
+// 8 elements (others are packed first); kp is K rounded up to 8 where a
+// k-contiguous operand is zero-padded to it, else K.
+struct GemmArgs {
+    const void* a;
+    const void* b;
+    int32_t ld_a, ld_b;  // elements
+    int32_t M, N, K, kp;
+    int32_t mp, np;      // row lengths of operands stored with k outermost (M, N rounded up to 8 when packed)
+    int32_t tiles_m, tiles_n;
+    int32_t splits, slices;  // K in `splits` runs of `slices` slices
+    float* partial;          // [splits][M][ld_p] when splits > 1
+    int32_t ld_p;
+    Epilogue epi;
+};
+
+constexpr int kGemmSlice = 32;  // K per pipeline stage
+
+struct GemmPlan {
+    int tile;    // 256 or 128
+    int splits;
+    int slices;  // per split
+};
+
+hipError_t launch_gemm(const GemmArgs& g, int tile, bool a_kc, bool b_kc, int dtype, hipStream_t st);
+hipError_t launch_gemm_reduce(const GemmArgs& g, int dtype, hipStream_t st);
+// dst [rows, cols_pad] <- src [rows, cols] with row stride ld, zero-padded
+hipError_t launch_pack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t cols_pad,
+                       hipStream_t st);
+// db[n] (+)= sum over rows of dy; part: colsum_blocks(rows, cols) x cols_pad floats
+int colsum_blocks(int64_t rows, int64_t cols);
+hipError_t launch_colsum(const void* dy, int64_t ld, int64_t rows, int64_t cols, int dtype, float* part, float* db,
+                         int accumulate, hipStream_t st);
+
+struct NormArgs {
+    int64_t rows;
+    int32_t cols;
+    int64_t ld_x, ld_y, ld_dx, ld_r;
+    float eps;
+    int32_t vec;    // x, y, dy, add, dx: every row starts 16-byte aligned
+    int32_t vec_w;  // weight, bias are 16-byte aligned
+    const void* x;
+    const float* weight;
+    const float* bias;
+    void* y;
+    float* mean;
+    float* rstd;
+    const void* dy;
+    const void* add;
+    void* dx;
+    float* dweight;
+    float* dbias;
+    int32_t accumulate;
+    float* part;   // [blocks][2][cols]
+    int32_t blocks;
+};
+
+int norm_backward_blocks(int64_t rows, int64_t cols);
+hipError_t launch_norm_forward(const NormArgs& n, int dtype, hipStream_t st);
+hipError_t launch_norm_backward(const NormArgs& n, int dtype, hipStream_t st);
+
+}  // namespace muon
