@@ -27,8 +27,6 @@ namespace muon {
 namespace {
 
 constexpr int BK = kGemmSlice;
-constexpr int NBUF = 4;
-constexpr int DIST = NBUF - 1;     // slices a load goes out ahead of its use
 constexpr int KROWB = 2 * BK;      // bytes of a row of a k-contiguous tile
 constexpr uint32_t OUT = 0x80000000u;  // an offset beyond every resource's range
 
@@ -67,7 +65,7 @@ struct Operand {
     int kch;           // KC: the lane's first k within a slice
     uint32_t off[NLD];
     int lds_row;       // wave's first LDS byte of a load instruction
-    int rd[BLK == 4 ? 4 : 2];  // fragment read offsets: KC uses [0], [1] per k16 half
+    int rd[4];  // fragment read offsets: KC uses [0], [1] per k16 half, else one per block
 
     __device__ __forceinline__ void init(const void* p, int ld, int i0, int n, int kp, int kend_, int wave, int lane,
                                          int wblk) {
@@ -168,14 +166,14 @@ __device__ __forceinline__ void tile_of(int b, int total, int tm, int tn, int& t
     tj = l / rows;
 }
 
-template <typename T, int TILE, bool AKC, bool BKC>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, TILE == 256 ? 1 : 2))) void k_gemm(
-    const GemmArgs g) {
-    constexpr int STAGE = 2 * TILE * KROWB;
-    constexpr int BOFF = TILE * KROWB;  // the B tile within a stage
-    constexpr int BLK = TILE / 64;
-    constexpr int WT = TILE / 2;
-    constexpr int SROW = WT * 4 + 16;  // bytes of a staged epilogue row
+template <typename T, int TM, int TN, int NBUF, bool AKC, bool BKC>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm(const GemmArgs g) {
+    constexpr int DIST = NBUF - 1;  // slices a load goes out ahead of its use
+    constexpr int BOFF = TM * KROWB;  // the B tile within a stage
+    constexpr int STAGE = (TM + TN) * KROWB;
+    constexpr int WM = TM / 2, WN = TN / 2;   // a wave's block
+    constexpr int FRI = WM / 32, FRJ = WN / 32;
+    constexpr int SROW = WN * 4 + 16;  // bytes of a staged epilogue row
     static_assert(4 * 32 * SROW <= NBUF * STAGE, "epilogue staging");
     __shared__ __attribute__((aligned(16))) char smem[NBUF * STAGE];
 
@@ -184,70 +182,93 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, TILE == 
     const int wi = wave >> 1, wj = wave & 1;
     int ti, tj, sp;
     tile_of(blockIdx.x, gridDim.x, g.tiles_m, g.tiles_n, ti, tj, sp);
-    const int i0 = ti * TILE, j0 = tj * TILE;
+    const int i0 = ti * TM, j0 = tj * TN;
     const int kmax = AKC || BKC ? g.kp : g.K;
     const int kb = sp * g.slices * BK;
     int ke = kb + g.slices * BK;
     ke = ke < kmax ? ke : kmax;
     const int nk = ke > kb ? (ke - kb + BK - 1) / BK : 0;
 
-    Operand<T, TILE, AKC> A;
-    Operand<T, TILE, BKC> B;
+    using OA = Operand<T, TM, AKC>;
+    using OB = Operand<T, TN, BKC>;
+    OA A;
+    OB B;
     A.init(g.a, g.ld_a, i0, AKC ? g.M : g.mp, g.kp, AKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wi);
     B.init(g.b, g.ld_b, j0, BKC ? g.N : g.np, g.kp, BKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wj);
-    constexpr int NLD = Operand<T, TILE, AKC>::NLD;
+    constexpr int NLD = OA::NLD + OB::NLD;  // load instructions a wave issues per slice
 
-    auto buf = [&](int k) { return smem + (k & (NBUF - 1)) * STAGE; };
-    auto dma_stage = [&](int kt) {
+    auto dma_stage = [&](int kt, char* S) {
         const auto sa = A.slice(kb + kt * BK);
         const auto sb = B.slice(kb + kt * BK);
-        char* S = buf(kt);
 #pragma unroll
-        for (int q = 0; q < NLD; ++q) A.load(sa, S, q);
+        for (int q = 0; q < OA::NLD; ++q) A.load(sa, S, q);
 #pragma unroll
-        for (int q = 0; q < NLD; ++q) B.load(sb, S + BOFF, q);
+        for (int q = 0; q < OB::NLD; ++q) B.load(sb, S + BOFF, q);
     };
 
-    f32x16 acc[BLK][BLK];
+    f32x16 acc[FRI][FRJ];
 #pragma unroll
-    for (int a = 0; a < BLK; ++a)
+    for (int a = 0; a < FRI; ++a)
 #pragma unroll
-        for (int b = 0; b < BLK; ++b)
+        for (int b = 0; b < FRJ; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
 
-    typename V8<T>::type pf[2][BLK], qf[2][BLK];
+    typename V8<T>::type pf[2][FRI], qf[2][FRJ];
     auto read_frags = [&](const char* S, int ks) {
 #pragma unroll
-        for (int f = 0; f < BLK; ++f) pf[ks][f] = A.read(S, ks, f);
+        for (int f = 0; f < FRJ; ++f) qf[ks][f] = B.read(S + BOFF, ks, f);
 #pragma unroll
-        for (int f = 0; f < BLK; ++f) qf[ks][f] = B.read(S + BOFF, ks, f);
+        for (int f = 0; f < FRI; ++f) pf[ks][f] = A.read(S, ks, f);
     };
     auto products = [&](int ks, int f0, int f1) {
 #pragma unroll
         for (int fi = f0; fi < f1; ++fi)
 #pragma unroll
-            for (int fj = 0; fj < BLK; ++fj) acc[fi][fj] = mfma<T>(qf[ks][fj], pf[ks][fi], acc[fi][fj]);
+            for (int fj = 0; fj < FRJ; ++fj) acc[fi][fj] = mfma<T>(qf[ks][fj], pf[ks][fi], acc[fi][fj]);
+    };
+    constexpr int NREAD = (AKC ? 1 : 2) * FRI + (BKC ? 1 : 2) * FRJ;  // LDS reads of a k16 half
+    // one matrix instruction, then its share of N LDS reads
+    auto interleave = [&](auto n_c, auto m_c) {
+        constexpr int N = decltype(n_c)::value, M = decltype(m_c)::value;
+        static_for<0, M>([&](auto i_c) {
+            constexpr int I = decltype(i_c)::value;
+            constexpr int R = N * (I + 1) / M - N * I / M;
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if constexpr (R > 0) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+        });
     };
 
     if (nk > 0) {
+        char* cur = smem;                   // slice kt
+        char* nxt = smem + STAGE;           // slice kt + 1
+        char* fre = smem + DIST * STAGE;    // the buffer of slice kt - 1, for slice kt + DIST
 #pragma unroll
-        for (int k = 0; k < DIST; ++k) dma_stage(k);
-        wait_vm<(DIST - 1) * 2 * NLD>();
+        for (int k = 0; k < DIST; ++k) dma_stage(k, smem + k * STAGE);
+        wait_vm<(DIST - 1) * NLD>();
         __syncthreads();
-        read_frags(buf(0), 0);
-        for (int kt = 0; kt < nk; ++kt) {
-            const char* S = buf(kt);
-            // slice kt + 3 into the buffer of slice kt - 1, which every wave
-            // had read before the last barrier
-            dma_stage(kt + DIST);
+        read_frags(cur, 0);
+        // S, N and F are distinct buffers, and the loads into F are invisible
+        // to the compiler: the explicit waits and barriers order the ring
+        auto slice = [&](const char* __restrict__ S, const char* __restrict__ N, char* __restrict__ F, int kt)
+                         __attribute__((always_inline)) {
+            dma_stage(kt + DIST, F);
             read_frags(S, 1);
-            products(0, 0, BLK);
-            products(1, 0, BLK / 2);
-            wait_vm<(DIST - 1) * 2 * NLD>();  // slice kt + 1 has landed
+            products(0, 0, FRI);
+            interleave(std::integral_constant<int, NREAD>{}, std::integral_constant<int, FRI * FRJ>{});
+            products(1, 0, FRI / 2);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vm<(DIST - 1) * NLD>();  // slice kt + 1 has landed
             __syncthreads();
-            read_frags(buf(kt + 1), 0);
-            products(1, BLK / 2, BLK);
+            read_frags(N, 0);
+            products(1, FRI / 2, FRI);
+            interleave(std::integral_constant<int, NREAD>{}, std::integral_constant<int, FRI * FRJ / 2>{});
+        };
+        for (int kt = 0; kt < nk; ++kt) {
+            slice(cur, nxt, fre, kt);
+            cur = nxt;
+            nxt = nxt == smem + (NBUF - 1) * STAGE ? smem : nxt + STAGE;
+            fre = fre == smem + (NBUF - 1) * STAGE ? smem : fre + STAGE;
         }
         wait_vm0();  // the loads past the end
     }
@@ -255,43 +276,68 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, TILE == 
 
     // ---- epilogue: lane holds C[i][j .. j+3], i = l32, j = 8 g + 4 hi; each
     // wave stages 32 rows at a time in its own LDS region and leaves with 8
-    // consecutive columns a lane ----
+    // consecutive columns a lane. What the epilogue reads for a block of 32
+    // rows goes out before the stores of the block before it, whose latency it
+    // would otherwise wait for (loads and stores retire in order). ----
     char* W = smem + wave * 32 * SROW;
     const int l32 = lane & 31, hi = lane >> 5;
-    constexpr int CPR = WT / 8;      // chunks of 8 per staged row
+    constexpr int CPR = WN / 8;      // chunks of 8 per staged row
     constexpr int RPI = 64 / CPR;    // rows per pass of the wave
+    constexpr int NP = 32 / RPI;     // passes per block
     const int ch = lane % CPR, rr = lane / CPR;
-    const int col = j0 + wj * WT + ch * 8;
-    const int ncol = g.N - col;
+    const int col = j0 + wj * WN + ch * 8;
+    const bool in = col < g.N;
+    const int64_t ccol = in ? col : 0;
+    const int row0 = i0 + wi * WM + rr;
+    const bool direct = g.direct != 0;
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (g.epi.bias && ncol > 0) load8(g.epi.bias + col, ncol, false, bias);
+    if (direct && g.epi.bias) load8(g.epi.bias + ccol, 8, false, bias);
+    Inputs<T> cin[NP], nin[NP];
+    auto fetch = [&](int fi, Inputs<T>(&x)[NP]) {
 #pragma unroll
-    for (int fi = 0; fi < BLK; ++fi) {
+        for (int it = 0; it < NP; ++it) {
+            const int row = row0 + 32 * fi + it * RPI;
+            x[it].fetch(g.epi, row < g.M ? row : g.M - 1, ccol);
+        }
+    };
+    if (direct) fetch(0, nin);
+#pragma unroll 1
+    for (int fi = 0; fi < FRI; ++fi) {
+        static_for<0, FRI>([&](auto f_c) {
+            constexpr int F = decltype(f_c)::value;
+            if (fi == F) {
 #pragma unroll
-        for (int fj = 0; fj < BLK; ++fj)
+                for (int fj = 0; fj < FRJ; ++fj)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                f32x4 v;
+                    for (int q = 0; q < 4; ++q) {
+                        f32x4 v;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = acc[fi][fj][4 * q + e];
-                *reinterpret_cast<f32x4*>(W + l32 * SROW + 4 * (32 * fj + 8 * q + 4 * hi)) = v;
+                        for (int e = 0; e < 4; ++e) v[e] = acc[F][fj][4 * q + e];
+                        *reinterpret_cast<f32x4*>(W + l32 * SROW + 4 * (32 * fj + 8 * q + 4 * hi)) = v;
+                    }
             }
+        });
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-#pragma unroll 2
-        for (int it = 0; it < 32 / RPI; ++it) {
-            const int row = i0 + wi * WT + 32 * fi + it * RPI + rr;
+        if (direct) {
+#pragma unroll
+            for (int it = 0; it < NP; ++it) cin[it] = nin[it];
+            if (fi + 1 < FRI) fetch(fi + 1, nin);
+        }
+#pragma unroll
+        for (int it = 0; it < NP; ++it) {
+            const int row = row0 + 32 * fi + it * RPI;
             const f32x4* s = reinterpret_cast<const f32x4*>(W + (it * RPI + rr) * SROW + 32 * ch);
             const f32x4 lo = s[0], up = s[1];
-            float v[8] = {lo[0], lo[1], lo[2], lo[3], up[0], up[1], up[2], up[3]};
-            if (row < g.M && ncol > 0) {
-                if (g.splits > 1) {
+            if (row < g.M && in) {
+                if (direct) {
+                    float v[8] = {lo[0], lo[1], lo[2], lo[3], up[0], up[1], up[2], up[3]};
+                    finish8<T>(g.epi, row, col, 8, true, v, bias, cin[it]);
+                } else {
                     // ld_p is N rounded up to 8: whole chunks
                     float* p = g.partial + ((int64_t)sp * g.M + row) * g.ld_p + col;
                     *reinterpret_cast<f32x4*>(p) = lo;
                     *reinterpret_cast<f32x4*>(p + 4) = up;
-                } else {
-                    epilogue8<T>(g.epi, row, col, ncol, v, bias);
                 }
             }
         }
@@ -320,7 +366,10 @@ __global__ __launch_bounds__(256) void k_gemm_reduce(const GemmArgs g) {
     }
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (g.epi.bias) load8(g.epi.bias + col, g.N - col, false, bias);
-    epilogue8<T>(g.epi, row, col, g.N - col, v, bias);
+    const bool vec = g.N - col >= 8 && g.epi.vec;
+    Inputs<T> in;
+    if (vec) in.fetch(g.epi, row, col);
+    finish8<T>(g.epi, row, col, g.N - col, vec, v, bias, in);
 }
 
 // Rows of any alignment and length to 16-byte aligned, zero-padded ones: one
@@ -380,23 +429,24 @@ __global__ __launch_bounds__(256) void k_colsum_join(const float* __restrict__ p
     db[c] = accumulate ? db[c] + s : s;
 }
 
-template <typename T, int TILE>
+template <typename T, int TM, int NBUF>
 hipError_t gemm_t(const GemmArgs& g, bool a_kc, bool b_kc, hipStream_t st) {
     const int grid = g.tiles_m * g.tiles_n * g.splits;
     if (a_kc && b_kc)
-        k_gemm<T, TILE, true, true><<<grid, 256, 0, st>>>(g);
+        k_gemm<T, TM, 128, NBUF, true, true><<<grid, 256, 0, st>>>(g);
     else if (a_kc)
-        k_gemm<T, TILE, true, false><<<grid, 256, 0, st>>>(g);
+        k_gemm<T, TM, 128, NBUF, true, false><<<grid, 256, 0, st>>>(g);
     else
-        k_gemm<T, TILE, false, false><<<grid, 256, 0, st>>>(g);
+        k_gemm<T, TM, 128, NBUF, false, false><<<grid, 256, 0, st>>>(g);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_gemm(const GemmArgs& g, int tile, bool a_kc, bool b_kc, int dtype, hipStream_t st) {
-    if (dtype == 0) return tile == 256 ? gemm_t<bf16, 256>(g, a_kc, b_kc, st) : gemm_t<bf16, 128>(g, a_kc, b_kc, st);
-    return tile == 256 ? gemm_t<f16, 256>(g, a_kc, b_kc, st) : gemm_t<f16, 128>(g, a_kc, b_kc, st);
+hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int dtype, hipStream_t st) {
+    if (dtype == 0)
+        return tile_m == 256 ? gemm_t<bf16, 256, 3>(g, a_kc, b_kc, st) : gemm_t<bf16, 128, 4>(g, a_kc, b_kc, st);
+    return tile_m == 256 ? gemm_t<f16, 256, 3>(g, a_kc, b_kc, st) : gemm_t<f16, 128, 4>(g, a_kc, b_kc, st);
 }
 
 hipError_t launch_gemm_reduce(const GemmArgs& g, int dtype, hipStream_t st) {

@@ -72,7 +72,8 @@ constexpr float kGeluCubic = 0.044715f;
 // gelu_tanh(z) = z/2 (1 + tanh u) = z sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3):
 // one exponential and one reciprocal, and no cancellation in the tail, where
 // 1 + tanh u loses its bits. gelu(z) = z erfc(-z / sqrt 2) / 2 for the same reason.
-__device__ __forceinline__ float act_value(int act, float z) {
+template <int act>
+__device__ __forceinline__ float act_value(float z) {
     switch (act) {
         case ACT_RELU: return z > 0.f ? z : z * 0.f;
         case ACT_RELU2: {
@@ -89,7 +90,8 @@ __device__ __forceinline__ float act_value(int act, float z) {
 // The derivative at z. relu'(0) = 0. Factors z times a vanishing term are
 // taken at z clamped to +-30, where that term is 0 already, so that no
 // inf * 0 comes up for a large finite z; a NaN stays one through the first term.
-__device__ __forceinline__ float act_slope(int act, float z) {
+template <int act>
+__device__ __forceinline__ float act_slope(float z) {
     const float zc = fminf(fmaxf(z, -30.f), 30.f);
     switch (act) {
         case ACT_RELU: return z > 0.f ? 1.f : z != z ? z : 0.f;
@@ -109,43 +111,108 @@ __device__ __forceinline__ float act_slope(int act, float z) {
     }
 }
 
-// The epilogue of 8 consecutive accumulators of row r from column c on, n of
-// them inside the matrix. bias: their bias values (forward).
+// One uniform branch for a chunk of 8, not one an element.
+#define MUON_ACT_CASE(A, F)                                 \
+    case A:                                                 \
+        _Pragma("unroll") for (int e = 0; e < 8; ++e) v[e] = F<A>(v[e]); \
+        break;
+__device__ __forceinline__ void act_values(int act, float (&v)[8]) {
+    switch (act) {
+        MUON_ACT_CASE(ACT_RELU, act_value)
+        MUON_ACT_CASE(ACT_RELU2, act_value)
+        MUON_ACT_CASE(ACT_GELU, act_value)
+        MUON_ACT_CASE(ACT_GELU_TANH, act_value)
+        MUON_ACT_CASE(ACT_SILU, act_value)
+    }
+}
+__device__ __forceinline__ void act_slopes(int act, float (&v)[8]) {
+    switch (act) {
+        MUON_ACT_CASE(ACT_RELU, act_slope)
+        MUON_ACT_CASE(ACT_RELU2, act_slope)
+        MUON_ACT_CASE(ACT_GELU, act_slope)
+        MUON_ACT_CASE(ACT_GELU_TANH, act_slope)
+        MUON_ACT_CASE(ACT_SILU, act_slope)
+    }
+}
+#undef MUON_ACT_CASE
+
+// What the epilogue reads of a chunk of 8 outputs, fetched ahead of its use as
+// 16-byte vectors: add and z (16-bit), or the weight gradient to add to.
 template <typename T>
-__device__ __forceinline__ void epilogue8(const Epilogue& E, int64_t r, int c, int n, float (&v)[8],
-                                          const float (&bias)[8]) {
+struct Inputs {
+    uint4 a, z;
+    __device__ __forceinline__ void fetch(const Epilogue& E, int64_t r, int64_t c) {
+        if (E.mode == EPI_GRAD_WEIGHT) {
+            if (E.accumulate) {
+                const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(E.y) + r * E.ld_y + c);
+                a = p[0];
+                z = p[1];
+            }
+            return;
+        }
+        if (E.add) a = *reinterpret_cast<const uint4*>(static_cast<const T*>(E.add) + r * E.ld_add + c);
+        if (E.mode == EPI_GRAD_INPUT && E.act != ACT_NONE)
+            z = *reinterpret_cast<const uint4*>(static_cast<const T*>(E.z) + r * E.ld_z + c);
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ void widen8(const uint4& u, float (&v)[8]) {
+    const typename V8<T>::type t = __builtin_bit_cast(typename V8<T>::type, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (float)t[e];
+}
+
+// The epilogue of 8 consecutive accumulators of row r from column c on, n of
+// them inside the matrix. bias: their bias values (forward). vec: all 8 are
+// inside, every row is 16-byte aligned, and `in` holds what is read;
+// otherwise elements are read and written one by one.
+template <typename T>
+__device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c, int n, bool vec, float (&v)[8],
+                                        const float (&bias)[8], const Inputs<T>& in) {
+    float t[8];
     if (E.mode == EPI_GRAD_WEIGHT) {
         float* y = static_cast<float*>(E.y) + r * E.ld_y + c;
         if (E.accumulate) {
-            float o[8];
-            load8(y, n, E.vec_y, o);
+            if (vec) {
+                const f32x4 lo = __builtin_bit_cast(f32x4, in.a), up = __builtin_bit_cast(f32x4, in.z);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += o[e];
+                for (int e = 0; e < 4; ++e) {
+                    t[e] = lo[e];
+                    t[4 + e] = up[e];
+                }
+            } else {
+                load8(y, n, false, t);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += t[e];
         }
-        store8(y, n, E.vec_y, v);
+        store8(y, n, vec, v);
         return;
     }
     if (E.mode == EPI_FORWARD) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += bias[e];
-        if (E.z) store8(static_cast<T*>(E.z) + r * E.ld_z + c, n, E.vec_z, v);
-        if (E.act != ACT_NONE) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = act_value(E.act, v[e]);
-        }
+        if (E.z) store8(static_cast<T*>(E.z) + r * E.ld_z + c, n, vec, v);
+        act_values(E.act, v);
     } else if (E.act != ACT_NONE) {
-        float z[8];
-        load8(static_cast<const T*>(E.z) + r * E.ld_z + c, n, E.vec_z, z);
+        if (vec)
+            widen8<T>(in.z, t);
+        else
+            load8(static_cast<const T*>(E.z) + r * E.ld_z + c, n, false, t);
+        act_slopes(E.act, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= act_slope(E.act, z[e]);
+        for (int e = 0; e < 8; ++e) v[e] *= t[e];
     }
     if (E.add) {
-        float a[8];
-        load8(static_cast<const T*>(E.add) + r * E.ld_add + c, n, E.vec_add, a);
+        if (vec)
+            widen8<T>(in.a, t);
+        else
+            load8(static_cast<const T*>(E.add) + r * E.ld_add + c, n, false, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += a[e];
+        for (int e = 0; e < 8; ++e) v[e] += t[e];
     }
-    store8(static_cast<T*>(E.y) + r * E.ld_y + c, n, E.vec_y, v);
+    store8(static_cast<T*>(E.y) + r * E.ld_y + c, n, vec, v);
 }
 
 }  // namespace muon

@@ -157,12 +157,11 @@ muon::GemmPlan choose_plan(int64_t M, int64_t N, int64_t K) {
     const int64_t slices = (K + muon::kGemmSlice - 1) / muon::kGemmSlice;
     muon::GemmPlan best{128, 1, (int)(slices > 0 ? slices : 1)};
     double best_t = 1e300;
-    for (int tile : {256, 128}) {
-        const int64_t tiles = ((M + tile - 1) / tile) * ((N + tile - 1) / tile);
-        // one 256 tile fills a CU; two 128 tiles share one. Clocks: a slice's
-        // matrix work, and what a workgroup spends outside its main loop
-        const double slots = tile == 256 ? 256 : 512, per_slice = tile == 256 ? 1400 : 900,
-                     fixed = tile == 256 ? 14000 : 7000;
+    for (int tm : {256, 128}) {
+        const int64_t tiles = ((M + tm - 1) / tm) * ((N + muon::kGemmTileN - 1) / muon::kGemmTileN);
+        // two workgroups share a CU. Clocks: a slice's matrix work, and what a
+        // workgroup spends outside its main loop
+        const double slots = 512, per_slice = tm == 256 ? 1400 : 900, fixed = tm == 256 ? 14000 : 7000;
         for (int s = 1; s <= 64; ++s) {
             if (s > 1 && (s > slices || tiles * s > 2 * slots)) break;
             const int64_t per = (slices + s - 1) / s;
@@ -172,7 +171,7 @@ muon::GemmPlan choose_plan(int64_t M, int64_t N, int64_t K) {
             if (s > 1) t += 8.0 * (double)M * (double)N * s / 1700.0 + 6000.0;
             if (t < best_t) {
                 best_t = t;
-                best = {tile, s, (int)(per > 0 ? per : 1)};
+                best = {tm, s, (int)(per > 0 ? per : 1)};
             }
         }
     }
@@ -184,6 +183,7 @@ struct Product {
     int64_t M, N, K;
     Tensor a, b;
     bool a_kc, b_kc;  // k is the contiguous index
+    bool direct;
     bool pack_a, pack_b;
     muon::GemmPlan plan;
     size_t off_a, off_b, off_part, off_cols, bytes;
@@ -191,32 +191,39 @@ struct Product {
 
 bool needs_pack(const Tensor& t) { return t.rows > 0 && (!aligned16(t.p, t.ld, 2) || t.cols % 8 != 0); }
 
-muon_status plan_product(const muon_linear& d, int op, const void* pa, const void* pb, bool dbias, Product* P) {
+// vec: all that the epilogue touches moves as whole 16-byte vectors (else, and
+// with K splits, the sums go through the workspace and the join kernel does
+// the epilogue element by element).
+muon_status plan_product(const muon_linear& d, int op, const void* pa, const void* pb, bool vec, bool dbias,
+                         Product* P) {
     const bool io = d.weight_layout == MUON_WEIGHT_IN_OUT;
     if (op == MUON_LINEAR_FORWARD) {
-        *P = {d.tokens, d.out_features, d.in_features, tensor_x(d, pa), tensor_w(d, pb, 2), true, !io};
+        *P = {d.tokens, d.out_features, d.in_features, tensor_x(d, pa), tensor_w(d, pb, 2), true, !io, false};
     } else if (op == MUON_LINEAR_GRAD_INPUT) {
-        *P = {d.tokens, d.in_features, d.out_features, tensor_y(d, pa), tensor_w(d, pb, 2), true, io};
+        *P = {d.tokens, d.in_features, d.out_features, tensor_y(d, pa), tensor_w(d, pb, 2), true, io, false};
     } else {
         const Tensor x = tensor_x(d, pa), dy = tensor_y(d, pb);
         if (io)
-            *P = {d.in_features, d.out_features, d.tokens, x, dy, false, false};
+            *P = {d.in_features, d.out_features, d.tokens, x, dy, false, false, false};
         else
-            *P = {d.out_features, d.in_features, d.tokens, dy, x, false, false};
+            *P = {d.out_features, d.in_features, d.tokens, dy, x, false, false, false};
     }
     P->pack_a = needs_pack(P->a);
     P->pack_b = needs_pack(P->b);
     P->plan = choose_plan(P->M, P->N, P->K);
-    const int64_t T = P->plan.tile;
-    if (((P->M + T - 1) / T) * ((P->N + T - 1) / T) >= (int64_t)1 << 23)
+    const int64_t tm = P->plan.tile_m, tn = muon::kGemmTileN;
+    if (((P->M + tm - 1) / tm) * ((P->N + tn - 1) / tn) >= (int64_t)1 << 23)
         return fail(MUON_E_SHAPE, "linear: output too large");
+    P->direct = vec && P->N % 8 == 0 && P->plan.splits == 1;
+    if (!P->direct && P->M * (up8(P->N) / 8) >= (int64_t)1 << 32)
+        return fail(MUON_E_SHAPE, "linear: output too large for unaligned or odd-length rows");
     size_t o = 0;
     P->off_a = o;
     if (P->pack_a) o = up256(o + (size_t)P->a.rows * up8(P->a.cols) * 2);
     P->off_b = o;
     if (P->pack_b) o = up256(o + (size_t)P->b.rows * up8(P->b.cols) * 2);
     P->off_part = o;
-    if (P->plan.splits > 1) o = up256(o + (size_t)P->plan.splits * P->M * up8(P->N) * 4);
+    if (!P->direct) o = up256(o + (size_t)P->plan.splits * P->M * up8(P->N) * 4);
     P->off_cols = o;
     if (dbias) o = up256(o + (size_t)muon::colsum_blocks(d.tokens, d.out_features) * up8(d.out_features) * 4);
     P->bytes = o;
@@ -232,7 +239,7 @@ muon_status run_product(Product& P, int dtype, muon::Epilogue& E, char* ws, hipS
         t.p = dst;
         t.ld = up8(t.cols);
     }
-    const int T = P.plan.tile;
+    const int tm = P.plan.tile_m, tn = muon::kGemmTileN;
     muon::GemmArgs g{};
     g.a = P.a.p;
     g.b = P.b.p;
@@ -244,16 +251,47 @@ muon_status run_product(Product& P, int dtype, muon::Epilogue& E, char* ws, hipS
     g.kp = (int)((P.a_kc || P.b_kc) ? up8(P.K) : P.K);
     g.mp = (int)up8(P.M);
     g.np = (int)up8(P.N);
-    g.tiles_m = (int)((P.M + T - 1) / T);
-    g.tiles_n = (int)((P.N + T - 1) / T);
+    g.tiles_m = (int)((P.M + tm - 1) / tm);
+    g.tiles_n = (int)((P.N + tn - 1) / tn);
     g.splits = P.plan.splits;
     g.slices = P.plan.slices;
+    g.direct = P.direct;
     g.partial = reinterpret_cast<float*>(ws + P.off_part);
     g.ld_p = (int)up8(P.N);
     g.epi = E;
-    TRY(hip_status(muon::launch_gemm(g, T, P.a_kc, P.b_kc, dtype, st), "product kernel"));
-    if (g.splits > 1) TRY(hip_status(muon::launch_gemm_reduce(g, dtype, st), "split join kernel"));
+    TRY(hip_status(muon::launch_gemm(g, tm, P.a_kc, P.b_kc, dtype, st), "product kernel"));
+    if (!g.direct) TRY(hip_status(muon::launch_gemm_reduce(g, dtype, st), "split join kernel"));
     return MUON_OK;
+}
+
+muon_status check_epilogue(const muon_linear& d, int op, const muon_epilogue& e) {
+    const bool fwd = op == MUON_LINEAR_FORWARD;
+    const int64_t cols = fwd ? d.out_features : d.in_features;
+    if (e.activation < MUON_ACT_NONE || e.activation > MUON_ACT_SILU)
+        return fail(MUON_E_INVALID_ARG, "epilogue: unknown activation");
+    if (e.reserved != 0) return fail(MUON_E_INVALID_ARG, "epilogue: reserved must be 0");
+    if (!fwd && e.bias) return fail(MUON_E_INVALID_ARG, "grad input: takes no bias");
+    TRY(check_ld(e.ld_add, cols, "ld_add"));
+    return check_ld(e.ld_z, cols, "ld_z");
+}
+
+// What a product's epilogue reads and writes (e NULL: only the output).
+struct Outputs {
+    Tensor y, add, z;
+    bool vec() const { return vec_of(y) && vec_of(add) && vec_of(z); }
+    static bool vec_of(const Tensor& t) { return !t.p || aligned16(t.p, t.ld, t.size); }
+};
+
+Outputs outputs_of(const muon_linear& d, int op, const muon_epilogue* e, const void* y) {
+    if (op == MUON_LINEAR_GRAD_WEIGHT) return {tensor_w(d, y, 4), {}, {}};
+    const bool fwd = op == MUON_LINEAR_FORWARD;
+    const int64_t cols = fwd ? d.out_features : d.in_features;
+    Outputs o{fwd ? tensor_y(d, y) : tensor_x(d, y), {}, {}};
+    if (!e) return o;
+    o.add = {e->add, d.tokens, cols, e->ld_add ? e->ld_add : cols, 2};
+    // the way back reads z only for an activation
+    if (fwd || e->activation != MUON_ACT_NONE) o.z = {e->z, d.tokens, cols, e->ld_z ? e->ld_z : cols, 2};
+    return o;
 }
 
 // forward and grad input
@@ -261,29 +299,21 @@ muon_status run_layer(const muon_linear* d, int op, const void* a, const void* w
                       void* ws, size_t ws_bytes, void* stream) {
     TRY(check_linear(d));
     const bool fwd = op == MUON_LINEAR_FORWARD;
-    const int64_t out_cols = fwd ? d->out_features : d->in_features;
     muon_epilogue none{};
     if (!e) e = &none;
-    if (e->activation < MUON_ACT_NONE || e->activation > MUON_ACT_SILU)
-        return fail(MUON_E_INVALID_ARG, "epilogue: unknown activation");
-    if (e->reserved != 0) return fail(MUON_E_INVALID_ARG, "epilogue: reserved must be 0");
-    if (!fwd && e->bias) return fail(MUON_E_INVALID_ARG, "grad input: takes no bias");
-    TRY(check_ld(e->ld_add, out_cols, "ld_add"));
-    TRY(check_ld(e->ld_z, out_cols, "ld_z"));
+    TRY(check_epilogue(*d, op, *e));
     if (d->tokens == 0) return MUON_OK;
     if (!a || !w || !y) return fail(MUON_E_INVALID_ARG, "null tensor");
     if (!fwd && e->activation != MUON_ACT_NONE && !e->z)
         return fail(MUON_E_INVALID_ARG, "grad input: an activation needs its pre-activation z");
-    const bool use_z = e->z && (fwd || e->activation != MUON_ACT_NONE);
     const Tensor A = fwd ? tensor_x(*d, a) : tensor_y(*d, a), W = tensor_w(*d, w, 2);
-    const Tensor Y = fwd ? tensor_y(*d, y) : tensor_x(*d, y);
-    const Tensor R{e->add, d->tokens, out_cols, e->ld_add ? e->ld_add : out_cols, 2};
-    const Tensor Z{use_z ? e->z : nullptr, d->tokens, out_cols, e->ld_z ? e->ld_z : out_cols, 2};
+    const Outputs o = outputs_of(*d, op, e, y);
+    const Tensor &Y = o.y, &R = o.add, &Z = o.z;
     const Tensor Bi{e->bias, 1, d->out_features, d->out_features, 4};
     for (const Tensor& t : {A, W, Y, R, Z}) TRY(check_align(t.p, 2, "a 16-bit tensor"));
     TRY(check_align(e->bias, 4, "bias"));
     Product P;
-    TRY(plan_product(*d, op, a, w, false, &P));
+    TRY(plan_product(*d, op, a, w, o.vec(), false, &P));
     TRY(check_workspace(ws, ws_bytes, P.bytes));
     const Tensor S{ws, 1, (int64_t)P.bytes, (int64_t)P.bytes, 1};
     TRY(check_disjoint(Y, {A, W, R, Z, Bi, S}, &R));
@@ -296,14 +326,12 @@ muon_status run_layer(const muon_linear* d, int op, const void* a, const void* w
     E.act = e->activation;
     E.bias = e->bias;
     E.add = e->add;
-    E.z = use_z ? e->z : nullptr;
+    E.z = e->z && Z.p ? e->z : nullptr;
     E.y = y;
     E.ld_add = R.ld;
     E.ld_z = Z.ld;
     E.ld_y = Y.ld;
-    E.vec_add = aligned16(R.p, R.ld, 2);
-    E.vec_z = aligned16(Z.p, Z.ld, 2);
-    E.vec_y = aligned16(Y.p, Y.ld, 2);
+    E.vec = o.vec();
     return run_product(P, d->dtype, E, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
 }
 
@@ -345,7 +373,7 @@ extern "C" {
 const char* muon_op_last_error(void) { return g_error.c_str(); }
 
 muon_status muon_linear_workspace_bytes(const muon_linear* d, int32_t op, const void* a, const void* b,
-                                        size_t* out_bytes) {
+                                        const muon_epilogue* e, const void* y, size_t* out_bytes) {
     return guarded([&]() -> muon_status {
         if (!out_bytes) return fail(MUON_E_INVALID_ARG, "null out_bytes");
         TRY(check_linear(d));
@@ -353,8 +381,9 @@ muon_status muon_linear_workspace_bytes(const muon_linear* d, int32_t op, const 
             return fail(MUON_E_INVALID_ARG, "unknown linear operation");
         *out_bytes = 0;
         if (d->tokens == 0 && op != MUON_LINEAR_GRAD_WEIGHT) return MUON_OK;
+        if (e && op != MUON_LINEAR_GRAD_WEIGHT) TRY(check_epilogue(*d, op, *e));
         Product P;
-        TRY(plan_product(*d, op, a, b, op == MUON_LINEAR_GRAD_WEIGHT, &P));
+        TRY(plan_product(*d, op, a, b, outputs_of(*d, op, e, y).vec(), op == MUON_LINEAR_GRAD_WEIGHT, &P));
         *out_bytes = P.bytes;
         return MUON_OK;
     });
@@ -382,7 +411,8 @@ muon_status muon_linear_grad_weight(const muon_linear* d, const void* x, const v
         TRY(check_align(dw, 4, "dw"));
         TRY(check_align(dbias, 4, "dbias"));
         Product P;
-        TRY(plan_product(*d, MUON_LINEAR_GRAD_WEIGHT, x, dy, dbias != nullptr, &P));
+        const Outputs o = outputs_of(*d, MUON_LINEAR_GRAD_WEIGHT, nullptr, dw);
+        TRY(plan_product(*d, MUON_LINEAR_GRAD_WEIGHT, x, dy, o.vec(), dbias != nullptr, &P));
         TRY(check_workspace(workspace, ws_bytes, P.bytes));
         const Tensor S{workspace, 1, (int64_t)P.bytes, (int64_t)P.bytes, 1};
         TRY(check_disjoint(W, {X, Y, Bi, S}, nullptr));
@@ -395,7 +425,7 @@ muon_status muon_linear_grad_weight(const muon_linear* d, const void* x, const v
         E.mode = muon::EPI_GRAD_WEIGHT;
         E.y = dw;
         E.ld_y = W.ld;
-        E.vec_y = aligned16(dw, W.ld, 4);
+        E.vec = o.vec();
         E.accumulate = accumulate != 0;
         TRY(run_product(P, d->dtype, E, ws, st));
         if (dbias) {

@@ -22,8 +22,8 @@ struct Epilogue {
     void* z;            // forward: written if not null; grad input: read if act != none
     void* y;            // 16-bit output, or float32 for the weight gradient
     int64_t ld_add, ld_z, ld_y;
-    int32_t accumulate;                // weight gradient: add to what is there
-    int32_t vec_add, vec_z, vec_y;     // rows start 16-byte aligned: chunks of 8 move as vectors
+    int32_t accumulate;  // weight gradient: add to what is there
+    int32_t vec;         // every row touched starts 16-byte aligned
 };
 
 // C[M, N] = sum_k A(m, k) B(k, n) over 16-bit operands, each stored with its k
@@ -39,20 +39,22 @@ struct GemmArgs {
     int32_t mp, np;      // row lengths of operands stored with k outermost (M, N rounded up to 8 when packed)
     int32_t tiles_m, tiles_n;
     int32_t splits, slices;  // K in `splits` runs of `slices` slices
-    float* partial;          // [splits][M][ld_p] when splits > 1
+    int32_t direct;          // the product kernel does the epilogue (one split, everything moves as whole vectors)
+    float* partial;          // else [splits][M][ld_p]
     int32_t ld_p;
     Epilogue epi;
 };
 
-constexpr int kGemmSlice = 32;  // K per pipeline stage
+constexpr int kGemmSlice = 32;   // K per pipeline stage
+constexpr int kGemmTileN = 128;
 
 struct GemmPlan {
-    int tile;    // 256 or 128
+    int tile_m;  // 256 or 128; tiles are 128 wide
     int splits;
     int slices;  // per split
 };
 
-hipError_t launch_gemm(const GemmArgs& g, int tile, bool a_kc, bool b_kc, int dtype, hipStream_t st);
+hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int dtype, hipStream_t st);
 hipError_t launch_gemm_reduce(const GemmArgs& g, int dtype, hipStream_t st);
 // dst [rows, cols_pad] <- src [rows, cols] with row stride ld, zero-padded
 hipError_t launch_pack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t cols_pad,

@@ -128,11 +128,11 @@ def _run_linear(op, call, what, a, w, act, bias, add, z, out, layout, device, dt
         if z is not None:
             e.ld_z = _matrix("preact", z, dtype, device, rows, cols)
             e.z = z.data_ptr()
-    pa, pw = a.data_ptr(), w.data_ptr()
-    s, nbytes = B.muon_linear_workspace_bytes(d, op, pa, pw)
+    pa, pw, po = a.data_ptr(), w.data_ptr(), out.data_ptr()
+    s, nbytes = B.muon_linear_workspace_bytes(d, op, pa, pw, e, po)
     _check(s, what)
     ws, pws = _workspace(nbytes, device)
-    _check(_call(device, lambda st: call(d, pa, pw, e, out.data_ptr(), pws, nbytes, st)), what)
+    _check(_call(device, lambda st: call(d, pa, pw, e, po, pws, nbytes, st)), what)
     return out
 
 
@@ -181,11 +181,11 @@ def linear_grad_weight(x, dy, dw=None, dbias=None, accumulate=False, weight_layo
         dbias = torch.empty(fout, dtype=torch.float32, device=device)
     pb = 0 if dbias is None else _vector("dbias", dbias, fout, device)
     d = B.muon_linear(x.shape[0], fin, fout, ld_x, ld_w, ld_y, _TYPES[dtype], lay)
-    px, py = x.data_ptr(), dy.data_ptr()
-    s, nbytes = B.muon_linear_workspace_bytes(d, B.MUON_LINEAR_GRAD_WEIGHT, px, py)
+    px, py, pd = x.data_ptr(), dy.data_ptr(), dw.data_ptr()
+    s, nbytes = B.muon_linear_workspace_bytes(d, B.MUON_LINEAR_GRAD_WEIGHT, px, py, None, pd)
     _check(s, "linear_grad_weight")
     ws, pws = _workspace(nbytes, device)
-    _check(_call(device, lambda st: B.muon_linear_grad_weight(d, px, py, dw.data_ptr(), pb, int(accumulate),
+    _check(_call(device, lambda st: B.muon_linear_grad_weight(d, px, py, pd, pb, int(accumulate),
                                                                       pws, nbytes, st)), "linear_grad_weight")
     return dw, dbias
 
