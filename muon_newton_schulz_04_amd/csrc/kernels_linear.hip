@@ -27,6 +27,7 @@ namespace muon {
 namespace {
 
 constexpr int BK = kGemmSlice;
+constexpr int NKS = BK / 16;       // k16 steps of a slice
 constexpr int KROWB = 2 * BK;      // bytes of a row of a k-contiguous tile
 constexpr uint32_t OUT = 0x80000000u;  // an offset beyond every resource's range
 
@@ -41,65 +42,71 @@ __device__ __forceinline__ f32x16 mfma<f16>(f16x8 a, f16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-// s_waitcnt vmcnt(n), the other counters left alone
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+// 16 bytes per lane, global -> LDS: lane i lands at lds + 16 i (a wave-uniform
+// LDS address, passed in M0, which the asm sets right before the load: see
+// dma16, whose conditions hold here too).
+__device__ __forceinline__ void load_lds(u32x4 r, uint32_t lds, uint32_t voff, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :
+                 : "v"(voff), "s"(r), "s"(soff), "s"(__builtin_amdgcn_readfirstlane(lds)));
 }
 
-// How one operand's tile is loaded and read. KC: T rows of KROWB bytes, chunk
-// c (16 bytes) of row r stored at c ^ ((r >> 2) & 3), so that the 16 rows of a
-// phase of ds_read_b128 fall in 16 distinct 16-byte slots. Otherwise BK rows
-// of 2T bytes, chunk c of row r at c ^ (4 (r & 3)), so that the 4 rows x 64
-// bytes of a half-wave's transposing read fall in 4 distinct 64-byte windows.
+// How one operand's tile is loaded and read. KC: TILE rows of 128 bytes (whole
+// cache lines), chunk c (16 bytes) of row r stored at c ^ ((r >> 1) & 7), so
+// that the 16 rows of a phase of ds_read_b128 fall in 16 distinct 16-byte
+// slots. Otherwise BK rows of 2 TILE bytes, chunk c of row r at c ^ (4 (r & 3)),
+// so that the 4 rows x 64 bytes of a half-wave's transposing read fall in 4
+// distinct 64-byte windows.
 template <typename T, int TILE, bool KC>
 struct Operand {
-    static constexpr int XCH = TILE / 8;  // 16-byte chunks of a row (not KC)
-    static constexpr int NLD = TILE * BK * 2 / 4096;  // load instructions a wave issues per slice
-    static constexpr int BLK = TILE / 64;             // 32-wide fragment blocks of a wave
-    const char* base;  // KC: first row of the tile; else row 0, first column of the tile
-    int64_t step;      // bytes per slice (not KC)
-    uint32_t range;    // KC: bytes of the tile's valid rows; else bytes of one row's remainder
+    static constexpr int BYTES = TILE * BK * 2;
+    static constexpr int NLD = BYTES / 4096;  // load instructions a wave issues per slice
+    static constexpr int BLK = TILE / 64;     // 32-wide fragment blocks of a wave
+    u32x4 r;           // KC: the tile's rows; else the slice's
+    uint32_t range;    // bytes of a whole slice's resource (not KC)
+    uint32_t tail;     // bytes of the last row (not KC)
     uint32_t rowb;     // row stride in bytes
-    int kend;          // k at which this split ends
+    uint32_t soff;     // KC: byte offset of the next slice to load
+    int left;          // k values from the next slice to load to the split's end
     int kch;           // KC: the lane's first k within a slice
     uint32_t off[NLD];
-    int lds_row;       // wave's first LDS byte of a load instruction
-    int rd[4];  // fragment read offsets: KC uses [0], [1] per k16 half, else one per block
+    uint32_t lds_row;  // wave's first LDS byte of a load instruction
+    int rd[4];         // fragment read offsets: KC one per k16 step, else one per block
 
-    __device__ __forceinline__ void init(const void* p, int ld, int i0, int n, int kp, int kend_, int wave, int lane,
-                                         int wblk) {
+    __device__ __forceinline__ void init(const void* p, int ld, int i0, int n, int kp, int kb, int kend, int wave,
+                                         int lane, int wblk) {
         rowb = (uint32_t)ld * 2u;
-        kend = kend_;
+        left = kend - kb;
         if constexpr (KC) {
-            // 16 rows of 4 chunks per instruction
+            // 8 rows of 8 chunks per instruction
             const int rows = n - i0 < TILE ? n - i0 : TILE;
-            base = static_cast<const char*>(p) + (int64_t)i0 * rowb;
-            range = (uint32_t)(rows - 1) * rowb + (uint32_t)kp * 2u;
-            const int r = wave * 16 + (lane >> 2);
-            const int c = (lane & 3) ^ ((r >> 2) & 3);
+            r = rsrc(static_cast<const char*>(p) + (int64_t)i0 * rowb, (uint32_t)(rows - 1) * rowb + (uint32_t)kp * 2u);
+            soff = (uint32_t)kb * 2u;
+            const int row0 = wave * 8 + (lane >> 3);
+            const int c = (lane & 7) ^ ((row0 >> 1) & 7);
             kch = c * 8;
 #pragma unroll
             for (int q = 0; q < NLD; ++q) {
-                const int row = r + q * 64;
+                const int row = row0 + q * 32;
                 off[q] = row < rows ? (uint32_t)row * rowb + (uint32_t)c * 16u : OUT;
             }
-            lds_row = wave * 16 * KROWB;
+            lds_row = wave * 8 * KROWB;
             const int l32 = lane & 31, hi = lane >> 5;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-                rd[ks] = (wblk * (TILE / 2) + l32) * KROWB + 16 * ((2 * ks + hi) ^ ((l32 >> 2) & 3));
+            for (int ks = 0; ks < 4; ++ks)
+                rd[ks] = (wblk * (TILE / 2) + l32) * KROWB + 16 * ((2 * ks + hi) ^ ((l32 >> 1) & 7));
         } else {
-            base = static_cast<const char*>(p) + (int64_t)i0 * 2;
-            step = (int64_t)BK * rowb;
-            const int cols = n - i0 < TILE ? n - i0 : TILE;
-            range = (uint32_t)cols * 2u;
+            constexpr int XCH = TILE / 8;  // chunks of a row
             constexpr int RPI = 64 / XCH;  // rows per instruction
-            const int r = wave * RPI + lane / XCH;
-            const int c = (lane % XCH) ^ (4 * (r & 3));
+            const int cols = n - i0 < TILE ? n - i0 : TILE;
+            tail = (uint32_t)cols * 2u;
+            range = (uint32_t)(BK - 1) * rowb + tail;
+            r = rsrc(static_cast<const char*>(p) + (int64_t)kb * rowb + (int64_t)i0 * 2, 0u);
+            const int row0 = wave * RPI + lane / XCH;
+            const int c = (lane % XCH) ^ (4 * (row0 & 3));
 #pragma unroll
             for (int q = 0; q < NLD; ++q)
-                off[q] = c * 8 < cols ? (uint32_t)(r + q * 4 * RPI) * rowb + (uint32_t)c * 16u : OUT;
+                off[q] = c * 8 < cols ? (uint32_t)(row0 + q * 4 * RPI) * rowb + (uint32_t)c * 16u : OUT;
             lds_row = wave * 1024;
             const int g = lane >> 4, s = lane & 15;
             const int row = 8 * (g >> 1) + (s >> 2);
@@ -111,32 +118,25 @@ struct Operand {
         }
     }
 
-    // what a slice's loads need besides off[]: the resource, the scalar offset
-    // and (KC) whether the lane's chunk lies before the end of k
-    struct Slice {
-        u32x4 r;
-        int soff;
-        uint32_t dead;
-    };
-    __device__ __forceinline__ Slice slice(int k0) const {
-        Slice s;
-        const int left = kend - k0;
+    // issue the next slice's loads to LDS address S
+    __device__ __forceinline__ void load(uint32_t S) {
         if constexpr (KC) {
-            s.r = rsrc(base, range);
-            s.soff = left > 0 ? k0 * 2 : 0;
-            s.dead = kch < left ? 0u : OUT;
+            const uint32_t dead = kch < left ? 0u : OUT;  // chunks past the end of k
+            const uint32_t so = left > 0 ? soff : 0u;
+#pragma unroll
+            for (int q = 0; q < NLD; ++q) load_lds(r, S + lds_row + q * 4096, off[q] | dead, so);
+            soff += 2 * BK;
         } else {
-            const int rows = left < 0 ? 0 : left < BK ? left : BK;
-            s.r = rsrc(rows > 0 ? base + (int64_t)k0 * rowb : base, rows > 0 ? (uint32_t)(rows - 1) * rowb + range : 0u);
-            s.soff = 0;
-            s.dead = 0u;
+            r[2] = left >= BK ? range : left > 0 ? (uint32_t)(left - 1) * rowb + tail : 0u;
+#pragma unroll
+            for (int q = 0; q < NLD; ++q) load_lds(r, S + lds_row + q * 4096, off[q], 0u);
+            const uint64_t base = (((uint64_t)r[1] << 32) | r[0]) + (uint64_t)BK * rowb;
+            r[0] = (uint32_t)base;
+            r[1] = (uint32_t)(base >> 32) & 0xffffu;
         }
-        return s;
+        left -= BK;
     }
-    __device__ __forceinline__ void load(const Slice& s, char* S, int q) const {
-        dma16(s.r, S + lds_row + q * 4096, (int)(KC ? (off[q] | s.dead) : off[q]), s.soff);
-    }
-    // fragment block f of k16 half ks
+    // fragment block f of k16 step ks
     __device__ __forceinline__ typename V8<T>::type read(const char* S, int ks, int f) const {
         if constexpr (KC) {
             return *reinterpret_cast<const typename V8<T>::type*>(S + rd[ks] + f * 32 * KROWB);
@@ -166,16 +166,16 @@ __device__ __forceinline__ void tile_of(int b, int total, int tm, int tn, int& t
     tj = l / rows;
 }
 
-template <typename T, int TM, int TN, int NBUF, bool AKC, bool BKC>
+template <typename T, int TM, int TN, bool AKC, bool BKC>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm(const GemmArgs g) {
-    constexpr int DIST = NBUF - 1;  // slices a load goes out ahead of its use
-    constexpr int BOFF = TM * KROWB;  // the B tile within a stage
-    constexpr int STAGE = (TM + TN) * KROWB;
+    using OA = Operand<T, TM, AKC>;
+    using OB = Operand<T, TN, BKC>;
     constexpr int WM = TM / 2, WN = TN / 2;   // a wave's block
     constexpr int FRI = WM / 32, FRJ = WN / 32;
     constexpr int SROW = WN * 4 + 16;  // bytes of a staged epilogue row
-    static_assert(4 * 32 * SROW <= NBUF * STAGE, "epilogue staging");
-    __shared__ __attribute__((aligned(16))) char smem[NBUF * STAGE];
+    constexpr int SMEM = 2 * OA::BYTES + OB::BYTES;
+    static_assert(4 * 32 * SROW <= SMEM, "epilogue staging");
+    __shared__ __attribute__((aligned(16))) char smem[SMEM];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -189,22 +189,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     ke = ke < kmax ? ke : kmax;
     const int nk = ke > kb ? (ke - kb + BK - 1) / BK : 0;
 
-    using OA = Operand<T, TM, AKC>;
-    using OB = Operand<T, TN, BKC>;
     OA A;
     OB B;
-    A.init(g.a, g.ld_a, i0, AKC ? g.M : g.mp, g.kp, AKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wi);
-    B.init(g.b, g.ld_b, j0, BKC ? g.N : g.np, g.kp, BKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wj);
-    constexpr int NLD = OA::NLD + OB::NLD;  // load instructions a wave issues per slice
-
-    auto dma_stage = [&](int kt, char* S) {
-        const auto sa = A.slice(kb + kt * BK);
-        const auto sb = B.slice(kb + kt * BK);
-#pragma unroll
-        for (int q = 0; q < OA::NLD; ++q) A.load(sa, S, q);
-#pragma unroll
-        for (int q = 0; q < OB::NLD; ++q) B.load(sb, S + BOFF, q);
-    };
+    A.init(g.a, g.ld_a, i0, AKC ? g.M : g.mp, g.kp, kb, AKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wi);
+    B.init(g.b, g.ld_b, j0, BKC ? g.N : g.np, g.kp, kb, BKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wj);
 
     f32x16 acc[FRI][FRJ];
 #pragma unroll
@@ -214,21 +202,23 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
 
-    typename V8<T>::type pf[2][FRI], qf[2][FRJ];
-    auto read_frags = [&](const char* S, int ks) {
+    typename V8<T>::type pf[2][FRI], qf[NKS][FRJ];
+    auto read_a = [&](const char* S, int ks) {
 #pragma unroll
-        for (int f = 0; f < FRJ; ++f) qf[ks][f] = B.read(S + BOFF, ks, f);
+        for (int f = 0; f < FRI; ++f) pf[ks & 1][f] = A.read(S, ks, f);
+    };
+    auto read_b = [&](const char* S, int ks) {
 #pragma unroll
-        for (int f = 0; f < FRI; ++f) pf[ks][f] = A.read(S, ks, f);
+        for (int f = 0; f < FRJ; ++f) qf[ks][f] = B.read(S, ks, f);
     };
     auto products = [&](int ks, int f0, int f1) {
 #pragma unroll
         for (int fi = f0; fi < f1; ++fi)
 #pragma unroll
-            for (int fj = 0; fj < FRJ; ++fj) acc[fi][fj] = mfma<T>(qf[ks][fj], pf[ks][fi], acc[fi][fj]);
+            for (int fj = 0; fj < FRJ; ++fj) acc[fi][fj] = mfma<T>(qf[ks][fj], pf[ks & 1][fi], acc[fi][fj]);
     };
-    constexpr int NREAD = (AKC ? 1 : 2) * FRI + (BKC ? 1 : 2) * FRJ;  // LDS reads of a k16 half
-    // one matrix instruction, then its share of N LDS reads
+    constexpr int RA = (AKC ? 1 : 2) * FRI, RB = (BKC ? 1 : 2) * FRJ;  // LDS reads of a k16 step
+    // M matrix instructions with N LDS reads spread over them
     auto interleave = [&](auto n_c, auto m_c) {
         constexpr int N = decltype(n_c)::value, M = decltype(m_c)::value;
         static_for<0, M>([&](auto i_c) {
@@ -238,39 +228,54 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             if constexpr (R > 0) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
         });
     };
+    using CM = std::integral_constant<int, FRI * FRJ>;
+    using CH = std::integral_constant<int, FRI * FRJ / 2>;
 
     if (nk > 0) {
-        char* cur = smem;                   // slice kt
-        char* nxt = smem + STAGE;           // slice kt + 1
-        char* fre = smem + DIST * STAGE;    // the buffer of slice kt - 1, for slice kt + DIST
-#pragma unroll
-        for (int k = 0; k < DIST; ++k) dma_stage(k, smem + k * STAGE);
-        wait_vm<(DIST - 1) * NLD>();
+        const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)smem;
+        char* const SB = smem + 2 * OA::BYTES;
+        A.load(lds0);
+        B.load(lds0 + 2 * OA::BYTES);
+        wait_vm0();
         __syncthreads();
-        read_frags(cur, 0);
-        // S, N and F are distinct buffers, and the loads into F are invisible
-        // to the compiler: the explicit waits and barriers order the ring
-        auto slice = [&](const char* __restrict__ S, const char* __restrict__ N, char* __restrict__ F, int kt)
-                         __attribute__((always_inline)) {
-            dma_stage(kt + DIST, F);
-            read_frags(S, 1);
-            products(0, 0, FRI);
-            interleave(std::integral_constant<int, NREAD>{}, std::integral_constant<int, FRI * FRJ>{});
-            products(1, 0, FRI / 2);
+        read_b(SB, 0);
+        read_a(smem, 0);
+        // One slice: its A tile in S (its B tile in SB), the next slice's A
+        // tile coming into N. The loads are invisible to the compiler; the
+        // waits and barriers here order them.
+        auto slice = [&](const char* __restrict__ S, const char* __restrict__ N, const char* __restrict__ Q,
+                         uint32_t ldsN) __attribute__((always_inline)) {
+            A.load(ldsN);  // every wave had read this buffer before the last barrier
             __builtin_amdgcn_sched_barrier(0);
-            wait_vm<(DIST - 1) * NLD>();  // slice kt + 1 has landed
+            read_b(Q, 1);
+            read_b(Q, 2);
+            read_b(Q, 3);
+            read_a(S, 1);
+            products(0, 0, FRI);
+            interleave(std::integral_constant<int, 3 * RB + RA>{}, CM{});
+            __builtin_amdgcn_sched_barrier(0);
+            __syncthreads();  // every wave holds the slice's B fragments
+            B.load(lds0 + 2 * OA::BYTES);
+            __builtin_amdgcn_sched_barrier(0);
+            read_a(S, 2);
+            products(1, 0, FRI);
+            interleave(std::integral_constant<int, RA>{}, CM{});
+            read_a(S, 3);
+            products(2, 0, FRI);
+            interleave(std::integral_constant<int, RA>{}, CM{});
+            products(3, 0, FRI / 2);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vm0();  // the next slice has landed
             __syncthreads();
-            read_frags(N, 0);
-            products(1, FRI / 2, FRI);
-            interleave(std::integral_constant<int, NREAD>{}, std::integral_constant<int, FRI * FRJ / 2>{});
+            read_b(Q, 0);
+            read_a(N, 0);
+            products(3, FRI / 2, FRI);
+            interleave(std::integral_constant<int, RA + RB>{}, CH{});
         };
-        for (int kt = 0; kt < nk; ++kt) {
-            slice(cur, nxt, fre, kt);
-            cur = nxt;
-            nxt = nxt == smem + (NBUF - 1) * STAGE ? smem : nxt + STAGE;
-            fre = fre == smem + (NBUF - 1) * STAGE ? smem : fre + STAGE;
+        for (int kt = 0; kt < nk; kt += 2) {
+            slice(smem, smem + OA::BYTES, SB, lds0 + OA::BYTES);
+            if (kt + 1 < nk) slice(smem + OA::BYTES, smem, SB, lds0);
         }
-        wait_vm0();  // the loads past the end
     }
     __syncthreads();
 
@@ -429,15 +434,15 @@ __global__ __launch_bounds__(256) void k_colsum_join(const float* __restrict__ p
     db[c] = accumulate ? db[c] + s : s;
 }
 
-template <typename T, int TM, int NBUF>
+template <typename T, int TM>
 hipError_t gemm_t(const GemmArgs& g, bool a_kc, bool b_kc, hipStream_t st) {
     const int grid = g.tiles_m * g.tiles_n * g.splits;
     if (a_kc && b_kc)
-        k_gemm<T, TM, 128, NBUF, true, true><<<grid, 256, 0, st>>>(g);
+        k_gemm<T, TM, 128, true, true><<<grid, 256, 0, st>>>(g);
     else if (a_kc)
-        k_gemm<T, TM, 128, NBUF, true, false><<<grid, 256, 0, st>>>(g);
+        k_gemm<T, TM, 128, true, false><<<grid, 256, 0, st>>>(g);
     else
-        k_gemm<T, TM, 128, NBUF, false, false><<<grid, 256, 0, st>>>(g);
+        k_gemm<T, TM, 128, false, false><<<grid, 256, 0, st>>>(g);
     return hipGetLastError();
 }
 
@@ -445,8 +450,8 @@ hipError_t gemm_t(const GemmArgs& g, bool a_kc, bool b_kc, hipStream_t st) {
 
 hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int dtype, hipStream_t st) {
     if (dtype == 0)
-        return tile_m == 256 ? gemm_t<bf16, 256, 3>(g, a_kc, b_kc, st) : gemm_t<bf16, 128, 4>(g, a_kc, b_kc, st);
-    return tile_m == 256 ? gemm_t<f16, 256, 3>(g, a_kc, b_kc, st) : gemm_t<f16, 128, 4>(g, a_kc, b_kc, st);
+        return tile_m == 256 ? gemm_t<bf16, 256>(g, a_kc, b_kc, st) : gemm_t<bf16, 128>(g, a_kc, b_kc, st);
+    return tile_m == 256 ? gemm_t<f16, 256>(g, a_kc, b_kc, st) : gemm_t<f16, 128>(g, a_kc, b_kc, st);
 }
 
 hipError_t launch_gemm_reduce(const GemmArgs& g, int dtype, hipStream_t st) {

@@ -161,7 +161,7 @@ muon::GemmPlan choose_plan(int64_t M, int64_t N, int64_t K) {
         const int64_t tiles = ((M + tm - 1) / tm) * ((N + muon::kGemmTileN - 1) / muon::kGemmTileN);
         // two workgroups share a CU. Clocks: a slice's matrix work, and what a
         // workgroup spends outside its main loop
-        const double slots = 512, per_slice = tm == 256 ? 1400 : 900, fixed = tm == 256 ? 14000 : 7000;
+        const double slots = 512, per_slice = tm == 256 ? 2800 : 1800, fixed = tm == 256 ? 14000 : 7000;
         for (int s = 1; s <= 64; ++s) {
             if (s > 1 && (s > slices || tiles * s > 2 * slots)) break;
             const int64_t per = (slices + s - 1) / s;

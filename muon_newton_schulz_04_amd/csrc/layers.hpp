@@ -45,7 +45,7 @@ struct GemmArgs {
     Epilogue epi;
 };
 
-constexpr int kGemmSlice = 32;   // K per pipeline stage
+constexpr int kGemmSlice = 64;   // K per pipeline stage
 constexpr int kGemmTileN = 128;
 
 struct GemmPlan {
