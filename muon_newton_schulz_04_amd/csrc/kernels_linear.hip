@@ -148,25 +148,45 @@ struct Operand {
     }
 };
 
-// blockIdx -> (tile row, tile column, split). Workgroups go round-robin over
-// the 8 XCDs, so each XCD takes one contiguous run of the order in which
-// tiles of 8 tile rows at a time walk down the columns: the tiles an XCD
-// works on at once share their operand panels in its L2.
-__device__ __forceinline__ void tile_of(int b, int total, int tm, int tn, int& ti, int& tj, int& sp) {
+// Workgroups go round-robin over the 8 XCDs: of `total` of them, each XCD takes
+// one contiguous run of the logical order, so what it works on at once shares
+// operand panels in its L2.
+__device__ __forceinline__ int per_xcd(int b, int total) {
     const int x = b & 7, i = b >> 3, q = total >> 3, r = total & 7;
-    int l = x * q + (x < r ? x : r) + i;
-    const int tiles = tm * tn;
-    sp = l / tiles;
-    l -= sp * tiles;
-    const int per = 8 * tn;
+    return x * q + (x < r ? x : r) + i;
+}
+
+// Tile l in the order of groups of kGroup tile rows that walk along the columns.
+constexpr int kGroup = 4;
+__device__ __forceinline__ void tile_at(const GemmArgs& g, int l, int& ti, int& tj) {
+    const int per = kGroup * g.tiles_n;
     const int grp = l / per;
-    const int rows = tm - grp * 8 < 8 ? tm - grp * 8 : 8;
+    const int rows = g.tiles_m - grp * kGroup < kGroup ? g.tiles_m - grp * kGroup : kGroup;
     l -= grp * per;
-    ti = grp * 8 + l % rows;
+    ti = grp * kGroup + l % rows;
     tj = l / rows;
 }
 
-template <typename T, int TM, int TN, bool AKC, bool BKC>
+// v + the sum of a fragment's 8 elements
+__device__ __forceinline__ float add8(bf16x8 f, float v) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 one = {(bf16)1.f, (bf16)1.f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v = __builtin_amdgcn_fdot2_f32_bf16(bf16x2{f[2 * e], f[2 * e + 1]}, one, v, false);
+    return v;
+}
+__device__ __forceinline__ float add8(f16x8 f, float v) {
+    typedef f16 f16x2 __attribute__((ext_vector_type(2)));
+    const f16x2 one = {(f16)1.f, (f16)1.f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v = __builtin_amdgcn_fdot2(f16x2{f[2 * e], f[2 * e + 1]}, one, v, false);
+    return v;
+}
+
+// SUM: also the sums over k of the B (1) or A (2) operand's rows, for the bias
+// gradient: two-element dot products with 1 on the fragments in registers, in
+// the shadow of the matrix instructions.
+template <typename T, int TM, int TN, bool AKC, bool BKC, int SUM>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm(const GemmArgs g) {
     using OA = Operand<T, TM, AKC>;
     using OB = Operand<T, TN, BKC>;
@@ -180,14 +200,27 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wi = wave >> 1, wj = wave & 1;
-    int ti, tj, sp;
-    tile_of(blockIdx.x, gridDim.x, g.tiles_m, g.tiles_n, ti, tj, sp);
-    const int i0 = ti * TM, j0 = tj * TN;
+    // a whole tile, or piece number `piece` (-1: none): all split tiles' first
+    // K runs come before their second ones, so that pieces running at the same
+    // time share operand panels
+    const int b = blockIdx.x;
+    int tile, piece = -1, s0 = 0, nk = g.slices;
+    if (b < g.whole) {
+        tile = per_xcd(b, g.whole);
+    } else {
+        const int split = g.tiles_m * g.tiles_n - g.whole;
+        piece = per_xcd(b - g.whole, gridDim.x - g.whole);
+        tile = g.whole + piece % split;
+        s0 = piece / split * g.per;
+        nk = g.slices - s0 < g.per ? g.slices - s0 : g.per;
+    }
     const int kmax = AKC || BKC ? g.kp : g.K;
-    const int kb = sp * g.slices * BK;
-    int ke = kb + g.slices * BK;
+    int ti, tj;
+    tile_at(g, tile, ti, tj);
+    const int i0 = ti * TM, j0 = tj * TN;
+    const int kb = s0 * BK;
+    int ke = kb + nk * BK;
     ke = ke < kmax ? ke : kmax;
-    const int nk = ke > kb ? (ke - kb + BK - 1) / BK : 0;
 
     OA A;
     OB B;
@@ -228,10 +261,21 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             if constexpr (R > 0) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
         });
     };
+    constexpr int NSUM = SUM == 1 ? FRJ : SUM == 2 ? FRI : 1;
+    float sums[NSUM];
+#pragma unroll
+    for (int f = 0; f < NSUM; ++f) sums[f] = 0.f;
+    auto add_sums = [&](int ks) {
+#pragma unroll
+        for (int f = 0; f < NSUM; ++f) {
+            if constexpr (SUM == 1) sums[f] = add8(qf[ks][f], sums[f]);
+            if constexpr (SUM == 2) sums[f] = add8(pf[ks & 1][f], sums[f]);
+        }
+    };
     using CM = std::integral_constant<int, FRI * FRJ>;
     using CH = std::integral_constant<int, FRI * FRJ / 2>;
 
-    if (nk > 0) {
+    {
         const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)smem;
         char* const SB = smem + 2 * OA::BYTES;
         A.load(lds0);
@@ -252,6 +296,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             read_b(Q, 3);
             read_a(S, 1);
             products(0, 0, FRI);
+            add_sums(0);
             interleave(std::integral_constant<int, 3 * RB + RA>{}, CM{});
             __builtin_amdgcn_sched_barrier(0);
             __syncthreads();  // every wave holds the slice's B fragments
@@ -259,11 +304,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             __builtin_amdgcn_sched_barrier(0);
             read_a(S, 2);
             products(1, 0, FRI);
+            add_sums(1);
             interleave(std::integral_constant<int, RA>{}, CM{});
             read_a(S, 3);
             products(2, 0, FRI);
+            add_sums(2);
             interleave(std::integral_constant<int, RA>{}, CM{});
             products(3, 0, FRI / 2);
+            add_sums(3);
             __builtin_amdgcn_sched_barrier(0);
             wait_vm0();  // the next slice has landed
             __syncthreads();
@@ -294,7 +342,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const bool in = col < g.N;
     const int64_t ccol = in ? col : 0;
     const int row0 = i0 + wi * WM + rr;
-    const bool direct = g.direct != 0;
+    const bool direct = piece < 0;
+    float* const part = g.partial + (int64_t)piece * (TM * TN);
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (direct && g.epi.bias) load8(g.epi.bias + ccol, 8, false, bias);
     Inputs<T> cin[NP], nin[NP];
@@ -339,8 +388,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
                     float v[8] = {lo[0], lo[1], lo[2], lo[3], up[0], up[1], up[2], up[3]};
                     finish8<T>(g.epi, row, col, 8, true, v, bias, cin[it]);
                 } else {
-                    // ld_p is N rounded up to 8: whole chunks
-                    float* p = g.partial + ((int64_t)sp * g.M + row) * g.ld_p + col;
+                    float* p = part + (row - i0) * TN + (col - j0);
                     *reinterpret_cast<f32x4*>(p) = lo;
                     *reinterpret_cast<f32x4*>(p + 4) = up;
                 }
@@ -349,32 +397,76 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
     }
+    if constexpr (SUM != 0) {
+        // one tile of each row or column of tiles, spread over them, and the
+        // two waves that hold it all
+        const bool mine = SUM == 1 ? ti == tj % g.tiles_m && wi == 0 : tj == ti % g.tiles_n && wj == 0;
+        if (mine) {
+#pragma unroll
+            for (int f = 0; f < NSUM; ++f) {
+                const float v = sums[f] + __shfl_xor(sums[f], 32, 64);
+                const int at = (SUM == 1 ? wj * WN : wi * WM) + 32 * f + l32;
+                const int n = (SUM == 1 ? j0 : i0) + at;
+                if (hi == 0 && n < (SUM == 1 ? g.N : g.M)) {
+                    if (direct)
+                        g.sums[n] = g.epi.accumulate ? g.sums[n] + v : v;
+                    else
+                        g.sum_part[(int64_t)piece * 256 + at] = v;
+                }
+            }
+        }
+    }
 }
 
-// The splits' partial tiles added in order, then the epilogue.
-template <typename T>
-__global__ __launch_bounds__(256) void k_gemm_reduce(const GemmArgs g) {
-    const int cpr = g.ld_p / 8;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row = id / cpr;
-    if (row >= g.M) return;
-    const int col = (int)(id - row * cpr) * 8;
-    const float* p = g.partial + row * g.ld_p + col;
-    const int64_t stride = (int64_t)g.M * g.ld_p;
+// The pieces of each split tile added in order, then the epilogue: GS
+// neighbouring lanes share a chunk of 8 outputs, each adding a run of pieces.
+template <typename T, int TM, int GS, int SUM>
+__global__ __launch_bounds__(256) void k_gemm_join(const GemmArgs g) {
+    constexpr int TN = kGemmTileN;
+    constexpr int PER = 256 / GS;                 // chunks a block takes
+    constexpr int BLOCKS = TM * (TN / 8) / PER;   // blocks per tile
+    const int t = blockIdx.x / BLOCKS, sub = blockIdx.x % BLOCKS;
+    const int split = g.tiles_m * g.tiles_n - g.whole;
+    int ti, tj;
+    tile_at(g, g.whole + t, ti, tj);
+    if (SUM != 0 && sub == 0 && (SUM == 1 ? ti == tj % g.tiles_m : tj == ti % g.tiles_n)) {
+        const int at = threadIdx.x, n = (SUM == 1 ? tj * TN : ti * TM) + at;
+        if (at < (SUM == 1 ? TN : TM) && n < (SUM == 1 ? g.N : g.M)) {
+            float v = 0.f;
+            for (int s = 0; s < g.splits; ++s) v += g.sum_part[((int64_t)s * split + t) * 256 + at];
+            g.sums[n] = g.epi.accumulate ? g.sums[n] + v : v;
+        }
+    }
+    const int id = sub * PER + threadIdx.x / GS, part = threadIdx.x % GS;
+    const int64_t row = (int64_t)ti * TM + id / (TN / 8);
+    const int col = tj * TN + id % (TN / 8) * 8;
+    if (row >= g.M || col >= g.N) return;  // all GS lanes of a chunk alike
+    const int run = (g.splits + GS - 1) / GS;
+    const int sa = part * run, sb = sa + run < g.splits ? sa + run : g.splits;
+    const float* p = g.partial + (int64_t)t * (TM * TN) + id * 8;
+    const int64_t stride = (int64_t)split * (TM * TN);
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int s = 0; s < g.splits; ++s) {
-        float t[8];
-        load8(p + s * stride, 8, true, t);
+    for (int s = sa; s < sb; ++s) {
+        float u[8];
+        load8(p + s * stride, 8, true, u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += t[e];
+        for (int e = 0; e < 8; ++e) v[e] += u[e];
     }
+    if constexpr (GS > 1) {
+#pragma unroll
+        for (int off = 1; off < GS; off <<= 1)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += __shfl_xor(v[e], off, 64);
+        if (part) return;
+    }
+    const int left = g.N - col;
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (g.epi.bias) load8(g.epi.bias + col, g.N - col, false, bias);
-    const bool vec = g.N - col >= 8 && g.epi.vec;
+    if (g.epi.bias) load8(g.epi.bias + col, left, false, bias);
+    const bool vec = left >= 8 && g.epi.vec;
     Inputs<T> in;
     if (vec) in.fetch(g.epi, row, col);
-    finish8<T>(g.epi, row, col, g.N - col, vec, v, bias, in);
+    finish8<T>(g.epi, row, col, left, vec, v, bias, in);
 }
 
 // Rows of any alignment and length to 16-byte aligned, zero-padded ones: one
@@ -392,76 +484,53 @@ __global__ __launch_bounds__(256) void k_pack(const uint16_t* __restrict__ src, 
     }
 }
 
-// Column sums of a 16-bit matrix whose rows are 16-byte aligned and a
-// multiple of 8 long: a block takes 256 columns (32 lanes x 8) of a run of
-// rows, 8 rows at a time, and writes one partial row.
-template <typename T>
-__global__ __launch_bounds__(256) void k_colsum(const T* __restrict__ dy, int64_t ld, int64_t rows, int cols,
-                                                int64_t per, float* __restrict__ part) {
-    __shared__ float red[8][32][9];
-    const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
-    const int c = blockIdx.x * 256 + lane * 8;
-    const int64_t r0 = blockIdx.y * per;
-    const int64_t r1 = r0 + per < rows ? r0 + per : rows;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (c < cols) {
-#pragma unroll 4
-        for (int64_t r = r0 + rl; r < r1; r += 8) {
-            float t[8];
-            load8(dy + r * ld + c, 8, true, t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += t[e];
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) red[rl][lane][e] = v[e];
-    __syncthreads();
-    const int l = threadIdx.x >> 3, e = threadIdx.x & 7;
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s += red[k][l][e];
-    const int cc = blockIdx.x * 256 + l * 8 + e;
-    if (cc < cols) part[(int64_t)blockIdx.y * cols + cc] = s;
-}
-
-__global__ __launch_bounds__(256) void k_colsum_join(const float* __restrict__ part, int blocks, int cols, int n,
-                                                     float* __restrict__ db, int accumulate) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= n) return;
-    float s = 0.f;
-#pragma unroll 8
-    for (int b = 0; b < blocks; ++b) s += part[(int64_t)b * cols + c];
-    db[c] = accumulate ? db[c] + s : s;
-}
-
 template <typename T, int TM>
-hipError_t gemm_t(const GemmArgs& g, bool a_kc, bool b_kc, hipStream_t st) {
-    const int grid = g.tiles_m * g.tiles_n * g.splits;
+hipError_t gemm_t(const GemmArgs& g, bool a_kc, bool b_kc, int sum, hipStream_t st) {
+    const int wgs = g.whole + (g.tiles_m * g.tiles_n - g.whole) * g.splits;
     if (a_kc && b_kc)
-        k_gemm<T, TM, 128, true, true><<<grid, 256, 0, st>>>(g);
+        k_gemm<T, TM, 128, true, true, 0><<<wgs, 256, 0, st>>>(g);
     else if (a_kc)
-        k_gemm<T, TM, 128, true, false><<<grid, 256, 0, st>>>(g);
+        k_gemm<T, TM, 128, true, false, 0><<<wgs, 256, 0, st>>>(g);
+    else if (sum == 0)
+        k_gemm<T, TM, 128, false, false, 0><<<wgs, 256, 0, st>>>(g);
+    else if (sum == 1)
+        k_gemm<T, TM, 128, false, false, 1><<<wgs, 256, 0, st>>>(g);
     else
-        k_gemm<T, TM, 128, false, false><<<grid, 256, 0, st>>>(g);
+        k_gemm<T, TM, 128, false, false, 2><<<wgs, 256, 0, st>>>(g);
+    return hipGetLastError();
+}
+
+template <typename T, int TM, int GS>
+void join_gs(const GemmArgs& g, int sum, hipStream_t st) {
+    const int grid = (g.tiles_m * g.tiles_n - g.whole) * (TM * 16 * GS / 256);
+    if (sum == 0)
+        k_gemm_join<T, TM, GS, 0><<<grid, 256, 0, st>>>(g);
+    else if (sum == 1)
+        k_gemm_join<T, TM, GS, 1><<<grid, 256, 0, st>>>(g);
+    else
+        k_gemm_join<T, TM, GS, 2><<<grid, 256, 0, st>>>(g);
+}
+template <typename T, int TM>
+hipError_t join_t(const GemmArgs& g, int sum, hipStream_t st) {
+    // four lanes a chunk for eight pieces or more
+    if (g.splits >= 8)
+        join_gs<T, TM, 4>(g, sum, st);
+    else
+        join_gs<T, TM, 1>(g, sum, st);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int dtype, hipStream_t st) {
+hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int dtype, int sum, hipStream_t st) {
     if (dtype == 0)
-        return tile_m == 256 ? gemm_t<bf16, 256>(g, a_kc, b_kc, st) : gemm_t<bf16, 128>(g, a_kc, b_kc, st);
-    return tile_m == 256 ? gemm_t<f16, 256>(g, a_kc, b_kc, st) : gemm_t<f16, 128>(g, a_kc, b_kc, st);
+        return tile_m == 256 ? gemm_t<bf16, 256>(g, a_kc, b_kc, sum, st) : gemm_t<bf16, 128>(g, a_kc, b_kc, sum, st);
+    return tile_m == 256 ? gemm_t<f16, 256>(g, a_kc, b_kc, sum, st) : gemm_t<f16, 128>(g, a_kc, b_kc, sum, st);
 }
 
-hipError_t launch_gemm_reduce(const GemmArgs& g, int dtype, hipStream_t st) {
-    const int64_t n = (int64_t)g.M * (g.ld_p / 8);
-    const unsigned grid = (unsigned)((n + 255) / 256);
-    if (dtype == 0)
-        k_gemm_reduce<bf16><<<grid, 256, 0, st>>>(g);
-    else
-        k_gemm_reduce<f16><<<grid, 256, 0, st>>>(g);
-    return hipGetLastError();
+hipError_t launch_gemm_join(const GemmArgs& g, int tile_m, int dtype, int sum, hipStream_t st) {
+    if (dtype == 0) return tile_m == 256 ? join_t<bf16, 256>(g, sum, st) : join_t<bf16, 128>(g, sum, st);
+    return tile_m == 256 ? join_t<f16, 256>(g, sum, st) : join_t<f16, 128>(g, sum, st);
 }
 
 hipError_t launch_pack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t cols_pad,
@@ -471,31 +540,6 @@ hipError_t launch_pack(const void* src, int64_t ld, int64_t rows, int64_t cols, 
     const int64_t blocks = (n + 255) / 256;
     k_pack<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(static_cast<const uint16_t*>(src), ld, rows,
                                                                         cols, static_cast<uint4*>(dst), cols_pad / 8);
-    return hipGetLastError();
-}
-
-int colsum_blocks(int64_t rows, int64_t cols) {
-    // about 1024 blocks in all, each at least 64 rows
-    const int64_t cb = (cols + 255) / 256;
-    int64_t b = (1024 + cb - 1) / cb;
-    const int64_t most = (rows + 63) / 64;
-    if (b > most) b = most;
-    return (int)(b < 1 ? 1 : b);
-}
-
-hipError_t launch_colsum(const void* dy, int64_t ld, int64_t rows, int64_t cols, int dtype, float* part, float* db,
-                         int accumulate, hipStream_t st) {
-    const int64_t cp = (cols + 7) / 8 * 8;
-    const int blocks = colsum_blocks(rows, cols);
-    const int64_t per = (rows + blocks - 1) / blocks;
-    const dim3 grid((unsigned)((cp + 255) / 256), (unsigned)blocks);
-    if (dtype == 0)
-        k_colsum<bf16><<<grid, 256, 0, st>>>(static_cast<const bf16*>(dy), ld, rows, (int)cp, per, part);
-    else
-        k_colsum<f16><<<grid, 256, 0, st>>>(static_cast<const f16*>(dy), ld, rows, (int)cp, per, part);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    k_colsum_join<<<(unsigned)((cols + 255) / 256), 256, 0, st>>>(part, blocks, (int)cp, (int)cols, db, accumulate);
     return hipGetLastError();
 }
 

@@ -152,27 +152,50 @@ Tensor tensor_w(const muon_linear& d, const void* p, int size) {
     return {p, r, c, d.ld_w ? d.ld_w : c, size};
 }
 
-// The tile and the number of K splits for an M x N x K product.
-muon::GemmPlan choose_plan(int64_t M, int64_t N, int64_t K) {
-    const int64_t slices = (K + muon::kGemmSlice - 1) / muon::kGemmSlice;
-    muon::GemmPlan best{128, 1, (int)(slices > 0 ? slices : 1)};
+// How an M x N x K product is cut: tile height, how many tiles run whole, and
+// in how many K pieces the others go. Each candidate is priced in clocks (2.4
+// GHz): slice costs of a workgroup alone on its CU and beside a second one,
+// what it spends outside its main loop, the join's traffic and launch, and
+// the rate at which the whole chip multiplies however it is filled.
+// direct: whole tiles can be finished by the product kernel.
+muon::GemmPlan choose_plan(int64_t M, int64_t N, int64_t K, bool direct) {
+    int64_t slices = (K + muon::kGemmSlice - 1) / muon::kGemmSlice;
+    if (slices < 1) slices = 1;
+    muon::GemmPlan best{};
     double best_t = 1e300;
     for (int tm : {256, 128}) {
-        const int64_t tiles = ((M + tm - 1) / tm) * ((N + muon::kGemmTileN - 1) / muon::kGemmTileN);
-        // two workgroups share a CU. Clocks: a slice's matrix work, and what a
-        // workgroup spends outside its main loop
-        const double slots = 512, per_slice = tm == 256 ? 2800 : 1800, fixed = tm == 256 ? 14000 : 7000;
-        for (int s = 1; s <= 64; ++s) {
-            if (s > 1 && (s > slices || tiles * s > 2 * slots)) break;
+        const int64_t tiles_m = (M + tm - 1) / tm, tiles_n = (N + muon::kGemmTileN - 1) / muon::kGemmTileN;
+        const int64_t tiles = tiles_m * tiles_n;
+        const double alone = tm == 256 ? 2100 : 1300, beside = tm == 256 ? 3500 : 2200,
+                     fixed = tm == 256 ? 9000 : 6000;
+        const double chip = (double)tiles * (double)slices * (tm == 256 ? 8.8 : 5.5);
+        auto rounds = [&](int64_t wgs, double per) {
+            const int64_t rest = wgs % 512;
+            return (double)(wgs / 512) * (per * beside + fixed) +
+                   (rest == 0 ? 0.0 : per * (rest > 256 ? beside : alone) + fixed);
+        };
+        auto consider = [&](double t, int64_t whole, int64_t splits, int64_t per) {
+            if (t < chip) t = chip;
+            if (whole < tiles)
+                t += 8.0 * (double)((tiles - whole) * splits) * (double)(M < tm ? M : tm) * 128.0 / 2300.0 + 7000.0;
+            if (t >= best_t) return;
+            best_t = t;
+            best = {tm, (int)tiles_m, (int)tiles_n, (int)slices, (int)whole, (int)splits, (int)per};
+        };
+        if (direct)
+            consider(rounds(tiles, (double)slices), tiles, 1, slices);
+        else
+            consider(rounds(tiles, (double)slices), 0, 1, slices);
+        for (int64_t s = 2; s <= 64 && s <= slices; ++s) {
             const int64_t per = (slices + s - 1) / s;
-            if (s > 1 && (slices + per - 1) / per != s) continue;  // every split has work
-            double t = std::ceil((double)tiles * s / slots) * ((double)per * per_slice + fixed);
-            // partial tiles out and in (float32, about 1700 bytes a clock) and one more launch
-            if (s > 1) t += 8.0 * (double)M * (double)N * s / 1700.0 + 6000.0;
-            if (t < best_t) {
-                best_t = t;
-                best = {tm, s, (int)(per > 0 ? per : 1)};
-            }
+            if ((slices + per - 1) / per != s) continue;  // every piece has work
+            if (tiles * s <= 1024) consider(rounds(tiles * s, (double)per), 0, s, per);
+            // one tile a CU and the rest of a round in pieces beside them
+            const int64_t rest = tiles % 512 - 256, n = (rest * s + 255) / 256;
+            if (direct && rest > 0 && n * per <= slices)
+                consider((double)(tiles / 512) * ((double)slices * beside + fixed) + (double)(n * per) * beside +
+                             (double)(slices - n * per) * alone + 2 * fixed,
+                         tiles - rest, s, per);
         }
     }
     return best;
@@ -183,10 +206,9 @@ struct Product {
     int64_t M, N, K;
     Tensor a, b;
     bool a_kc, b_kc;  // k is the contiguous index
-    bool direct;
     bool pack_a, pack_b;
     muon::GemmPlan plan;
-    size_t off_a, off_b, off_part, off_cols, bytes;
+    size_t off_a, off_b, off_part, off_sums, bytes;
 };
 
 bool needs_pack(const Tensor& t) { return t.rows > 0 && (!aligned16(t.p, t.ld, 2) || t.cols % 8 != 0); }
@@ -198,39 +220,39 @@ muon_status plan_product(const muon_linear& d, int op, const void* pa, const voi
                          Product* P) {
     const bool io = d.weight_layout == MUON_WEIGHT_IN_OUT;
     if (op == MUON_LINEAR_FORWARD) {
-        *P = {d.tokens, d.out_features, d.in_features, tensor_x(d, pa), tensor_w(d, pb, 2), true, !io, false};
+        *P = {d.tokens, d.out_features, d.in_features, tensor_x(d, pa), tensor_w(d, pb, 2), true, !io};
     } else if (op == MUON_LINEAR_GRAD_INPUT) {
-        *P = {d.tokens, d.in_features, d.out_features, tensor_y(d, pa), tensor_w(d, pb, 2), true, io, false};
+        *P = {d.tokens, d.in_features, d.out_features, tensor_y(d, pa), tensor_w(d, pb, 2), true, io};
     } else {
         const Tensor x = tensor_x(d, pa), dy = tensor_y(d, pb);
         if (io)
-            *P = {d.in_features, d.out_features, d.tokens, x, dy, false, false, false};
+            *P = {d.in_features, d.out_features, d.tokens, x, dy, false, false};
         else
-            *P = {d.out_features, d.in_features, d.tokens, dy, x, false, false, false};
+            *P = {d.out_features, d.in_features, d.tokens, dy, x, false, false};
     }
     P->pack_a = needs_pack(P->a);
     P->pack_b = needs_pack(P->b);
-    P->plan = choose_plan(P->M, P->N, P->K);
-    const int64_t tm = P->plan.tile_m, tn = muon::kGemmTileN;
-    if (((P->M + tm - 1) / tm) * ((P->N + tn - 1) / tn) >= (int64_t)1 << 23)
+    // launches hold fewer than 2^32 threads
+    if (((P->M + 127) / 128) * ((P->N + 127) / 128) >= (int64_t)1 << (vec && P->N % 8 == 0 ? 22 : 18))
         return fail(MUON_E_SHAPE, "linear: output too large");
-    P->direct = vec && P->N % 8 == 0 && P->plan.splits == 1;
-    if (!P->direct && P->M * (up8(P->N) / 8) >= (int64_t)1 << 32)
-        return fail(MUON_E_SHAPE, "linear: output too large for unaligned or odd-length rows");
+    P->plan = choose_plan(P->M, P->N, P->K, vec && P->N % 8 == 0);
     size_t o = 0;
     P->off_a = o;
     if (P->pack_a) o = up256(o + (size_t)P->a.rows * up8(P->a.cols) * 2);
     P->off_b = o;
     if (P->pack_b) o = up256(o + (size_t)P->b.rows * up8(P->b.cols) * 2);
+    const muon::GemmPlan& G = P->plan;
+    const size_t pieces = (size_t)(G.tiles_m * G.tiles_n - G.whole) * (size_t)G.splits;
     P->off_part = o;
-    if (!P->direct) o = up256(o + (size_t)P->plan.splits * P->M * up8(P->N) * 4);
-    P->off_cols = o;
-    if (dbias) o = up256(o + (size_t)muon::colsum_blocks(d.tokens, d.out_features) * up8(d.out_features) * 4);
+    o = up256(o + pieces * (size_t)(G.tile_m * muon::kGemmTileN) * 4);
+    P->off_sums = o;
+    if (dbias) o = up256(o + pieces * 256 * 4);
     P->bytes = o;
     return MUON_OK;
 }
 
-muon_status run_product(Product& P, int dtype, muon::Epilogue& E, char* ws, hipStream_t st) {
+// sums (bias gradient) and sum: see GemmArgs and launch_gemm
+muon_status run_product(Product& P, int dtype, muon::Epilogue& E, float* sums, int sum, char* ws, hipStream_t st) {
     for (int k = 0; k < 2; ++k) {
         Tensor& t = k ? P.b : P.a;
         if (!(k ? P.pack_b : P.pack_a)) continue;
@@ -239,7 +261,7 @@ muon_status run_product(Product& P, int dtype, muon::Epilogue& E, char* ws, hipS
         t.p = dst;
         t.ld = up8(t.cols);
     }
-    const int tm = P.plan.tile_m, tn = muon::kGemmTileN;
+    const muon::GemmPlan& G = P.plan;
     muon::GemmArgs g{};
     g.a = P.a.p;
     g.b = P.b.p;
@@ -251,16 +273,18 @@ muon_status run_product(Product& P, int dtype, muon::Epilogue& E, char* ws, hipS
     g.kp = (int)((P.a_kc || P.b_kc) ? up8(P.K) : P.K);
     g.mp = (int)up8(P.M);
     g.np = (int)up8(P.N);
-    g.tiles_m = (int)((P.M + tm - 1) / tm);
-    g.tiles_n = (int)((P.N + tn - 1) / tn);
-    g.splits = P.plan.splits;
-    g.slices = P.plan.slices;
-    g.direct = P.direct;
+    g.tiles_m = G.tiles_m;
+    g.tiles_n = G.tiles_n;
+    g.slices = G.slices;
+    g.whole = G.whole;
+    g.splits = G.splits;
+    g.per = G.per;
     g.partial = reinterpret_cast<float*>(ws + P.off_part);
-    g.ld_p = (int)up8(P.N);
+    g.sums = sums;
+    g.sum_part = reinterpret_cast<float*>(ws + P.off_sums);
     g.epi = E;
-    TRY(hip_status(muon::launch_gemm(g, tm, P.a_kc, P.b_kc, dtype, st), "product kernel"));
-    if (!g.direct) TRY(hip_status(muon::launch_gemm_reduce(g, dtype, st), "split join kernel"));
+    TRY(hip_status(muon::launch_gemm(g, G.tile_m, P.a_kc, P.b_kc, dtype, sum, st), "product kernel"));
+    if (G.whole < G.tiles_m * G.tiles_n) TRY(hip_status(muon::launch_gemm_join(g, G.tile_m, dtype, sum, st), "join kernel"));
     return MUON_OK;
 }
 
@@ -332,7 +356,7 @@ muon_status run_layer(const muon_linear* d, int op, const void* a, const void* w
     E.ld_z = Z.ld;
     E.ld_y = Y.ld;
     E.vec = o.vec();
-    return run_product(P, d->dtype, E, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
+    return run_product(P, d->dtype, E, nullptr, 0, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
 }
 
 muon_status check_norm(const muon_layernorm* d) {
@@ -427,15 +451,9 @@ muon_status muon_linear_grad_weight(const muon_linear* d, const void* x, const v
         E.ld_y = W.ld;
         E.vec = o.vec();
         E.accumulate = accumulate != 0;
-        TRY(run_product(P, d->dtype, E, ws, st));
-        if (dbias) {
-            // dy as the product read it (packed or in place)
-            const Tensor& t = d->weight_layout == MUON_WEIGHT_IN_OUT ? P.b : P.a;
-            TRY(hip_status(muon::launch_colsum(t.p, t.ld, d->tokens, d->out_features, d->dtype,
-                                               reinterpret_cast<float*>(ws + P.off_cols), dbias, accumulate != 0, st),
-                           "bias gradient kernels"));
-        }
-        return MUON_OK;
+        // dy is the second operand of an [in, out] gradient, else the first
+        const int sum = !dbias ? 0 : d->weight_layout == MUON_WEIGHT_IN_OUT ? 1 : 2;
+        return run_product(P, d->dtype, E, dbias, sum, ws, st);
     });
 }
 

@@ -38,32 +38,31 @@ struct GemmArgs {
     int32_t M, N, K, kp;
     int32_t mp, np;      // row lengths of operands stored with k outermost (M, N rounded up to 8 when packed)
     int32_t tiles_m, tiles_n;
-    int32_t splits, slices;  // K in `splits` runs of `slices` slices
-    int32_t direct;          // the product kernel does the epilogue (one split, everything moves as whole vectors)
-    float* partial;          // else [splits][M][ld_p]
-    int32_t ld_p;
+    // K is `slices` slices of kGemmSlice. The first `whole` tiles (a multiple
+    // of 8, or all) are one workgroup each, which finishes them; the others
+    // are `splits` pieces of `per` slices each, whose sums meet in the
+    // workspace: piece p belongs to tile whole + p % (tiles - whole).
+    int32_t slices, whole, splits, per;
+    float* partial;   // piece p: [tile_m][kGemmTileN] at index p
+    float* sums;      // bias gradient, or null
+    float* sum_part;  // its pieces: 256 floats at index p
     Epilogue epi;
 };
 
-constexpr int kGemmSlice = 64;   // K per pipeline stage
+constexpr int kGemmSlice = 64;  // K per pipeline stage
 constexpr int kGemmTileN = 128;
 
 struct GemmPlan {
     int tile_m;  // 256 or 128; tiles are 128 wide
-    int splits;
-    int slices;  // per split
+    int tiles_m, tiles_n, slices, whole, splits, per;
 };
 
-hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int dtype, hipStream_t st);
-hipError_t launch_gemm_reduce(const GemmArgs& g, int dtype, hipStream_t st);
+// sum: the bias gradient is the sums over k of neither (0), B's (1) or A's (2) rows
+hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int dtype, int sum, hipStream_t st);
+hipError_t launch_gemm_join(const GemmArgs& g, int tile_m, int dtype, int sum, hipStream_t st);
 // dst [rows, cols_pad] <- src [rows, cols] with row stride ld, zero-padded
 hipError_t launch_pack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t cols_pad,
                        hipStream_t st);
-// db[n] (+)= sum over rows of dy; part: colsum_blocks(rows, cols) x cols_pad floats
-int colsum_blocks(int64_t rows, int64_t cols);
-hipError_t launch_colsum(const void* dy, int64_t ld, int64_t rows, int64_t cols, int dtype, float* part, float* db,
-                         int accumulate, hipStream_t st);
-
 struct NormArgs {
     int64_t rows;
     int32_t cols;
