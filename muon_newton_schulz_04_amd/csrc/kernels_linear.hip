@@ -330,8 +330,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     // ---- epilogue: lane holds C[i][j .. j+3], i = l32, j = 8 g + 4 hi; each
     // wave stages 32 rows at a time in its own LDS region and leaves with 8
     // consecutive columns a lane. What the epilogue reads for a block of 32
-    // rows goes out before the stores of the block before it, whose latency it
-    // would otherwise wait for (loads and stores retire in order). ----
+    // rows goes out two blocks ahead, before the stores of the blocks between,
+    // which it would otherwise wait for (loads and stores retire in order). ----
     char* W = smem + wave * 32 * SROW;
     const int l32 = lane & 31, hi = lane >> 5;
     constexpr int CPR = WN / 8;      // chunks of 8 per staged row
@@ -339,22 +339,25 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     constexpr int NP = 32 / RPI;     // passes per block
     const int ch = lane % CPR, rr = lane / CPR;
     const int col = j0 + wj * WN + ch * 8;
-    const bool in = col < g.N;
-    const int64_t ccol = in ? col : 0;
+    const bool inside = col < g.N;
+    const int64_t ccol = inside ? col : 0;
     const int row0 = i0 + wi * WM + rr;
     const bool direct = piece < 0;
     float* const part = g.partial + (int64_t)piece * (TM * TN);
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (direct && g.epi.bias) load8(g.epi.bias + ccol, 8, false, bias);
-    Inputs<T> cin[NP], nin[NP];
-    auto fetch = [&](int fi, Inputs<T>(&x)[NP]) {
+    uint4 in0[NP], in1[NP], in2[NP];  // this block's, the next one's and the one's after that
+    auto fetch = [&](int fi, uint4(&x)[NP]) {
 #pragma unroll
         for (int it = 0; it < NP; ++it) {
             const int row = row0 + 32 * fi + it * RPI;
-            x[it].fetch(g.epi, row < g.M ? row : g.M - 1, ccol);
+            x[it] = fetch8<T>(g.epi, row < g.M ? row : g.M - 1, ccol);
         }
     };
-    if (direct) fetch(0, nin);
+    if (direct) {
+        fetch(0, in0);
+        fetch(1, in1);
+    }
 #pragma unroll 1
     for (int fi = 0; fi < FRI; ++fi) {
         static_for<0, FRI>([&](auto f_c) {
@@ -373,26 +376,27 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         });
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        if (direct) {
-#pragma unroll
-            for (int it = 0; it < NP; ++it) cin[it] = nin[it];
-            if (fi + 1 < FRI) fetch(fi + 1, nin);
-        }
+        if (direct && fi + 2 < FRI) fetch(fi + 2, in2);
 #pragma unroll
         for (int it = 0; it < NP; ++it) {
             const int row = row0 + 32 * fi + it * RPI;
             const f32x4* s = reinterpret_cast<const f32x4*>(W + (it * RPI + rr) * SROW + 32 * ch);
             const f32x4 lo = s[0], up = s[1];
-            if (row < g.M && in) {
+            if (row < g.M && inside) {
                 if (direct) {
                     float v[8] = {lo[0], lo[1], lo[2], lo[3], up[0], up[1], up[2], up[3]};
-                    finish8<T>(g.epi, row, col, 8, true, v, bias, cin[it]);
+                    finish8<T>(g.epi, row, col, 8, true, v, bias, in0[it]);
                 } else {
                     float* p = part + (row - i0) * TN + (col - j0);
                     *reinterpret_cast<f32x4*>(p) = lo;
                     *reinterpret_cast<f32x4*>(p + 4) = up;
                 }
             }
+        }
+#pragma unroll
+        for (int it = 0; it < NP; ++it) {
+            in0[it] = in1[it];
+            in1[it] = in2[it];
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -464,8 +468,8 @@ __global__ __launch_bounds__(256) void k_gemm_join(const GemmArgs g) {
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (g.epi.bias) load8(g.epi.bias + col, left, false, bias);
     const bool vec = left >= 8 && g.epi.vec;
-    Inputs<T> in;
-    if (vec) in.fetch(g.epi, row, col);
+    uint4 in = {0, 0, 0, 0};
+    if (vec) in = fetch8<T>(g.epi, row, col);
     finish8<T>(g.epi, row, col, left, vec, v, bias, in);
 }
 

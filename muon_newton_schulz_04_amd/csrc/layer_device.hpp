@@ -91,9 +91,34 @@ __device__ __forceinline__ float sigmoid(float x) {
 constexpr float kGeluTwoK = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluCubic = 0.044715f;
 
+// gelu(z) = z Phi(z) with the normal distribution's lower tail as
+// Phi(-a) = e^(-a^2/2) t p(t), t = 1 / (1 + a / 4), a >= 0: p of degree 9 fitted
+// to the scaled complementary error function with equal relative error on
+// t in (0, 1] (3.3e-8; 3.7e-7 evaluated in float32), so the tail keeps its
+// digits. Half the instructions of the library's erfc. `e`: e^(-a^2/2).
+__device__ __forceinline__ float normal_tail(float a, float& e) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.25f, a, 1.f));
+    e = __builtin_amdgcn_exp2f(-0.72134752044448170f * a * a);
+    float p = 0.0198428007f;
+    p = fmaf(p, t, -0.0811460938f);
+    p = fmaf(p, t, 0.0960938974f);
+    p = fmaf(p, t, -0.03221571f);
+    p = fmaf(p, t, 0.0639933433f);
+    p = fmaf(p, t, 0.0588711657f);
+    p = fmaf(p, t, 0.0816244597f);
+    p = fmaf(p, t, 0.0934640081f);
+    p = fmaf(p, t, 0.0997365477f);
+    p = fmaf(p, t, 0.099735565f);
+    return p * t * e;
+}
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+    const float q = normal_tail(fabsf(z), e);
+    return z > 0.f ? 1.f - q : q;
+}
+
 // gelu_tanh(z) = z/2 (1 + tanh u) = z sigmoid(2u), u = sqrt(2/pi) (z + 0.044715 z^3):
 // one exponential and one reciprocal, and no cancellation in the tail, where
-// 1 + tanh u loses its bits. gelu(z) = z erfc(-z / sqrt 2) / 2 for the same reason.
+// 1 + tanh u loses its bits.
 template <int act>
 __device__ __forceinline__ float act_value(float z) {
     switch (act) {
@@ -102,7 +127,10 @@ __device__ __forceinline__ float act_value(float z) {
             const float r = z > 0.f ? z : z * 0.f;
             return r * r;
         }
-        case ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+        case ACT_GELU: {
+            float e;
+            return z * normal_cdf(z, e);
+        }
         case ACT_GELU_TANH: return z * sigmoid(kGeluTwoK * z * fmaf(kGeluCubic * z, z, 1.f));
         case ACT_SILU: return z * sigmoid(z);
         default: return z;
@@ -118,9 +146,11 @@ __device__ __forceinline__ float act_slope(float z) {
     switch (act) {
         case ACT_RELU: return z > 0.f ? 1.f : z != z ? z : 0.f;
         case ACT_RELU2: return z > 0.f ? 2.f * z : z != z ? z : 0.f;
-        case ACT_GELU:
-            return fmaf(zc * 0.3989422804014327f, __builtin_amdgcn_exp2f(-0.72134752044448170f * zc * zc),
-                        0.5f * erfcf(-0.70710678118654752f * z));
+        case ACT_GELU: {
+            float e;
+            const float q = normal_cdf(z, e);
+            return fmaf(zc * 0.3989422804014327f, e, q);
+        }
         case ACT_GELU_TANH: {
             const float q = sigmoid(kGeluTwoK * z * fmaf(kGeluCubic * z, z, 1.f));
             return fmaf(zc * q * (1.f - q) * kGeluTwoK, fmaf(3.f * kGeluCubic * zc, zc, 1.f), q);
@@ -158,25 +188,22 @@ __device__ __forceinline__ void act_slopes(int act, float (&v)[8]) {
 }
 #undef MUON_ACT_CASE
 
-// What the epilogue reads of a chunk of 8 outputs, fetched ahead of its use as
-// 16-byte vectors: add and z (16-bit), or the weight gradient to add to.
+// What the epilogue reads first of a chunk of 8 outputs, fetched ahead of its
+// use as a 16-byte vector: z on the way back through an activation, else add;
+// or half of the weight gradient to add to. (A call with z and add both, and
+// the other half, read the rest in place.)
 template <typename T>
-struct Inputs {
-    uint4 a, z;
-    __device__ __forceinline__ void fetch(const Epilogue& E, int64_t r, int64_t c) {
-        if (E.mode == EPI_GRAD_WEIGHT) {
-            if (E.accumulate) {
-                const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(E.y) + r * E.ld_y + c);
-                a = p[0];
-                z = p[1];
-            }
-            return;
-        }
-        if (E.add) a = *reinterpret_cast<const uint4*>(static_cast<const T*>(E.add) + r * E.ld_add + c);
-        if (E.mode == EPI_GRAD_INPUT && E.act != ACT_NONE)
-            z = *reinterpret_cast<const uint4*>(static_cast<const T*>(E.z) + r * E.ld_z + c);
+__device__ __forceinline__ uint4 fetch8(const Epilogue& E, int64_t r, int64_t c) {
+    const void* p = nullptr;
+    if (E.mode == EPI_GRAD_WEIGHT) {
+        if (E.accumulate) p = static_cast<const float*>(E.y) + r * E.ld_y + c;
+    } else if (E.mode == EPI_GRAD_INPUT && E.act != ACT_NONE) {
+        p = static_cast<const T*>(E.z) + r * E.ld_z + c;
+    } else if (E.add) {
+        p = static_cast<const T*>(E.add) + r * E.ld_add + c;
     }
-};
+    return p ? *reinterpret_cast<const uint4*>(p) : uint4{0, 0, 0, 0};
+}
 
 template <typename T>
 __device__ __forceinline__ void widen8(const uint4& u, float (&v)[8]) {
@@ -187,17 +214,17 @@ __device__ __forceinline__ void widen8(const uint4& u, float (&v)[8]) {
 
 // The epilogue of 8 consecutive accumulators of row r from column c on, n of
 // them inside the matrix. bias: their bias values (forward). vec: all 8 are
-// inside, every row is 16-byte aligned, and `in` holds what is read;
-// otherwise elements are read and written one by one.
+// inside, every row is 16-byte aligned, and `in` is fetch8's; otherwise
+// elements are read and written one by one.
 template <typename T>
 __device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c, int n, bool vec, float (&v)[8],
-                                        const float (&bias)[8], const Inputs<T>& in) {
+                                        const float (&bias)[8], const uint4& in) {
     float t[8];
     if (E.mode == EPI_GRAD_WEIGHT) {
         float* y = static_cast<float*>(E.y) + r * E.ld_y + c;
         if (E.accumulate) {
             if (vec) {
-                const f32x4 lo = __builtin_bit_cast(f32x4, in.a), up = __builtin_bit_cast(f32x4, in.z);
+                const f32x4 lo = __builtin_bit_cast(f32x4, in), up = *reinterpret_cast<const f32x4*>(y + 4);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     t[e] = lo[e];
@@ -212,14 +239,16 @@ __device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c,
         stream8(y, n, vec, v);
         return;
     }
+    bool fetched = false;  // `in` was z, not add
     if (E.mode == EPI_FORWARD) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += bias[e];
         if (E.z) stream8(static_cast<T*>(E.z) + r * E.ld_z + c, n, vec, v);
         act_values(E.act, v);
     } else if (E.act != ACT_NONE) {
+        fetched = true;
         if (vec)
-            widen8<T>(in.z, t);
+            widen8<T>(in, t);
         else
             load8(static_cast<const T*>(E.z) + r * E.ld_z + c, n, false, t);
         act_slopes(E.act, t);
@@ -227,10 +256,10 @@ __device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c,
         for (int e = 0; e < 8; ++e) v[e] *= t[e];
     }
     if (E.add) {
-        if (vec)
-            widen8<T>(in.a, t);
+        if (vec && !fetched)
+            widen8<T>(in, t);
         else
-            load8(static_cast<const T*>(E.add) + r * E.ld_add + c, n, false, t);
+            load8(static_cast<const T*>(E.add) + r * E.ld_add + c, n, vec, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += t[e];
     }
