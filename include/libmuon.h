@@ -321,14 +321,13 @@ typedef struct muon_epilogue {
 } muon_epilogue;
 
 /* Bytes of device workspace (256-byte aligned) the call `op` needs; often 0,
- * and NULL is then accepted. a, b, e, y are the call's own arguments (forward:
- * x, w, e, y; grad input: dy, w, e, dx; grad weight: x, dy, NULL, dw), of
- * whose tensors only addresses and strides are looked at: operands whose rows
- * do not start 16-byte aligned or whose length is no multiple of 8 are first
- * copied to aligned rows in the workspace, and outputs of that kind go through
- * it in float32. Host-only. */
+ * and NULL is then accepted. a, b: the addresses of its two operands (forward:
+ * x, w; grad input: dy, w; grad weight: x, dy), of which only the alignment is
+ * looked at: operands whose rows do not start 16-byte aligned or whose length
+ * is no multiple of 8 are first copied to aligned rows in the workspace.
+ * Host-only. */
 muon_status muon_linear_workspace_bytes(const muon_linear* d, int32_t op, const void* a, const void* b,
-                                        const muon_epilogue* e, const void* y, size_t* out_bytes);
+                                        size_t* out_bytes);
 
 /* Y = act(X W + bias) + add; e NULL: Y = X W. The activation is taken of the
  * unrounded sum. */

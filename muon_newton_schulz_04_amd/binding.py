@@ -186,7 +186,6 @@ _SIGS = {
     "muon_profile_read": (ctypes.c_int, [_P, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64),
                                          ctypes.POINTER(ctypes.c_double)]),
     "muon_linear_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(muon_linear), ctypes.c_int32, _P, _P,
-                                                   ctypes.POINTER(muon_epilogue), _P,
                                                    ctypes.POINTER(ctypes.c_size_t)]),
     "muon_linear_forward": (ctypes.c_int, [ctypes.POINTER(muon_linear), _P, _P, ctypes.POINTER(muon_epilogue), _P, _P,
                                            ctypes.c_size_t, _P]),
@@ -344,10 +343,9 @@ def muon_profile_read(h, kernel: int, clear: int = 0) -> tuple:
 
 # --- layer operators (tensors in layers.py; here the C calls as they are) -----
 
-def muon_linear_workspace_bytes(d: muon_linear, op: int, a_ptr: int, b_ptr: int, e: Optional[muon_epilogue],
-                                y_ptr: int) -> tuple:
+def muon_linear_workspace_bytes(d: muon_linear, op: int, a_ptr: int, b_ptr: int) -> tuple:
     out = ctypes.c_size_t(0)
-    s = load().muon_linear_workspace_bytes(d, op, a_ptr, b_ptr, e, y_ptr, out)
+    s = load().muon_linear_workspace_bytes(d, op, a_ptr, b_ptr, out)
     return s, out.value
 
 

@@ -20,39 +20,100 @@ namespace muon {
 
 namespace {
 
-// Sum over the lanes that share a row: a wave (WPR = 1) or the workgroup.
-template <int WPR>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-    if constexpr (WPR == 1)
-        return wave_sum(v);
-    else
-        return block_sum_256(v, red);
+// One step of a wave sum: v + v moved by a DPP control, 0 from outside.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+// Wave-wide sum in the vector unit: within rows of 16 lanes by shifts, then
+// across them by the row broadcasts; lane 63 holds it.
+__device__ __forceinline__ float wave_total(float v) {
+    v = dpp_add<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);  // row_bcast 15 into rows 1, 3
+    v = dpp_add<0x143, 0xc>(v);  // row_bcast 31 into rows 2, 3
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// Two sums at once.
+// Sums over the lanes that share a row: a wave, or WPR neighbouring waves of
+// the workgroup, all of which call it. red: two floats a wave; calls in turn
+// use two such buffers, so that one barrier a call orders them.
 template <int WPR>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float* red) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        a += __shfl_xor(a, off, 64);
-        b += __shfl_xor(b, off, 64);
-    }
+    a = wave_total(a);
+    b = wave_total(b);
     if constexpr (WPR > 1) {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        __syncthreads();
         if (lane == 0) {
-            red[wave] = a;
-            red[4 + wave] = b;
+            red[2 * wave] = a;
+            red[2 * wave + 1] = b;
         }
         __syncthreads();
-        a = ((red[0] + red[1]) + red[2]) + red[3];
-        b = ((red[4] + red[5]) + red[6]) + red[7];
+        const float* r = red + wave / WPR * WPR * 2;
+        a = r[0];
+        b = r[1];
+#pragma unroll
+        for (int w = 1; w < WPR; ++w) {
+            a += r[2 * w];
+            b += r[2 * w + 1];
+        }
     }
 }
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+    float none = 0.f;
+    row_sum2<WPR>(v, none, red);
+    return v;
+}
 
-template <typename T, int NCH, int WPR>
+// A chunk of 8 elements as loaded.
+template <typename T>
+struct Raw {
+    uint32_t w[sizeof(T) * 2];
+    // n of the elements exist, the others are 0. VEC: n is 8 or more, or none
+    template <bool VEC>
+    __device__ __forceinline__ void load(const T* __restrict__ p, int n) {
+        if (VEC && n <= 0) {
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(T) * 2; ++k) w[k] = 0;
+        } else if (VEC || n >= 8) {
+            const u32x4_mem* q = reinterpret_cast<const u32x4_mem*>(p);
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+                const u32x4 t = q[k];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[4 * k + e] = t[e];
+            }
+        } else {
+            T t[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = e < n ? p[e] : (T)0.f;
+            __builtin_memcpy(w, t, sizeof(w));
+        }
+    }
+    // the compiler takes the words as new: it widens them again rather than
+    // keep the float values across
+    __device__ __forceinline__ void renew() {
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) * 2; ++k) asm volatile("" : "+v"(w[k]));
+    }
+    __device__ __forceinline__ float get(int e) const {
+        if constexpr (sizeof(T) == 4) {
+            return __uint_as_float(w[e]);
+        } else {
+            T t;
+            const uint16_t u = (uint16_t)(w[e / 2] >> (e % 2 * 16));
+            __builtin_memcpy(&t, &u, 2);
+            return (float)t;
+        }
+    }
+};
+
+template <typename T, int NCH, int WPR, bool VEC>
 __global__ __launch_bounds__(256) void k_norm_forward(const NormArgs n) {
-    __shared__ float red[8];
+    __shared__ float red[16];
     constexpr int LPR = 64 * WPR;  // lanes per row
     const int lane = threadIdx.x % LPR;
     const int64_t row = (int64_t)blockIdx.x * (4 / WPR) + threadIdx.x / LPR;
@@ -60,43 +121,56 @@ __global__ __launch_bounds__(256) void k_norm_forward(const NormArgs n) {
     const T* x = static_cast<const T*>(n.x) + row * n.ld_x;
     T* y = static_cast<T*>(n.y) + row * n.ld_y;
     const float inv = 1.f / (float)n.cols;
-    float v[NCH][8];
-    float s = 0.f;
+    Raw<T> v[NCH];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
         const int c = (i * LPR + lane) * 8;
-        load8(x + c, n.cols - c, n.vec, v[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += v[i][e];
+        v[i].template load<VEC>(x + c, n.cols - c);
     }
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += v[i].get(e);
     const float mean = row_sum<WPR>(s, red) * inv;
     float q = 0.f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
         const int left = n.cols - (i * LPR + lane) * 8;
+        if (VEC ? left > 0 : left >= 8) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[i][e] = e < left ? v[i][e] - mean : 0.f;
-            q = fmaf(v[i][e], v[i][e], q);
+            for (int e = 0; e < 8; ++e) {
+                const float d = v[i].get(e) - mean;
+                q = fmaf(d, d, q);
+            }
+        } else if (!VEC) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = e < left ? v[i].get(e) - mean : 0.f;
+                q = fmaf(d, d, q);
+            }
         }
     }
-    const float rstd = 1.f / sqrtf(row_sum<WPR>(q, red) * inv + n.eps);
+    const float rstd = 1.f / sqrtf(row_sum<WPR>(q, red + 8) * inv + n.eps);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
         const int c = (i * LPR + lane) * 8;
         const int left = n.cols - c;
         if (left <= 0) continue;
-        float w[8], b[8];
-        if (n.weight) load8(n.weight + c, left, n.vec_w, w);
-        if (n.bias) load8(n.bias + c, left, n.vec_w, b);
+        float t[8], u[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float t = v[i][e] * rstd;
-            if (n.weight) t *= w[e];
-            if (n.bias) t += b[e];
-            v[i][e] = t;
+        for (int e = 0; e < 8; ++e) t[e] = (v[i].get(e) - mean) * rstd;
+        if (n.weight) {
+            load8(n.weight + c, left, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] *= u[e];
         }
-        store8(y + c, left, n.vec, v[i]);
+        if (n.bias) {
+            load8(n.bias + c, left, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] += u[e];
+        }
+        store8(y + c, VEC ? 8 : left, t);
     }
     if (lane == 0) {
         n.mean[row] = mean;
@@ -107,7 +181,7 @@ __global__ __launch_bounds__(256) void k_norm_forward(const NormArgs n) {
 // Rows of any length, one workgroup each, read three times (twice from cache).
 template <typename T>
 __global__ __launch_bounds__(256) void k_norm_forward_wide(const NormArgs n) {
-    __shared__ float red[8];
+    __shared__ float red[16];
     const int64_t row = blockIdx.x;
     const T* x = static_cast<const T*>(n.x) + row * n.ld_x;
     T* y = static_cast<T*>(n.y) + row * n.ld_y;
@@ -115,35 +189,35 @@ __global__ __launch_bounds__(256) void k_norm_forward_wide(const NormArgs n) {
     float s = 0.f;
     for (int c = threadIdx.x * 8; c < n.cols; c += 2048) {
         float v[8];
-        load8(x + c, n.cols - c, n.vec, v);
+        load8(x + c, n.cols - c, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += v[e];
     }
-    const float mean = block_sum_256(s, red) * inv;
+    const float mean = row_sum<4>(s, red) * inv;
     float q = 0.f;
     for (int c = threadIdx.x * 8; c < n.cols; c += 2048) {
         float v[8];
-        load8(x + c, n.cols - c, n.vec, v);
+        load8(x + c, n.cols - c, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float d = c + e < n.cols ? v[e] - mean : 0.f;
             q = fmaf(d, d, q);
         }
     }
-    const float rstd = 1.f / sqrtf(block_sum_256(q, red) * inv + n.eps);
+    const float rstd = 1.f / sqrtf(row_sum<4>(q, red + 8) * inv + n.eps);
     for (int c = threadIdx.x * 8; c < n.cols; c += 2048) {
         const int left = n.cols - c;
         float v[8], w[8], b[8];
-        load8(x + c, left, n.vec, v);
-        if (n.weight) load8(n.weight + c, left, n.vec_w, w);
-        if (n.bias) load8(n.bias + c, left, n.vec_w, b);
+        load8(x + c, left, v);
+        if (n.weight) load8(n.weight + c, left, w);
+        if (n.bias) load8(n.bias + c, left, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             v[e] = (v[e] - mean) * rstd;
             if (n.weight) v[e] *= w[e];
             if (n.bias) v[e] += b[e];
         }
-        store8(y + c, left, n.vec, v);
+        store8(y + c, left, v);
     }
     if (threadIdx.x == 0) {
         n.mean[row] = mean;
@@ -152,13 +226,21 @@ __global__ __launch_bounds__(256) void k_norm_forward_wide(const NormArgs n) {
 }
 
 // dx = rstd (g - mean(g) - xhat mean(g xhat)) + add with g = dy w, and the
-// workgroup's sums of dy xhat and dy per column.
-template <typename T, int NCH, int WPR>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_norm_backward(const NormArgs n) {
+// workgroup's sums of dy xhat and dy per column. WPR waves share a row, and go
+// through their rows with the next row's x, dy and add on the way in; these
+// stay as loaded and are widened twice, so that a lane of two chunks leaves
+// room for them at two or three waves a SIMD (four chunks a lane, one wave a
+// row of 2048, spilled: 90 us at 16384 x 1600 bf16, against 52 without the
+// next row on the way). VEC: rows are whole chunks.
+template <typename T, int NCH, int WPR, bool VEC>
+__global__ __launch_bounds__(WPR == 8 ? 512 : 256) __attribute__((amdgpu_waves_per_eu(2))) void k_norm_backward(
+    const NormArgs n) {
     constexpr int LPR = 64 * WPR;
-    constexpr int RPB = 4 / WPR;  // rows a workgroup works on at once
-    __shared__ float red[8];
-    __shared__ float col[WPR == 1 ? 2 * NCH * 512 : 1];
+    constexpr int WAVES = WPR == 8 ? 8 : 4;
+    constexpr int RPB = WAVES / WPR;  // rows a workgroup works on at once
+    constexpr int CW = NCH * LPR * 8;
+    __shared__ float red[2][2 * WAVES];
+    __shared__ float col[RPB > 1 ? RPB / 2 * 2 * CW : 1];
     const int lane = threadIdx.x % LPR;
     const float inv = 1.f / (float)n.cols;
     float w[NCH][8], dw[NCH][8], db[NCH][8];
@@ -166,7 +248,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
     for (int i = 0; i < NCH; ++i) {
         const int c = (i * LPR + lane) * 8;
         if (n.weight) {
-            load8(n.weight + c, n.cols - c, n.vec_w, w[i]);
+            load8(n.weight + c, n.cols - c, w[i]);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[i][e] = 1.f;
@@ -174,86 +256,118 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.f;
     }
-    const int64_t step = (int64_t)gridDim.x * RPB;
-    for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR; row < n.rows; row += step) {
+    struct Row {
+        Raw<T> x[NCH], dy[NCH], add[NCH];
+        float mean, rstd;
+    };
+    auto fetch = [&](Row& r, int64_t row) {
         const T* x = static_cast<const T*>(n.x) + row * n.ld_x;
         const T* dy = static_cast<const T*>(n.dy) + row * n.ld_y;
-        const float mean = n.mean[row], rstd = n.rstd[row];
-        float xh[NCH][8], g[NCH][8];
-        float s0 = 0.f, s1 = 0.f;
+        const T* add = static_cast<const T*>(n.add) + row * n.ld_r;
+        r.mean = n.mean[row];
+        r.rstd = n.rstd[row];
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             const int c = (i * LPR + lane) * 8;
-            load8(x + c, n.cols - c, n.vec, xh[i]);
-            load8(dy + c, n.cols - c, n.vec, g[i]);
+            r.x[i].template load<VEC>(x + c, n.cols - c);
+            r.dy[i].template load<VEC>(dy + c, n.cols - c);
+            if (n.add) r.add[i].template load<VEC>(add + c, n.cols - c);
         }
+    };
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
+    Row cur, nxt;
+    if (row < n.rows) fetch(cur, row);
+    // the same number of turns for every wave: with no row left, dy and so
+    // every sum is left as it is
+    const int64_t turns = (n.rows + step - 1) / step;
+    for (int64_t t = 0; t < turns; ++t, row += step) {
+        const bool live = row < n.rows;
+        if (row + step < n.rows) fetch(nxt, row + step);
+        const float rstd = cur.rstd, shift = -cur.mean;
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
+            if (!live) break;
             // columns past the row's end have dy = 0, so they add nothing to any sum
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                xh[i][e] = (xh[i][e] - mean) * rstd;
-                dw[i][e] = fmaf(g[i][e], xh[i][e], dw[i][e]);
-                db[i][e] += g[i][e];
-                g[i][e] *= w[i][e];
-                s0 += g[i][e];
-                s1 = fmaf(g[i][e], xh[i][e], s1);
+                const float xh = (cur.x[i].get(e) + shift) * rstd, d = cur.dy[i].get(e);
+                dw[i][e] = fmaf(d, xh, dw[i][e]);
+                db[i][e] += d;
+                const float g = d * w[i][e];
+                s0 += g;
+                s1 = fmaf(g, xh, s1);
             }
         }
-        row_sum2<WPR>(s0, s1, red);
+        row_sum2<WPR>(s0, s1, red[t & 1]);
         s0 *= inv;
         s1 *= inv;
         T* dx = static_cast<T*>(n.dx) + row * n.ld_dx;
-        const T* add = n.add ? static_cast<const T*>(n.add) + row * n.ld_r : nullptr;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             const int c = (i * LPR + lane) * 8;
             const int left = n.cols - c;
-            if (left <= 0) continue;
+            if (left <= 0 || !live) continue;
+            cur.x[i].renew();
+            cur.dy[i].renew();
+            float t[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[i][e] = (g[i][e] - fmaf(xh[i][e], s1, s0)) * rstd;
-            if (add) {
-                float a[8];
-                load8(add + c, left, n.vec, a);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) g[i][e] += a[e];
+            for (int e = 0; e < 8; ++e) {
+                const float xh = (cur.x[i].get(e) + shift) * rstd;
+                t[e] = (cur.dy[i].get(e) * w[i][e] - fmaf(xh, s1, s0)) * rstd;
             }
-            store8(dx + c, left, n.vec, g[i]);
+            if (n.add) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] += cur.add[i].get(e);
+            }
+            store8(dx + c, VEC ? 8 : left, t);
         }
+        cur = nxt;
     }
     if (!n.part) return;
     float* part = n.part + (int64_t)blockIdx.x * 2 * n.cols;
-    if constexpr (WPR == 1) {
-        // the four waves' sums, added in wave order
-        constexpr int CW = NCH * 512;
-        for (int wv = 0; wv < 4; ++wv) {
-            if ((threadIdx.x >> 6) == wv) {
+    if constexpr (RPB > 1) {
+        // the sums of waves that hold the same columns, halved each time, in
+        // fixed order
+        const int grp = threadIdx.x / LPR;
+#pragma unroll
+        for (int half = RPB / 2; half >= 1; half /= 2) {
+            if (grp >= half && grp < 2 * half) {
+                float* o = col + (grp - half) * 2 * CW;
 #pragma unroll
                 for (int i = 0; i < NCH; ++i) {
-                    const int c = (i * 64 + lane) * 8;
+                    const int c = (i * LPR + lane) * 8;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        col[c + e] = (wv ? col[c + e] : 0.f) + dw[i][e];
-                        col[CW + c + e] = (wv ? col[CW + c + e] : 0.f) + db[i][e];
+                        o[c + e] = dw[i][e];
+                        o[CW + c + e] = db[i][e];
+                    }
+                }
+            }
+            __syncthreads();
+            if (grp < half) {
+                const float* o = col + grp * 2 * CW;
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) {
+                    const int c = (i * LPR + lane) * 8;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        dw[i][e] += o[c + e];
+                        db[i][e] += o[CW + c + e];
                     }
                 }
             }
             __syncthreads();
         }
-        for (int c = threadIdx.x; c < n.cols; c += 256) {
-            part[c] = col[c];
-            part[n.cols + c] = col[CW + c];
-        }
-    } else {
+        if (grp != 0) return;
+    }
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int c = (i * LPR + lane) * 8;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < n.cols) {
-                    part[c + e] = dw[i][e];
-                    part[n.cols + c + e] = db[i][e];
-                }
+    for (int i = 0; i < NCH; ++i) {
+        const int c = (i * LPR + lane) * 8;
+        if (c < n.cols) {
+            store8(part + c, n.cols - c, dw[i]);
+            store8(part + n.cols + c, n.cols - c, db[i]);
         }
     }
 }
@@ -270,9 +384,9 @@ __global__ __launch_bounds__(256) void k_norm_backward_wide(const NormArgs n) {
     auto chunk = [&](int c, float (&xh)[8], float (&g)[8]) {
         const int left = n.cols - c;
         float w[8];
-        load8(x + c, left, n.vec, xh);
-        load8(dy + c, left, n.vec, g);
-        if (n.weight) load8(n.weight + c, left, n.vec_w, w);
+        load8(x + c, left, xh);
+        load8(dy + c, left, g);
+        if (n.weight) load8(n.weight + c, left, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             xh[e] = (xh[e] - mean) * rstd;
@@ -299,11 +413,11 @@ __global__ __launch_bounds__(256) void k_norm_backward_wide(const NormArgs n) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = (g[e] - fmaf(xh[e], s1, s0)) * rstd;
         if (add) {
-            load8(add + c, n.cols - c, n.vec, a);
+            load8(add + c, n.cols - c, a);
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] += a[e];
         }
-        store8(dx + c, n.cols - c, n.vec, g);
+        store8(dx + c, n.cols - c, g);
     }
 }
 
@@ -320,8 +434,8 @@ __global__ __launch_bounds__(256) void k_norm_columns(const NormArgs n) {
     if (c < n.cols) {
         for (int64_t r = (int64_t)blockIdx.y * 8 + rl; r < n.rows; r += (int64_t)n.blocks * 8) {
             float x[8], g[8];
-            load8(static_cast<const T*>(n.x) + r * n.ld_x + c, n.cols - c, n.vec, x);
-            load8(static_cast<const T*>(n.dy) + r * n.ld_y + c, n.cols - c, n.vec, g);
+            load8(static_cast<const T*>(n.x) + r * n.ld_x + c, n.cols - c, x);
+            load8(static_cast<const T*>(n.dy) + r * n.ld_y + c, n.cols - c, g);
             const float mean = n.mean[r], rstd = n.rstd[r];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -348,48 +462,71 @@ __global__ __launch_bounds__(256) void k_norm_columns(const NormArgs n) {
     }
 }
 
-// dweight, dbias (+)= the partial rows, added in order: 64 columns a
-// workgroup, each wave a quarter of the partial rows.
-__global__ __launch_bounds__(256) void k_norm_join(const NormArgs n) {
-    __shared__ float red[4][64];
+// dweight, dbias (+)= the partial rows: 64 columns a workgroup, each of its 16
+// waves a run of the rows, added in order.
+__global__ __launch_bounds__(1024) void k_norm_join(const NormArgs n) {
+    __shared__ float red[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = blockIdx.x * 64 + lane;
     float* out = blockIdx.y ? n.dbias : n.dweight;
     if (!out) return;
-    const int per = (n.blocks + 3) / 4;
+    const int per = (n.blocks + 15) / 16;
     const int b1 = (wave + 1) * per < n.blocks ? (wave + 1) * per : n.blocks;
     float s = 0.f;
     if (c < n.cols) {
-#pragma unroll 8
+#pragma unroll 16
         for (int b = wave * per; b < b1; ++b) s += n.part[((int64_t)b * 2 + blockIdx.y) * n.cols + c];
     }
     red[wave][lane] = s;
     __syncthreads();
     if (wave == 0 && c < n.cols) {
-        s = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
+        s = red[0][lane];
+#pragma unroll
+        for (int w = 1; w < 16; ++w) s += red[w][lane];
         out[c] = n.accumulate ? out[c] + s : s;
     }
 }
 
-constexpr int kWaveCols = 2048;   // a wave's registers hold a row
-constexpr int kBlockCols = 8192;  // a workgroup's do
+constexpr int kBlockCols = 8192;  // longest rows that live in registers
+
+template <typename T, bool VEC>
+void forward_rows(const NormArgs& n, hipStream_t st) {
+    const unsigned g4 = (unsigned)((n.rows + 3) / 4), g1 = (unsigned)n.rows;
+    if (n.cols <= 512)
+        k_norm_forward<T, 1, 1, VEC><<<g4, 256, 0, st>>>(n);
+    else if (n.cols <= 1024)
+        k_norm_forward<T, 2, 1, VEC><<<g4, 256, 0, st>>>(n);
+    else if (n.cols <= 2048)
+        k_norm_forward<T, 4, 1, VEC><<<g4, 256, 0, st>>>(n);
+    else if (n.cols <= 4096)
+        k_norm_forward<T, 2, 4, VEC><<<g1, 256, 0, st>>>(n);
+    else
+        k_norm_forward<T, 4, 4, VEC><<<g1, 256, 0, st>>>(n);
+}
+
+template <typename T, bool VEC>
+void backward_rows(const NormArgs& n, hipStream_t st) {
+    const unsigned b = (unsigned)n.blocks;
+    if (n.cols <= 512)
+        k_norm_backward<T, 1, 1, VEC><<<b, 256, 0, st>>>(n);
+    else if (n.cols <= 1024)
+        k_norm_backward<T, 2, 1, VEC><<<b, 256, 0, st>>>(n);
+    else if (n.cols <= 2048)
+        k_norm_backward<T, 2, 2, VEC><<<b, 256, 0, st>>>(n);
+    else if (n.cols <= 4096)
+        k_norm_backward<T, 2, 4, VEC><<<b, 256, 0, st>>>(n);
+    else
+        k_norm_backward<T, 2, 8, VEC><<<b, 512, 0, st>>>(n);
+}
 
 template <typename T>
 hipError_t forward_t(const NormArgs& n, hipStream_t st) {
-    if (n.rows == 0) return hipSuccess;
-    const unsigned g4 = (unsigned)((n.rows + 3) / 4), g1 = (unsigned)n.rows;
-    if (n.cols <= 512)
-        k_norm_forward<T, 1, 1><<<g4, 256, 0, st>>>(n);
-    else if (n.cols <= 1024)
-        k_norm_forward<T, 2, 1><<<g4, 256, 0, st>>>(n);
-    else if (n.cols <= kWaveCols)
-        k_norm_forward<T, 4, 1><<<g4, 256, 0, st>>>(n);
-    else if (n.cols <= 4096)
-        k_norm_forward<T, 2, 4><<<g1, 256, 0, st>>>(n);
-    else if (n.cols <= kBlockCols)
-        k_norm_forward<T, 4, 4><<<g1, 256, 0, st>>>(n);
+    if (n.cols > kBlockCols)
+        k_norm_forward_wide<T><<<(unsigned)n.rows, 256, 0, st>>>(n);
+    else if (n.cols % 8 == 0)
+        forward_rows<T, true>(n, st);
     else
-        k_norm_forward_wide<T><<<g1, 256, 0, st>>>(n);
+        forward_rows<T, false>(n, st);
     return hipGetLastError();
 }
 
@@ -397,30 +534,23 @@ template <typename T>
 hipError_t backward_t(const NormArgs& n, hipStream_t st) {
     hipError_t e = hipSuccess;
     if (n.rows > 0) {
-        const unsigned b = (unsigned)n.blocks;
-        if (n.cols <= 512) {
-            k_norm_backward<T, 1, 1><<<b, 256, 0, st>>>(n);
-        } else if (n.cols <= 1024) {
-            k_norm_backward<T, 2, 1><<<b, 256, 0, st>>>(n);
-        } else if (n.cols <= kWaveCols) {
-            k_norm_backward<T, 4, 1><<<b, 256, 0, st>>>(n);
-        } else if (n.cols <= 4096) {
-            k_norm_backward<T, 2, 4><<<b, 256, 0, st>>>(n);
-        } else if (n.cols <= kBlockCols) {
-            k_norm_backward<T, 4, 4><<<b, 256, 0, st>>>(n);
-        } else {
+        if (n.cols > kBlockCols) {
             if (n.part) {
-                k_norm_columns<T><<<dim3((unsigned)((n.cols + 255) / 256), b), 256, 0, st>>>(n);
+                k_norm_columns<T><<<dim3((unsigned)((n.cols + 255) / 256), (unsigned)n.blocks), 256, 0, st>>>(n);
                 e = hipGetLastError();
                 if (e != hipSuccess) return e;
             }
             k_norm_backward_wide<T><<<(unsigned)n.rows, 256, 0, st>>>(n);
+        } else if (n.cols % 8 == 0) {
+            backward_rows<T, true>(n, st);
+        } else {
+            backward_rows<T, false>(n, st);
         }
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (n.dweight || n.dbias) {
-        k_norm_join<<<dim3((unsigned)((n.cols + 63) / 64), 2), 256, 0, st>>>(n);
+        k_norm_join<<<dim3((unsigned)((n.cols + 63) / 64), 2), 1024, 0, st>>>(n);
         e = hipGetLastError();
     }
     return e;
@@ -429,16 +559,11 @@ hipError_t backward_t(const NormArgs& n, hipStream_t st) {
 }  // namespace
 
 // Workgroups of the backward pass (each leaves one partial row of column
-// sums): up to 512, two for every CU, one row (or 4, a wave each) at a time.
+// sums): two a CU of 4 waves (one of 8 beyond 4096 columns), each with four
+// rows or more; for rows longer than registers hold, runs of at least 64 rows.
 int norm_backward_blocks(int64_t rows, int64_t cols) {
-    int64_t b;
-    if (cols <= kWaveCols)
-        b = (rows + 3) / 4;
-    else if (cols <= kBlockCols)
-        b = rows;
-    else
-        b = (rows + 63) / 64;
-    const int64_t most = cols <= kBlockCols ? 512 : 64;
+    const int64_t b = cols <= kBlockCols ? (rows + 3) / 4 : (rows + 63) / 64;
+    const int64_t most = cols <= 4096 ? 512 : cols <= kBlockCols ? 256 : 64;
     return (int)(b < most ? b : most);
 }
 

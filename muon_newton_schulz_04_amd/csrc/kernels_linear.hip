@@ -345,9 +345,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const bool direct = piece < 0;
     float* const part = g.partial + (int64_t)piece * (TM * TN);
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (direct && g.epi.bias) load8(g.epi.bias + ccol, 8, false, bias);
-    uint4 in0[NP], in1[NP], in2[NP];  // this block's, the next one's and the one's after that
-    auto fetch = [&](int fi, uint4(&x)[NP]) {
+    if (direct && g.epi.bias) load8(g.epi.bias + ccol, 8, bias);
+    u32x4 in0[NP], in1[NP], in2[NP];  // this block's, the next one's and the one's after that
+    auto fetch = [&](int fi, u32x4(&x)[NP]) {
 #pragma unroll
         for (int it = 0; it < NP; ++it) {
             const int row = row0 + 32 * fi + it * RPI;
@@ -385,7 +385,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             if (row < g.M && inside) {
                 if (direct) {
                     float v[8] = {lo[0], lo[1], lo[2], lo[3], up[0], up[1], up[2], up[3]};
-                    finish8<T>(g.epi, row, col, 8, true, v, bias, in0[it]);
+                    finish8<T>(g.epi, row, col, 8, v, bias, in0[it]);
                 } else {
                     float* p = part + (row - i0) * TN + (col - j0);
                     *reinterpret_cast<f32x4*>(p) = lo;
@@ -453,7 +453,7 @@ __global__ __launch_bounds__(256) void k_gemm_join(const GemmArgs g) {
 #pragma unroll 4
     for (int s = sa; s < sb; ++s) {
         float u[8];
-        load8(p + s * stride, 8, true, u);
+        load8(p + s * stride, 8, u);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += u[e];
     }
@@ -466,25 +466,28 @@ __global__ __launch_bounds__(256) void k_gemm_join(const GemmArgs g) {
     }
     const int left = g.N - col;
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (g.epi.bias) load8(g.epi.bias + col, left, false, bias);
-    const bool vec = left >= 8 && g.epi.vec;
-    uint4 in = {0, 0, 0, 0};
-    if (vec) in = fetch8<T>(g.epi, row, col);
-    finish8<T>(g.epi, row, col, left, vec, v, bias, in);
+    if (g.epi.bias) load8(g.epi.bias + col, left, bias);
+    u32x4 in = {0, 0, 0, 0};
+    if (left >= 8) in = fetch8<T>(g.epi, row, col);
+    finish8<T>(g.epi, row, col, left, v, bias, in);
 }
 
 // Rows of any alignment and length to 16-byte aligned, zero-padded ones: one
 // 16-byte chunk per thread.
 __global__ __launch_bounds__(256) void k_pack(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
-                                              uint4* __restrict__ dst, int64_t chunks) {
+                                              u32x4* __restrict__ dst, int64_t chunks) {
     const int64_t n = rows * chunks;
     for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < n; id += (int64_t)gridDim.x * 256) {
         const int64_t r = id / chunks, c = (id - r * chunks) * 8;
         const uint16_t* p = src + r * ld + c;
-        uint32_t w[8];
+        if (c + 8 <= cols) {
+            dst[id] = *reinterpret_cast<const u32x4_mem*>(p);
+        } else {
+            uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = c + e < cols ? p[e] : 0u;
-        dst[id] = uint4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+            for (int e = 0; e < 8; ++e) w[e] = c + e < cols ? p[e] : 0u;
+            dst[id] = u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+        }
     }
 }
 
@@ -543,7 +546,7 @@ hipError_t launch_pack(const void* src, int64_t ld, int64_t rows, int64_t cols, 
     const int64_t n = rows * (cols_pad / 8);
     const int64_t blocks = (n + 255) / 256;
     k_pack<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(static_cast<const uint16_t*>(src), ld, rows,
-                                                                        cols, static_cast<uint4*>(dst), cols_pad / 8);
+                                                                        cols, static_cast<u32x4*>(dst), cols_pad / 8);
     return hipGetLastError();
 }
 

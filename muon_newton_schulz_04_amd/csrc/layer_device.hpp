@@ -12,29 +12,34 @@ typedef _Float16 f16;
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x8_a16 __attribute__((ext_vector_type(8), aligned(16)));  // in memory
 
+// 8 elements as a vector, and the same in memory at any element's address (the
+// hardware takes unaligned 16-byte accesses).
 template <typename T>
 struct V8;
 template <>
 struct V8<bf16> {
     typedef bf16x8 type;
+    typedef bf16x8 mem __attribute__((aligned(2)));
 };
 template <>
 struct V8<f16> {
     typedef f16x8 type;
+    typedef f16x8 mem __attribute__((aligned(2)));
 };
 template <>
 struct V8<float> {
-    typedef f32x8_a16 type;
+    typedef f32x8 type;
+    typedef f32x8 mem __attribute__((aligned(4)));
 };
+typedef u32x4 u32x4_mem __attribute__((aligned(2)));
+typedef f32x4 f32x4_mem __attribute__((aligned(4)));
 
-// 8 consecutive elements as float; `n` of them exist (the rest read as 0).
-// vec: p is 16-byte aligned.
+// 8 consecutive elements as float; n of them exist (the others read as 0).
 template <typename T>
-__device__ __forceinline__ void load8(const T* __restrict__ p, int n, bool vec, float (&v)[8]) {
-    if (n >= 8 && vec) {
-        const typename V8<T>::type t = *reinterpret_cast<const typename V8<T>::type*>(p);
+__device__ __forceinline__ void load8(const T* __restrict__ p, int n, float (&v)[8]) {
+    if (n >= 8) {
+        const typename V8<T>::type t = *reinterpret_cast<const typename V8<T>::mem*>(p);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = (float)t[e];
     } else {
@@ -45,12 +50,12 @@ __device__ __forceinline__ void load8(const T* __restrict__ p, int n, bool vec, 
 
 // The same 8 elements rounded once (nearest even) to T.
 template <typename T>
-__device__ __forceinline__ void store8(T* __restrict__ p, int n, bool vec, const float (&v)[8]) {
-    if (n >= 8 && vec) {
+__device__ __forceinline__ void store8(T* __restrict__ p, int n, const float (&v)[8]) {
+    if (n >= 8) {
         f32x8 t;
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] = v[e];
-        *reinterpret_cast<typename V8<T>::type*>(p) = __builtin_convertvector(t, typename V8<T>::type);
+        *reinterpret_cast<typename V8<T>::mem*>(p) = __builtin_convertvector(t, typename V8<T>::type);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -62,21 +67,21 @@ __device__ __forceinline__ void store8(T* __restrict__ p, int n, bool vec, const
 // panels that the workgroups share out of L2 (c_fc forward at 16384 x 1600 x
 // 6400 with the pre-activation kept: 401 us with plain stores, 366 so).
 template <typename T>
-__device__ __forceinline__ void stream8(T* __restrict__ p, int n, bool vec, const float (&v)[8]) {
-    if (n >= 8 && vec) {
+__device__ __forceinline__ void stream8(T* __restrict__ p, int n, const float (&v)[8]) {
+    if (n >= 8) {
         f32x8 t;
 #pragma unroll
         for (int e = 0; e < 8; ++e) t[e] = v[e];
         if constexpr (sizeof(T) == 2) {
             __builtin_nontemporal_store(__builtin_convertvector(t, typename V8<T>::type),
-                                        reinterpret_cast<typename V8<T>::type*>(p));
+                                        reinterpret_cast<typename V8<T>::mem*>(p));
         } else {
             const f32x4 lo = {t[0], t[1], t[2], t[3]}, up = {t[4], t[5], t[6], t[7]};
-            __builtin_nontemporal_store(lo, reinterpret_cast<f32x4*>(p));
-            __builtin_nontemporal_store(up, reinterpret_cast<f32x4*>(p) + 1);
+            __builtin_nontemporal_store(lo, reinterpret_cast<f32x4_mem*>(p));
+            __builtin_nontemporal_store(up, reinterpret_cast<f32x4_mem*>(p + 4));
         }
     } else {
-        store8(p, n, false, v);
+        store8(p, n, v);
     }
 }
 
@@ -193,7 +198,7 @@ __device__ __forceinline__ void act_slopes(int act, float (&v)[8]) {
 // or half of the weight gradient to add to. (A call with z and add both, and
 // the other half, read the rest in place.)
 template <typename T>
-__device__ __forceinline__ uint4 fetch8(const Epilogue& E, int64_t r, int64_t c) {
+__device__ __forceinline__ u32x4 fetch8(const Epilogue& E, int64_t r, int64_t c) {
     const void* p = nullptr;
     if (E.mode == EPI_GRAD_WEIGHT) {
         if (E.accumulate) p = static_cast<const float*>(E.y) + r * E.ld_y + c;
@@ -202,68 +207,67 @@ __device__ __forceinline__ uint4 fetch8(const Epilogue& E, int64_t r, int64_t c)
     } else if (E.add) {
         p = static_cast<const T*>(E.add) + r * E.ld_add + c;
     }
-    return p ? *reinterpret_cast<const uint4*>(p) : uint4{0, 0, 0, 0};
+    return p ? *static_cast<const u32x4_mem*>(p) : u32x4{0, 0, 0, 0};
 }
 
 template <typename T>
-__device__ __forceinline__ void widen8(const uint4& u, float (&v)[8]) {
+__device__ __forceinline__ void widen8(const u32x4& u, float (&v)[8]) {
     const typename V8<T>::type t = __builtin_bit_cast(typename V8<T>::type, u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = (float)t[e];
 }
 
 // The epilogue of 8 consecutive accumulators of row r from column c on, n of
-// them inside the matrix. bias: their bias values (forward). vec: all 8 are
-// inside, every row is 16-byte aligned, and `in` is fetch8's; otherwise
-// elements are read and written one by one.
+// them inside the matrix. bias: their bias values (forward). in: fetch8's if n
+// is 8 or more; a chunk at the matrix's edge is read in place.
 template <typename T>
-__device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c, int n, bool vec, float (&v)[8],
-                                        const float (&bias)[8], const uint4& in) {
+__device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c, int n, float (&v)[8],
+                                        const float (&bias)[8], const u32x4& in) {
     float t[8];
     if (E.mode == EPI_GRAD_WEIGHT) {
         float* y = static_cast<float*>(E.y) + r * E.ld_y + c;
         if (E.accumulate) {
-            if (vec) {
-                const f32x4 lo = __builtin_bit_cast(f32x4, in), up = *reinterpret_cast<const f32x4*>(y + 4);
+            if (n >= 8) {
+                const f32x4 lo = __builtin_bit_cast(f32x4, in), up = *reinterpret_cast<const f32x4_mem*>(y + 4);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     t[e] = lo[e];
                     t[4 + e] = up[e];
                 }
             } else {
-                load8(y, n, false, t);
+                load8(y, n, t);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += t[e];
         }
-        stream8(y, n, vec, v);
+        stream8(y, n, v);
         return;
     }
     bool fetched = false;  // `in` was z, not add
     if (E.mode == EPI_FORWARD) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += bias[e];
-        if (E.z) stream8(static_cast<T*>(E.z) + r * E.ld_z + c, n, vec, v);
+        if (E.z) stream8(static_cast<T*>(E.z) + r * E.ld_z + c, n, v);
         act_values(E.act, v);
     } else if (E.act != ACT_NONE) {
         fetched = true;
-        if (vec)
+        if (n >= 8)
             widen8<T>(in, t);
         else
-            load8(static_cast<const T*>(E.z) + r * E.ld_z + c, n, false, t);
+            load8(static_cast<const T*>(E.z) + r * E.ld_z + c, n, t);
         act_slopes(E.act, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= t[e];
     }
     if (E.add) {
-        if (vec && !fetched)
+        if (n >= 8 && !fetched)
             widen8<T>(in, t);
         else
-            load8(static_cast<const T*>(E.add) + r * E.ld_add + c, n, vec, t);
+            load8(static_cast<const T*>(E.add) + r * E.ld_add + c, n, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += t[e];
     }
-    stream8(static_cast<T*>(E.y) + r * E.ld_y + c, n, vec, v);
+    stream8(static_cast<T*>(E.y) + r * E.ld_y + c, n, v);
 }
 
 }  // namespace muon

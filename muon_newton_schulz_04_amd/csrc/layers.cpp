@@ -157,7 +157,7 @@ Tensor tensor_w(const muon_linear& d, const void* p, int size) {
 // GHz): slice costs of a workgroup alone on its CU and beside a second one,
 // what it spends outside its main loop, the join's traffic and launch, and
 // the rate at which the whole chip multiplies however it is filled.
-// direct: whole tiles can be finished by the product kernel.
+// direct: the product kernel can finish whole tiles (N is a multiple of 8).
 muon::GemmPlan choose_plan(int64_t M, int64_t N, int64_t K, bool direct) {
     int64_t slices = (K + muon::kGemmSlice - 1) / muon::kGemmSlice;
     if (slices < 1) slices = 1;
@@ -213,11 +213,7 @@ struct Product {
 
 bool needs_pack(const Tensor& t) { return t.rows > 0 && (!aligned16(t.p, t.ld, 2) || t.cols % 8 != 0); }
 
-// vec: all that the epilogue touches moves as whole 16-byte vectors (else, and
-// with K splits, the sums go through the workspace and the join kernel does
-// the epilogue element by element).
-muon_status plan_product(const muon_linear& d, int op, const void* pa, const void* pb, bool vec, bool dbias,
-                         Product* P) {
+muon_status plan_product(const muon_linear& d, int op, const void* pa, const void* pb, bool dbias, Product* P) {
     const bool io = d.weight_layout == MUON_WEIGHT_IN_OUT;
     if (op == MUON_LINEAR_FORWARD) {
         *P = {d.tokens, d.out_features, d.in_features, tensor_x(d, pa), tensor_w(d, pb, 2), true, !io};
@@ -233,9 +229,9 @@ muon_status plan_product(const muon_linear& d, int op, const void* pa, const voi
     P->pack_a = needs_pack(P->a);
     P->pack_b = needs_pack(P->b);
     // launches hold fewer than 2^32 threads
-    if (((P->M + 127) / 128) * ((P->N + 127) / 128) >= (int64_t)1 << (vec && P->N % 8 == 0 ? 22 : 18))
+    if (((P->M + 127) / 128) * ((P->N + 127) / 128) >= (int64_t)1 << (P->N % 8 == 0 ? 22 : 18))
         return fail(MUON_E_SHAPE, "linear: output too large");
-    P->plan = choose_plan(P->M, P->N, P->K, vec && P->N % 8 == 0);
+    P->plan = choose_plan(P->M, P->N, P->K, P->N % 8 == 0);
     size_t o = 0;
     P->off_a = o;
     if (P->pack_a) o = up256(o + (size_t)P->a.rows * up8(P->a.cols) * 2);
@@ -302,12 +298,9 @@ muon_status check_epilogue(const muon_linear& d, int op, const muon_epilogue& e)
 // What a product's epilogue reads and writes (e NULL: only the output).
 struct Outputs {
     Tensor y, add, z;
-    bool vec() const { return vec_of(y) && vec_of(add) && vec_of(z); }
-    static bool vec_of(const Tensor& t) { return !t.p || aligned16(t.p, t.ld, t.size); }
 };
 
 Outputs outputs_of(const muon_linear& d, int op, const muon_epilogue* e, const void* y) {
-    if (op == MUON_LINEAR_GRAD_WEIGHT) return {tensor_w(d, y, 4), {}, {}};
     const bool fwd = op == MUON_LINEAR_FORWARD;
     const int64_t cols = fwd ? d.out_features : d.in_features;
     Outputs o{fwd ? tensor_y(d, y) : tensor_x(d, y), {}, {}};
@@ -337,7 +330,7 @@ muon_status run_layer(const muon_linear* d, int op, const void* a, const void* w
     for (const Tensor& t : {A, W, Y, R, Z}) TRY(check_align(t.p, 2, "a 16-bit tensor"));
     TRY(check_align(e->bias, 4, "bias"));
     Product P;
-    TRY(plan_product(*d, op, a, w, o.vec(), false, &P));
+    TRY(plan_product(*d, op, a, w, false, &P));
     TRY(check_workspace(ws, ws_bytes, P.bytes));
     const Tensor S{ws, 1, (int64_t)P.bytes, (int64_t)P.bytes, 1};
     TRY(check_disjoint(Y, {A, W, R, Z, Bi, S}, &R));
@@ -355,7 +348,6 @@ muon_status run_layer(const muon_linear* d, int op, const void* a, const void* w
     E.ld_add = R.ld;
     E.ld_z = Z.ld;
     E.ld_y = Y.ld;
-    E.vec = o.vec();
     return run_product(P, d->dtype, E, nullptr, 0, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
 }
 
@@ -397,7 +389,7 @@ extern "C" {
 const char* muon_op_last_error(void) { return g_error.c_str(); }
 
 muon_status muon_linear_workspace_bytes(const muon_linear* d, int32_t op, const void* a, const void* b,
-                                        const muon_epilogue* e, const void* y, size_t* out_bytes) {
+                                        size_t* out_bytes) {
     return guarded([&]() -> muon_status {
         if (!out_bytes) return fail(MUON_E_INVALID_ARG, "null out_bytes");
         TRY(check_linear(d));
@@ -405,9 +397,8 @@ muon_status muon_linear_workspace_bytes(const muon_linear* d, int32_t op, const 
             return fail(MUON_E_INVALID_ARG, "unknown linear operation");
         *out_bytes = 0;
         if (d->tokens == 0 && op != MUON_LINEAR_GRAD_WEIGHT) return MUON_OK;
-        if (e && op != MUON_LINEAR_GRAD_WEIGHT) TRY(check_epilogue(*d, op, *e));
         Product P;
-        TRY(plan_product(*d, op, a, b, outputs_of(*d, op, e, y).vec(), op == MUON_LINEAR_GRAD_WEIGHT, &P));
+        TRY(plan_product(*d, op, a, b, op == MUON_LINEAR_GRAD_WEIGHT, &P));
         *out_bytes = P.bytes;
         return MUON_OK;
     });
@@ -435,8 +426,7 @@ muon_status muon_linear_grad_weight(const muon_linear* d, const void* x, const v
         TRY(check_align(dw, 4, "dw"));
         TRY(check_align(dbias, 4, "dbias"));
         Product P;
-        const Outputs o = outputs_of(*d, MUON_LINEAR_GRAD_WEIGHT, nullptr, dw);
-        TRY(plan_product(*d, MUON_LINEAR_GRAD_WEIGHT, x, dy, o.vec(), dbias != nullptr, &P));
+        TRY(plan_product(*d, MUON_LINEAR_GRAD_WEIGHT, x, dy, dbias != nullptr, &P));
         TRY(check_workspace(workspace, ws_bytes, P.bytes));
         const Tensor S{workspace, 1, (int64_t)P.bytes, (int64_t)P.bytes, 1};
         TRY(check_disjoint(W, {X, Y, Bi, S}, nullptr));
@@ -449,8 +439,7 @@ muon_status muon_linear_grad_weight(const muon_linear* d, const void* x, const v
         E.mode = muon::EPI_GRAD_WEIGHT;
         E.y = dw;
         E.ld_y = W.ld;
-        E.vec = o.vec();
-        E.accumulate = accumulate != 0;
+            E.accumulate = accumulate != 0;
         // dy is the second operand of an [in, out] gradient, else the first
         const int sum = !dbias ? 0 : d->weight_layout == MUON_WEIGHT_IN_OUT ? 1 : 2;
         return run_product(P, d->dtype, E, dbias, sum, ws, st);
@@ -480,9 +469,7 @@ muon_status muon_layernorm_forward(const muon_layernorm* d, const void* x, const
         n.y = y;
         n.mean = mean;
         n.rstd = rstd;
-        n.vec = aligned16(x, n.ld_x, size) && aligned16(y, n.ld_y, size);
-        n.vec_w = aligned16(weight, 0, 4) && aligned16(bias, 0, 4);
-        return hip_status(muon::launch_norm_forward(n, d->dtype, static_cast<hipStream_t>(stream)),
+            return hip_status(muon::launch_norm_forward(n, d->dtype, static_cast<hipStream_t>(stream)),
                           "layer norm kernel");
     });
 }
@@ -533,9 +520,6 @@ muon_status muon_layernorm_backward(const muon_layernorm* d, const void* dy, con
         n.accumulate = accumulate != 0;
         n.part = sums ? static_cast<float*>(workspace) : nullptr;
         n.blocks = muon::norm_backward_blocks(d->rows, d->cols);
-        n.vec = aligned16(dy, n.ld_y, size) && aligned16(x, n.ld_x, size) && aligned16(dx, n.ld_dx, size) &&
-                aligned16(add, n.ld_r, size);
-        n.vec_w = aligned16(weight, 0, 4);
         return hip_status(muon::launch_norm_backward(n, d->dtype, static_cast<hipStream_t>(stream)),
                           "layer norm gradient kernels");
     });

@@ -23,7 +23,6 @@ struct Epilogue {
     void* y;            // 16-bit output, or float32 for the weight gradient
     int64_t ld_add, ld_z, ld_y;
     int32_t accumulate;  // weight gradient: add to what is there
-    int32_t vec;         // every row touched starts 16-byte aligned
 };
 
 // C[M, N] = sum_k A(m, k) B(k, n) over 16-bit operands, each stored with its k
@@ -68,8 +67,6 @@ struct NormArgs {
     int32_t cols;
     int64_t ld_x, ld_y, ld_dx, ld_r;
     float eps;
-    int32_t vec;    // x, y, dy, add, dx: every row starts 16-byte aligned
-    int32_t vec_w;  // weight, bias are 16-byte aligned
     const void* x;
     const float* weight;
     const float* bias;

@@ -182,7 +182,7 @@ def linear_grad_input(dy, w, preact=None, activation="none", add=None, weight_la
 
 def _run_linear(op, call, what, d, a, w, e, out, device, dev):
     pa, pw, po = a.data_ptr(), w.data_ptr(), out.data_ptr()
-    s, nbytes = B.muon_linear_workspace_bytes(d, op, pa, pw, e, po)
+    s, nbytes = B.muon_linear_workspace_bytes(d, op, pa, pw)
     if s:
         _check(s, what)
     ws, pws = _workspace(nbytes, device)
@@ -213,7 +213,7 @@ def linear_grad_weight(x, dy, dw=None, dbias=None, accumulate=False, weight_layo
     pb = 0 if dbias is None else _vector("dbias", dbias, fout, dev)
     d = B.muon_linear(n, fin, fout, ld_x, ld_w, ld_y, code, lay)
     px, py, pd = x.data_ptr(), dy.data_ptr(), dw.data_ptr()
-    s, nbytes = B.muon_linear_workspace_bytes(d, B.MUON_LINEAR_GRAD_WEIGHT, px, py, None, pd)
+    s, nbytes = B.muon_linear_workspace_bytes(d, B.MUON_LINEAR_GRAD_WEIGHT, px, py)
     if s:
         _check(s, "linear_grad_weight")
     ws, pws = _workspace(nbytes, device)
