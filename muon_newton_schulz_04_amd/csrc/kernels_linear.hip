@@ -42,6 +42,12 @@ __device__ __forceinline__ f32x16 mfma<f16>(f16x8 a, f16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
+// s_waitcnt vmcnt(n), the other counters left alone
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
+
 // 16 bytes per lane, global -> LDS: lane i lands at lds + 16 i (a wave-uniform
 // LDS address, passed in M0, which the asm sets right before the load: see
 // dma16, whose conditions hold here too).
@@ -187,13 +193,18 @@ __device__ __forceinline__ float add8(f16x8 f, float v) {
 // gradient: two-element dot products with 1 on the fragments in registers, in
 // the shadow of the matrix instructions.
 template <typename T, int TM, int TN, bool AKC, bool BKC, int SUM>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_gemm(const GemmArgs g) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ? 1 : 2, TM == 128 ? 1 : 2))) void k_gemm(const GemmArgs g) {
     using OA = Operand<T, TM, AKC>;
     using OB = Operand<T, TN, BKC>;
     constexpr int WM = TM / 2, WN = TN / 2;   // a wave's block
     constexpr int FRI = WM / 32, FRJ = WN / 32;
     constexpr int SROW = WN * 4 + 16;  // bytes of a staged epilogue row
-    constexpr int SMEM = 2 * OA::BYTES + OB::BYTES;
+    // the tall tile: two A buffers and one B buffer, so that two workgroups fit
+    // a CU; the square tile, for products too small to fill the chip, whose
+    // time is load latency: a ring of four buffers of both
+    constexpr bool RING = TM == 128;
+    constexpr int STAGE = OA::BYTES + OB::BYTES;
+    constexpr int SMEM = RING ? 4 * STAGE : OA::BYTES + STAGE;
     static_assert(4 * 32 * SROW <= SMEM, "epilogue staging");
     __shared__ __attribute__((aligned(16))) char smem[SMEM];
 
@@ -275,8 +286,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     using CM = std::integral_constant<int, FRI * FRJ>;
     using CH = std::integral_constant<int, FRI * FRJ / 2>;
 
-    {
-        const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)smem;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)smem;
+    if constexpr (!RING) {
         char* const SB = smem + 2 * OA::BYTES;
         A.load(lds0);
         B.load(lds0 + 2 * OA::BYTES);
@@ -324,6 +335,45 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             slice(smem, smem + OA::BYTES, SB, lds0 + OA::BYTES);
             if (kt + 1 < nk) slice(smem + OA::BYTES, smem, SB, lds0);
         }
+    } else {
+        constexpr int NLD = OA::NLD + OB::NLD;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            A.load(lds0 + k * STAGE);
+            B.load(lds0 + k * STAGE + OA::BYTES);
+        }
+        wait_vm<2 * NLD>();
+        __syncthreads();
+        read_b(smem + OA::BYTES, 0);
+        read_a(smem, 0);
+        // S: this slice, N: the next, ldsF: the buffer of the one before,
+        // which every wave had read before the last barrier
+        auto slice = [&](const char* __restrict__ S, const char* __restrict__ N, uint32_t ldsF)
+                         __attribute__((always_inline)) {
+            A.load(ldsF);
+            B.load(ldsF + OA::BYTES);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int ks = 0; ks < NKS - 1; ++ks) {
+                read_b(S + OA::BYTES, ks + 1);
+                read_a(S, ks + 1);
+                products(ks, 0, FRI);
+                add_sums(ks);
+                interleave(std::integral_constant<int, RA + RB>{}, CM{});
+            }
+            products(NKS - 1, 0, FRI / 2);
+            add_sums(NKS - 1);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vm<2 * NLD>();  // the next slice has landed
+            __syncthreads();
+            read_b(N + OA::BYTES, 0);
+            read_a(N, 0);
+            products(NKS - 1, FRI / 2, FRI);
+            interleave(std::integral_constant<int, RA + RB>{}, CH{});
+        };
+        for (int kt = 0; kt < nk; ++kt)
+            slice(smem + (kt & 3) * STAGE, smem + ((kt + 1) & 3) * STAGE, lds0 + ((kt + 3) & 3) * STAGE);
+        wait_vm0();  // the loads past the end
     }
     __syncthreads();
 
@@ -472,6 +522,162 @@ __global__ __launch_bounds__(256) void k_gemm_join(const GemmArgs g) {
     finish8<T>(g.epi, row, col, left, v, bias, in);
 }
 
+template <typename T>
+__device__ __forceinline__ f32x4 mfma16(typename V8<T>::type a, typename V8<T>::type b, f32x4 c);
+template <>
+__device__ __forceinline__ f32x4 mfma16<bf16>(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x4 mfma16<f16>(f16x8 a, f16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Few rows of A (up to 16 MT tokens) against all of B, one launch: bound by
+// reading B once. A workgroup of 8 waves takes 16 columns of a k-contiguous B
+// or 32 of the other and all of K; the waves take its slices of 64 in turn,
+// each through a ring of its own in LDS (no barriers: a wave waits for its own
+// loads), 16 to 18 KB a wave on the way. Their sums meet in LDS, in wave order.
+template <typename T, bool BKC, int MT>
+__global__ __launch_bounds__(512) void k_skinny(const GemmArgs g) {
+    constexpr int TNS = BKC ? 16 : 32;       // columns
+    constexpr int WB = TNS * 128;            // bytes of a slice of B
+    constexpr int XB = MT * 2048;            // and of A
+    constexpr int STAGE = WB + XB;
+    constexpr int NI = STAGE / 1024;         // load instructions per slice
+    constexpr int R = BKC && MT == 1 ? 4 : BKC || MT == 1 ? 3 : 2;  // slices in a wave's ring
+    __shared__ __attribute__((aligned(16))) char smem[8 * R * STAGE];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int j0 = per_xcd(blockIdx.x, gridDim.x) * TNS;
+    char* const ring = smem + wave * R * STAGE;
+    const uint32_t lring = (uint32_t)(uintptr_t)(LDS_AS char*)ring;
+
+    // B, k-contiguous: 8 rows (columns of C) of 8 chunks per instruction, chunk
+    // c of row r at c ^ (r & 7); else 16 rows (k) of 4 chunks, chunk c of row r
+    // at c ^ (2 (r >> 3 & 1)). A: 8 rows of 8 chunks, as the former.
+    const uint32_t rowb = (uint32_t)g.ld_b * 2u, rowa = (uint32_t)g.ld_a * 2u;
+    const int r8 = lane >> 3, c8 = (lane & 7) ^ (r8 & 7);
+    uint32_t offw[WB / 1024], offx[XB / 1024];
+    u32x4 rw, rx;
+    uint32_t tail = 0;
+    const int rows = g.N - j0 < TNS ? g.N - j0 : TNS;
+    if constexpr (BKC) {
+#pragma unroll
+        for (int q = 0; q < WB / 1024; ++q)
+            offw[q] = r8 + 8 * q < rows ? (uint32_t)(r8 + 8 * q) * rowb + (uint32_t)c8 * 16u : OUT;
+        rw = rsrc(static_cast<const char*>(g.b) + (int64_t)j0 * rowb, (uint32_t)(rows - 1) * rowb + (uint32_t)g.kp * 2u);
+    } else {
+        const int r4 = lane >> 2, c4 = (lane & 3) ^ (2 * (r4 >> 3 & 1));
+        const int cols = g.np - j0 < TNS ? g.np - j0 : TNS;
+        tail = (uint32_t)cols * 2u;
+#pragma unroll
+        for (int q = 0; q < WB / 1024; ++q)
+            offw[q] = c4 * 8 < cols ? (uint32_t)(r4 + 16 * q) * rowb + (uint32_t)c4 * 16u : OUT;
+        rw = rsrc(g.b, 0u);
+    }
+#pragma unroll
+    for (int q = 0; q < XB / 1024; ++q)
+        offx[q] = r8 + 8 * q < g.M ? (uint32_t)(r8 + 8 * q) * rowa + (uint32_t)c8 * 16u : OUT;
+    rx = rsrc(g.a, (uint32_t)(g.M - 1) * rowa + (uint32_t)g.kp * 2u);
+
+    auto load = [&](int slice, uint32_t dst) {
+        const int k0 = slice * BK;
+        const uint32_t so = k0 < g.kp ? (uint32_t)k0 * 2u : 0u;
+        const uint32_t dead = c8 * 8 < g.kp - k0 ? 0u : OUT;
+        if constexpr (BKC) {
+#pragma unroll
+            for (int q = 0; q < WB / 1024; ++q) load_lds(rw, dst + q * 1024, offw[q] | dead, so);
+        } else {
+            const int left = g.K - k0;
+            const u32x4 r = rsrc(static_cast<const char*>(g.b) + (left > 0 ? (int64_t)k0 * rowb : 0) + (int64_t)j0 * 2,
+                                 left >= BK ? (uint32_t)(BK - 1) * rowb + tail
+                                            : left > 0 ? (uint32_t)(left - 1) * rowb + tail : 0u);
+#pragma unroll
+            for (int q = 0; q < WB / 1024; ++q) load_lds(r, dst + q * 1024, offw[q], 0u);
+        }
+#pragma unroll
+        for (int q = 0; q < XB / 1024; ++q) load_lds(rx, dst + WB + q * 1024, offx[q] | dead, so);
+    };
+
+    f32x4 acc[TNS / 16][MT];
+#pragma unroll
+    for (int a = 0; a < TNS / 16; ++a)
+#pragma unroll
+        for (int b = 0; b < MT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int l16 = lane & 15, g16 = lane >> 4;
+    const int mine = (g.slices - wave + 7) / 8;  // slices wave, wave + 8, ...
+#pragma unroll
+    for (int k = 0; k < R - 1; ++k) load(wave + 8 * k, lring + k * STAGE);
+    int at = 0;
+    for (int i = 0; i < mine; ++i) {
+        // the buffer read last turn takes the slice R - 1 ahead: its reads have
+        // returned (their products were issued), and none moves across here
+        int to = at + R - 1;
+        if (to >= R) to -= R;
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        load(wave + 8 * (i + R - 1), lring + to * STAGE);
+        wait_vm<(R - 1) * NI>();
+        asm volatile("" ::: "memory");
+        const char* S = ring + at * STAGE;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            typename V8<T>::type wf[TNS / 16], xf[MT];
+#pragma unroll
+            for (int h = 0; h < TNS / 16; ++h) {
+                if constexpr (BKC) {
+                    wf[h] = *reinterpret_cast<const typename V8<T>::type*>(S + l16 * 128 + 16 * ((4 * ks + g16) ^ (l16 & 7)));
+                } else {
+                    const int row = 32 * ks + 8 * g16 + (l16 >> 2);
+                    const char* p = S + row * 64 + 32 * (h ^ (g16 & 1)) + 8 * (l16 & 3);
+                    const bf16x4 lo = tr_read(p), up = tr_read(p + 4 * 64);
+                    wf[h] = __builtin_bit_cast(typename V8<T>::type, __builtin_shufflevector(lo, up, 0, 1, 2, 3, 4, 5, 6, 7));
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                xf[m] = *reinterpret_cast<const typename V8<T>::type*>(S + WB + (m * 16 + l16) * 128 +
+                                                                       16 * ((4 * ks + g16) ^ (l16 & 7)));
+#pragma unroll
+            for (int h = 0; h < TNS / 16; ++h)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) acc[h][m] = mfma16<T>(wf[h], xf[m], acc[h][m]);
+        }
+        at = at + 1 == R ? 0 : at + 1;
+    }
+    wait_vm0();  // the loads past the end
+    asm volatile("" ::: "memory");
+
+    // lane holds C[token l16 + 16 m][column 16 h + 4 g16 .. +3]; each wave's
+    // [16 MT][TNS] sums go into its own ring
+    float* const own = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int h = 0; h < TNS / 16; ++h)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            *reinterpret_cast<f32x4*>(own + (m * 16 + l16) * TNS + 16 * h + 4 * g16) = acc[h][m];
+    __syncthreads();
+    const int row = threadIdx.x / (TNS / 8), c = threadIdx.x % (TNS / 8) * 8;
+    const int col = j0 + c, left = g.N - col;
+    if (row >= g.M || left <= 0) return;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        const f32x4* p = reinterpret_cast<const f32x4*>(smem + w * R * STAGE + (row * TNS + c) * 4);
+        const f32x4 lo = p[0], up = p[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] += lo[e];
+            v[4 + e] += up[e];
+        }
+    }
+    float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (g.epi.bias) load8(g.epi.bias + col, left, bias);
+    u32x4 in = {0, 0, 0, 0};
+    if (left >= 8) in = fetch8<T>(g.epi, row, col);
+    finish8<T>(g.epi, row, col, left, v, bias, in);
+}
+
 // Rows of any alignment and length to 16-byte aligned, zero-padded ones: one
 // 16-byte chunk per thread.
 __global__ __launch_bounds__(256) void k_pack(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
@@ -507,6 +713,15 @@ hipError_t gemm_t(const GemmArgs& g, bool a_kc, bool b_kc, int sum, hipStream_t 
     return hipGetLastError();
 }
 
+template <typename T, int MT>
+hipError_t skinny_t(const GemmArgs& g, bool b_kc, hipStream_t st) {
+    if (b_kc)
+        k_skinny<T, true, MT><<<(g.N + 15) / 16, 512, 0, st>>>(g);
+    else
+        k_skinny<T, false, MT><<<(g.N + 31) / 32, 512, 0, st>>>(g);
+    return hipGetLastError();
+}
+
 template <typename T, int TM, int GS>
 void join_gs(const GemmArgs& g, int sum, hipStream_t st) {
     const int grid = (g.tiles_m * g.tiles_n - g.whole) * (TM * 16 * GS / 256);
@@ -538,6 +753,11 @@ hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int 
 hipError_t launch_gemm_join(const GemmArgs& g, int tile_m, int dtype, int sum, hipStream_t st) {
     if (dtype == 0) return tile_m == 256 ? join_t<bf16, 256>(g, sum, st) : join_t<bf16, 128>(g, sum, st);
     return tile_m == 256 ? join_t<f16, 256>(g, sum, st) : join_t<f16, 128>(g, sum, st);
+}
+
+hipError_t launch_skinny(const GemmArgs& g, bool b_kc, int dtype, hipStream_t st) {
+    if (dtype == 0) return g.M <= 16 ? skinny_t<bf16, 1>(g, b_kc, st) : skinny_t<bf16, 2>(g, b_kc, st);
+    return g.M <= 16 ? skinny_t<f16, 1>(g, b_kc, st) : skinny_t<f16, 2>(g, b_kc, st);
 }
 
 hipError_t launch_pack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t cols_pad,

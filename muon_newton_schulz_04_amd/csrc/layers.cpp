@@ -231,7 +231,10 @@ muon_status plan_product(const muon_linear& d, int op, const void* pa, const voi
     // launches hold fewer than 2^32 threads
     if (((P->M + 127) / 128) * ((P->N + 127) / 128) >= (int64_t)1 << (P->N % 8 == 0 ? 22 : 18))
         return fail(MUON_E_SHAPE, "linear: output too large");
-    P->plan = choose_plan(P->M, P->N, P->K, P->N % 8 == 0);
+    if (op != MUON_LINEAR_GRAD_WEIGHT && P->M <= muon::kSkinnyRows)
+        P->plan = {0, 0, 0, (int)((P->K + muon::kGemmSlice - 1) / muon::kGemmSlice), 0, 0, 0};
+    else
+        P->plan = choose_plan(P->M, P->N, P->K, P->N % 8 == 0);
     size_t o = 0;
     P->off_a = o;
     if (P->pack_a) o = up256(o + (size_t)P->a.rows * up8(P->a.cols) * 2);
@@ -279,6 +282,7 @@ muon_status run_product(Product& P, int dtype, muon::Epilogue& E, float* sums, i
     g.sums = sums;
     g.sum_part = reinterpret_cast<float*>(ws + P.off_sums);
     g.epi = E;
+    if (G.tile_m == 0) return hip_status(muon::launch_skinny(g, P.b_kc, dtype, st), "product kernel");
     TRY(hip_status(muon::launch_gemm(g, G.tile_m, P.a_kc, P.b_kc, dtype, sum, st), "product kernel"));
     if (G.whole < G.tiles_m * G.tiles_n) TRY(hip_status(muon::launch_gemm_join(g, G.tile_m, dtype, sum, st), "join kernel"));
     return MUON_OK;

@@ -50,15 +50,18 @@ struct GemmArgs {
 
 constexpr int kGemmSlice = 64;  // K per pipeline stage
 constexpr int kGemmTileN = 128;
+constexpr int kSkinnyRows = 32;
 
 struct GemmPlan {
-    int tile_m;  // 256 or 128; tiles are 128 wide
+    int tile_m;  // 256 or 128, tiles are 128 wide; 0: the kernel for up to kSkinnyRows rows of A
     int tiles_m, tiles_n, slices, whole, splits, per;
 };
 
 // sum: the bias gradient is the sums over k of neither (0), B's (1) or A's (2) rows
 hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int dtype, int sum, hipStream_t st);
 hipError_t launch_gemm_join(const GemmArgs& g, int tile_m, int dtype, int sum, hipStream_t st);
+// M <= kSkinnyRows, A k-contiguous
+hipError_t launch_skinny(const GemmArgs& g, bool b_kc, int dtype, hipStream_t st);
 // dst [rows, cols_pad] <- src [rows, cols] with row stride ld, zero-padded
 hipError_t launch_pack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t cols_pad,
                        hipStream_t st);

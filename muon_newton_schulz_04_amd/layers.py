@@ -76,12 +76,17 @@ def _check(status, what):
         raise B.MuonError(f"{what}: {B.muon_status_string(status)} ({B.muon_op_last_error()})")
 
 
+# the current stream's handle, without a Stream object around it where torch
+# offers that (1 us of a call's 10)
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _on(dev, fn, *args):
     """fn(*args, stream) on device `dev`'s current stream, with `dev` current."""
     if dev == torch.cuda.current_device():
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        return fn(*args, _stream(dev))
     with torch.cuda.device(dev):
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        return fn(*args, _stream(dev))
 
 
 def _workspace(nbytes, device):

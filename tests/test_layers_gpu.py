@@ -97,7 +97,8 @@ def _cpu64(t):
 # 256) and chunks (8), odd sizes (packed operands), K shorter than a slice,
 # long K with few outputs (split), more than one 256 tile
 SIZES = [(1, 1, 1), (1, 64, 48), (1, 1600, 400), (3, 8, 8), (5, 7, 9), (33, 40, 136), (127, 100, 129), (64, 333, 257),
-         (130, 1000, 264), (257, 96, 520), (300, 2048, 72), (17, 4104, 65), (600, 200, 640)]
+         (130, 1000, 264), (257, 96, 520), (300, 2048, 72), (17, 4104, 65), (600, 200, 640), (16, 1608, 96), (24, 6400, 200),
+         (32, 72, 1601)]
 
 
 @pytest.mark.parametrize("layout", ["in_out", "out_in"])
