@@ -396,12 +396,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
     float* const part = g.partial + (int64_t)piece * (TM * TN);
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (direct && g.epi.bias) load8(g.epi.bias + ccol, 8, bias);
-    u32x4 in0[NP], in1[NP], in2[NP];  // this block's, the next one's and the one's after that
+    // this block's first8, the next one's, and the one's after that or, where
+    // there is one, this block's second8
+    u32x4 in0[NP], in1[NP], in2[NP];
+    const bool second = direct && has_second(g.epi);
     auto fetch = [&](int fi, u32x4(&x)[NP]) {
 #pragma unroll
         for (int it = 0; it < NP; ++it) {
             const int row = row0 + 32 * fi + it * RPI;
-            x[it] = fetch8<T>(g.epi, row < g.M ? row : g.M - 1, ccol);
+            x[it] = first8<T>(g.epi, row < g.M ? row : g.M - 1, ccol);
         }
     };
     if (direct) {
@@ -426,7 +429,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
         });
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        if (direct && fi + 2 < FRI) fetch(fi + 2, in2);
+        if (second) {
+#pragma unroll
+            for (int it = 0; it < NP; ++it) {
+                const int row = row0 + 32 * fi + it * RPI;
+                in2[it] = second8<T>(g.epi, row < g.M ? row : g.M - 1, ccol);
+            }
+        } else if (direct && fi + 2 < FRI) {
+            fetch(fi + 2, in2);
+        }
 #pragma unroll
         for (int it = 0; it < NP; ++it) {
             const int row = row0 + 32 * fi + it * RPI;
@@ -435,7 +446,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
             if (row < g.M && inside) {
                 if (direct) {
                     float v[8] = {lo[0], lo[1], lo[2], lo[3], up[0], up[1], up[2], up[3]};
-                    finish8<T>(g.epi, row, col, 8, v, bias, in0[it]);
+                    finish8<T>(g.epi, row, col, 8, v, bias, in0[it], in2[it]);
                 } else {
                     float* p = part + (row - i0) * TN + (col - j0);
                     *reinterpret_cast<f32x4*>(p) = lo;
@@ -448,24 +459,31 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
             in0[it] = in1[it];
             in1[it] = in2[it];
         }
+        if (second && fi + 2 < FRI) fetch(fi + 2, in1);
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
     }
     if constexpr (SUM != 0) {
-        // one tile of each row or column of tiles, spread over them, and the
-        // two waves that hold it all
+        // the bias gradient: one tile of each row or column of tiles, spread
+        // over them, and the two waves that hold it all
         const bool mine = SUM == 1 ? ti == tj % g.tiles_m && wi == 0 : tj == ti % g.tiles_n && wj == 0;
         if (mine) {
+            const int at = (SUM == 1 ? wj * WN : wi * WM) + l32;
+            const int n = (SUM == 1 ? j0 : i0) + at, end = SUM == 1 ? g.N : g.M;
+            float old[NSUM];
 #pragma unroll
             for (int f = 0; f < NSUM; ++f) {
-                const float v = sums[f] + __shfl_xor(sums[f], 32, 64);
-                const int at = (SUM == 1 ? wj * WN : wi * WM) + 32 * f + l32;
-                const int n = (SUM == 1 ? j0 : i0) + at;
-                if (hi == 0 && n < (SUM == 1 ? g.N : g.M)) {
+                old[f] = 0.f;
+                if (direct && g.epi.accumulate && n + 32 * f < end) old[f] = g.sums[n + 32 * f];
+            }
+#pragma unroll
+            for (int f = 0; f < NSUM; ++f) {
+                const float v = old[f] + (sums[f] + __shfl_xor(sums[f], 32, 64));
+                if (hi == 0 && n + 32 * f < end) {
                     if (direct)
-                        g.sums[n] = g.epi.accumulate ? g.sums[n] + v : v;
+                        g.sums[n + 32 * f] = v;
                     else
-                        g.sum_part[(int64_t)piece * 256 + at] = v;
+                        g.sum_part[(int64_t)piece * 256 + at + 32 * f] = v;
                 }
             }
         }
@@ -517,9 +535,12 @@ __global__ __launch_bounds__(256) void k_gemm_join(const GemmArgs g) {
     const int left = g.N - col;
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (g.epi.bias) load8(g.epi.bias + col, left, bias);
-    u32x4 in = {0, 0, 0, 0};
-    if (left >= 8) in = fetch8<T>(g.epi, row, col);
-    finish8<T>(g.epi, row, col, left, v, bias, in);
+    u32x4 in = {0, 0, 0, 0}, in2 = in;
+    if (left >= 8) {
+        in = first8<T>(g.epi, row, col);
+        if (has_second(g.epi)) in2 = second8<T>(g.epi, row, col);
+    }
+    finish8<T>(g.epi, row, col, left, v, bias, in, in2);
 }
 
 template <typename T>
@@ -673,26 +694,30 @@ __global__ __launch_bounds__(512) void k_skinny(const GemmArgs g) {
     }
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (g.epi.bias) load8(g.epi.bias + col, left, bias);
-    u32x4 in = {0, 0, 0, 0};
-    if (left >= 8) in = fetch8<T>(g.epi, row, col);
-    finish8<T>(g.epi, row, col, left, v, bias, in);
+    u32x4 in = {0, 0, 0, 0}, in2 = in;
+    if (left >= 8) {
+        in = first8<T>(g.epi, row, col);
+        if (has_second(g.epi)) in2 = second8<T>(g.epi, row, col);
+    }
+    finish8<T>(g.epi, row, col, left, v, bias, in, in2);
 }
 
 // Rows of any alignment and length to 16-byte aligned, zero-padded ones: one
-// 16-byte chunk per thread.
-__global__ __launch_bounds__(256) void k_pack(const uint16_t* __restrict__ src, int64_t ld, int64_t rows, int64_t cols,
-                                              u32x4* __restrict__ dst, int64_t chunks) {
-    const int64_t n = rows * chunks;
+// 16-byte chunk per thread; one operand or both in a launch.
+__global__ __launch_bounds__(256) void k_pack(const PackArgs a, const PackArgs b) {
+    const PackArgs& p = blockIdx.y ? b : a;
+    const int64_t n = p.rows * p.chunks;
     for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < n; id += (int64_t)gridDim.x * 256) {
-        const int64_t r = id / chunks, c = (id - r * chunks) * 8;
-        const uint16_t* p = src + r * ld + c;
-        if (c + 8 <= cols) {
-            dst[id] = *reinterpret_cast<const u32x4_mem*>(p);
+        const int64_t r = id / p.chunks, c = (id - r * p.chunks) * 8;
+        const uint16_t* s = static_cast<const uint16_t*>(p.src) + r * p.ld + c;
+        u32x4* d = static_cast<u32x4*>(p.dst) + id;
+        if (c + 8 <= p.cols) {
+            *d = *reinterpret_cast<const u32x4_mem*>(s);
         } else {
             uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = c + e < cols ? p[e] : 0u;
-            dst[id] = u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+            for (int e = 0; e < 8; ++e) w[e] = c + e < p.cols ? s[e] : 0u;
+            *d = u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
         }
     }
 }
@@ -760,13 +785,12 @@ hipError_t launch_skinny(const GemmArgs& g, bool b_kc, int dtype, hipStream_t st
     return g.M <= 16 ? skinny_t<f16, 1>(g, b_kc, st) : skinny_t<f16, 2>(g, b_kc, st);
 }
 
-hipError_t launch_pack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t cols_pad,
-                       hipStream_t st) {
-    if (rows == 0) return hipSuccess;
-    const int64_t n = rows * (cols_pad / 8);
-    const int64_t blocks = (n + 255) / 256;
-    k_pack<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(static_cast<const uint16_t*>(src), ld, rows,
-                                                                        cols, static_cast<u32x4*>(dst), cols_pad / 8);
+hipError_t launch_pack(const PackArgs* p, int n, hipStream_t st) {
+    int64_t most = 0;
+    for (int k = 0; k < n; ++k) most = p[k].rows * p[k].chunks > most ? p[k].rows * p[k].chunks : most;
+    if (most == 0) return hipSuccess;
+    const int64_t blocks = (most + 255) / 256;
+    k_pack<<<dim3((unsigned)(blocks < 32768 ? blocks : 32768), (unsigned)n), 256, 0, st>>>(p[0], p[n - 1]);
     return hipGetLastError();
 }
 

@@ -193,12 +193,12 @@ __device__ __forceinline__ void act_slopes(int act, float (&v)[8]) {
 }
 #undef MUON_ACT_CASE
 
-// What the epilogue reads first of a chunk of 8 outputs, fetched ahead of its
-// use as a 16-byte vector: z on the way back through an activation, else add;
-// or half of the weight gradient to add to. (A call with z and add both, and
-// the other half, read the rest in place.)
+// What the epilogue reads of a chunk of 8 outputs, fetched ahead of its use as
+// 16-byte vectors: first8 is z on the way back through an activation, else
+// add, or the lower half of a weight gradient to add to; second8 is add where
+// first8 is z, or the upper half.
 template <typename T>
-__device__ __forceinline__ u32x4 fetch8(const Epilogue& E, int64_t r, int64_t c) {
+__device__ __forceinline__ u32x4 first8(const Epilogue& E, int64_t r, int64_t c) {
     const void* p = nullptr;
     if (E.mode == EPI_GRAD_WEIGHT) {
         if (E.accumulate) p = static_cast<const float*>(E.y) + r * E.ld_y + c;
@@ -209,6 +209,16 @@ __device__ __forceinline__ u32x4 fetch8(const Epilogue& E, int64_t r, int64_t c)
     }
     return p ? *static_cast<const u32x4_mem*>(p) : u32x4{0, 0, 0, 0};
 }
+__device__ __forceinline__ bool has_second(const Epilogue& E) {
+    return E.mode == EPI_GRAD_WEIGHT ? E.accumulate != 0 : E.mode == EPI_GRAD_INPUT && E.act != ACT_NONE && E.add;
+}
+template <typename T>
+__device__ __forceinline__ u32x4 second8(const Epilogue& E, int64_t r, int64_t c) {
+    const void* p = E.mode == EPI_GRAD_WEIGHT
+                        ? static_cast<const void*>(static_cast<const float*>(E.y) + r * E.ld_y + c + 4)
+                        : static_cast<const void*>(static_cast<const T*>(E.add) + r * E.ld_add + c);
+    return *static_cast<const u32x4_mem*>(p);
+}
 
 template <typename T>
 __device__ __forceinline__ void widen8(const u32x4& u, float (&v)[8]) {
@@ -218,17 +228,17 @@ __device__ __forceinline__ void widen8(const u32x4& u, float (&v)[8]) {
 }
 
 // The epilogue of 8 consecutive accumulators of row r from column c on, n of
-// them inside the matrix. bias: their bias values (forward). in: fetch8's if n
-// is 8 or more; a chunk at the matrix's edge is read in place.
+// them inside the matrix. bias: their bias values (forward). in, in2: first8's
+// and second8's if n is 8 or more; a chunk at the matrix's edge is read in place.
 template <typename T>
 __device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c, int n, float (&v)[8],
-                                        const float (&bias)[8], const u32x4& in) {
+                                        const float (&bias)[8], const u32x4& in, const u32x4& in2) {
     float t[8];
     if (E.mode == EPI_GRAD_WEIGHT) {
         float* y = static_cast<float*>(E.y) + r * E.ld_y + c;
         if (E.accumulate) {
             if (n >= 8) {
-                const f32x4 lo = __builtin_bit_cast(f32x4, in), up = *reinterpret_cast<const f32x4_mem*>(y + 4);
+                const f32x4 lo = __builtin_bit_cast(f32x4, in), up = __builtin_bit_cast(f32x4, in2);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     t[e] = lo[e];
@@ -243,7 +253,7 @@ __device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c,
         stream8(y, n, v);
         return;
     }
-    bool fetched = false;  // `in` was z, not add
+    bool fetched = false;  // `in` was z, and add is in2
     if (E.mode == EPI_FORWARD) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += bias[e];
@@ -260,7 +270,9 @@ __device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c,
         for (int e = 0; e < 8; ++e) v[e] *= t[e];
     }
     if (E.add) {
-        if (n >= 8 && !fetched)
+        if (n >= 8 && fetched)
+            widen8<T>(in2, t);
+        else if (n >= 8)
             widen8<T>(in, t);
         else
             load8(static_cast<const T*>(E.add) + r * E.ld_add + c, n, t);

@@ -154,9 +154,14 @@ Tensor tensor_w(const muon_linear& d, const void* p, int size) {
 
 // How an M x N x K product is cut: tile height, how many tiles run whole, and
 // in how many K pieces the others go. Each candidate is priced in clocks (2.4
-// GHz): slice costs of a workgroup alone on its CU and beside a second one,
-// what it spends outside its main loop, the join's traffic and launch, and
-// the rate at which the whole chip multiplies however it is filled.
+// GHz) with constants fitted to measured times (both tiles, one piece to 24,
+// 21 shapes: the choice was within 3% of the best everywhere but on shapes
+// under 20 us, within 10%): a slice of a workgroup alone on its CU and beside a
+// second one, launch and all that a workgroup does outside its main loop, the
+// join's launch and traffic, and the rate at which the whole chip multiplies
+// however it is filled. For instance 4096 x 1600 x 1600: tall tiles 33 us,
+// square ones 38; 1024 x 1600 x 1600: 29 and 20; 6400 x 1600 weight gradient
+// over 8192 tokens: 157 us with pieces beside whole tiles, 208 without.
 // direct: the product kernel can finish whole tiles (N is a multiple of 8).
 muon::GemmPlan choose_plan(int64_t M, int64_t N, int64_t K, bool direct) {
     int64_t slices = (K + muon::kGemmSlice - 1) / muon::kGemmSlice;
@@ -166,35 +171,32 @@ muon::GemmPlan choose_plan(int64_t M, int64_t N, int64_t K, bool direct) {
     for (int tm : {256, 128}) {
         const int64_t tiles_m = (M + tm - 1) / tm, tiles_n = (N + muon::kGemmTileN - 1) / muon::kGemmTileN;
         const int64_t tiles = tiles_m * tiles_n;
-        const double alone = tm == 256 ? 2100 : 1300, beside = tm == 256 ? 3500 : 2200,
-                     fixed = tm == 256 ? 9000 : 6000;
-        const double chip = (double)tiles * (double)slices * (tm == 256 ? 8.8 : 5.5);
+        // two tall workgroups share a CU, a square one fills it: a second one
+        // there starts once the first is done
+        const double alone = tm == 256 ? 2200 : 1140, beside = tm == 256 ? 3700 : 2 * alone,
+                     fixed = tm == 256 ? 23000 : 18000, next = tm == 256 ? 5000 : 12000;
+        const double chip = (double)tiles * (double)slices * (tm == 256 ? 8.0 : 5.5);
         auto rounds = [&](int64_t wgs, double per) {
-            const int64_t rest = wgs % 512;
-            return (double)(wgs / 512) * (per * beside + fixed) +
-                   (rest == 0 ? 0.0 : per * (rest > 256 ? beside : alone) + fixed);
+            const int64_t rest = wgs % 512, full = tm == 256 ? 512 : 256;
+            return fixed + next * (double)((wgs - 1) / full) + per * ((double)(wgs / 512) * beside + (rest == 0 ? 0.0 : rest > 256 ? beside : alone));
         };
         auto consider = [&](double t, int64_t whole, int64_t splits, int64_t per) {
             if (t < chip) t = chip;
             if (whole < tiles)
-                t += 8.0 * (double)((tiles - whole) * splits) * (double)(M < tm ? M : tm) * 128.0 / 2300.0 + 7000.0;
+                t += 8.0 * (double)((tiles - whole) * splits) * (double)(M < tm ? M : tm) * 128.0 / 2300.0 + 11000.0;
             if (t >= best_t) return;
             best_t = t;
             best = {tm, (int)tiles_m, (int)tiles_n, (int)slices, (int)whole, (int)splits, (int)per};
         };
-        if (direct)
-            consider(rounds(tiles, (double)slices), tiles, 1, slices);
-        else
-            consider(rounds(tiles, (double)slices), 0, 1, slices);
+        consider(rounds(tiles, (double)slices), direct ? tiles : 0, 1, slices);
         for (int64_t s = 2; s <= 64 && s <= slices; ++s) {
             const int64_t per = (slices + s - 1) / s;
             if ((slices + per - 1) / per != s) continue;  // every piece has work
             if (tiles * s <= 1024) consider(rounds(tiles * s, (double)per), 0, s, per);
-            // one tile a CU and the rest of a round in pieces beside them
+            // one tall tile a CU and the rest of a round in pieces beside them
             const int64_t rest = tiles % 512 - 256, n = (rest * s + 255) / 256;
-            if (direct && rest > 0 && n * per <= slices)
-                consider((double)(tiles / 512) * ((double)slices * beside + fixed) + (double)(n * per) * beside +
-                             (double)(slices - n * per) * alone + 2 * fixed,
+            if (direct && tm == 256 && rest > 0 && n * per <= slices)
+                consider(fixed + (double)(tiles / 512 * slices + n * per) * beside + (double)(slices - n * per) * alone,
                          tiles - rest, s, per);
         }
     }
@@ -252,14 +254,17 @@ muon_status plan_product(const muon_linear& d, int op, const void* pa, const voi
 
 // sums (bias gradient) and sum: see GemmArgs and launch_gemm
 muon_status run_product(Product& P, int dtype, muon::Epilogue& E, float* sums, int sum, char* ws, hipStream_t st) {
+    muon::PackArgs packs[2];
+    int n = 0;
     for (int k = 0; k < 2; ++k) {
         Tensor& t = k ? P.b : P.a;
         if (!(k ? P.pack_b : P.pack_a)) continue;
         char* dst = ws + (k ? P.off_b : P.off_a);
-        TRY(hip_status(muon::launch_pack(t.p, t.ld, t.rows, t.cols, dst, up8(t.cols), st), "pack kernel"));
+        packs[n++] = {t.p, t.ld, t.rows, t.cols, dst, up8(t.cols) / 8};
         t.p = dst;
         t.ld = up8(t.cols);
     }
+    if (n) TRY(hip_status(muon::launch_pack(packs, n, st), "pack kernel"));
     const muon::GemmPlan& G = P.plan;
     muon::GemmArgs g{};
     g.a = P.a.p;

@@ -62,9 +62,16 @@ hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int 
 hipError_t launch_gemm_join(const GemmArgs& g, int tile_m, int dtype, int sum, hipStream_t st);
 // M <= kSkinnyRows, A k-contiguous
 hipError_t launch_skinny(const GemmArgs& g, bool b_kc, int dtype, hipStream_t st);
-// dst [rows, cols_pad] <- src [rows, cols] with row stride ld, zero-padded
-hipError_t launch_pack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t cols_pad,
-                       hipStream_t st);
+// dst [rows, 8 chunks] <- src [rows, cols] of 16-bit elements with row stride
+// ld, zero-padded; n (1 or 2) of them in a launch
+struct PackArgs {
+    const void* src;
+    int64_t ld, rows, cols;
+    void* dst;
+    int64_t chunks;
+};
+hipError_t launch_pack(const PackArgs* p, int n, hipStream_t st);
+
 struct NormArgs {
     int64_t rows;
     int32_t cols;
