@@ -197,3 +197,388 @@ def test_layernorm_sizes(rows, cols, dtype):
     n = (8 + 4 * math.sqrt(max(rows, 1))) * u
     _close(dw, (d64 * xh).sum(0), n * (d64 * xh).abs().sum(0) + (d64.abs() * xht).sum(0), torch.float32)
     _close(db, d64.sum(0), n * d64.abs().sum(0), torch.float32)
+
+
+def _flat(n, fill, offset, dtype):
+    """A vector that starts `offset` elements into its allocation."""
+    return torch.full((n + offset,), fill, dtype=dtype, device="cuda")[offset:]
+
+
+@pytest.mark.parametrize("size", [(40, 64, 72), (7, 33, 50), (200, 136, 264)], ids=str)
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+def test_linear_strides_and_alignment(size, layout):
+    """Strided rows whose gaps hold NaN on the way in and must stay as they
+    were on the way out, and tensors that start off a 16-byte border; the
+    results are the packed, aligned call's, bit for bit."""
+    n, i, o = size
+    t = torch.bfloat16
+    g = _gen(o)
+
+    def off(r, c, src, dtype=t, pad=3):
+        buf = _flat(r * (c + pad), float("nan"), 1, dtype).view(r, c + pad)
+        buf[:, :c] = src
+        return buf, buf[:, :c]
+
+    wr, wc = (i, o) if layout == "in_out" else (o, i)
+    x0, w0, dy0 = _rand(g, (n, i), t), _rand(g, (wr, wc), t, std=i ** -0.5), _rand(g, (n, o), t, std=0.1)
+    res0, pre0 = _rand(g, (n, o), t), _rand(g, (n, i), t)
+    bias = torch.randn(o, generator=g).cuda()
+    x, w, dy, res, pre = (off(*s.shape, s)[1] for s in (x0, w0, dy0, res0, pre0))
+    kw = {"weight_layout": layout}
+    want = L.linear_forward(x0, w0, bias=bias, residual=res0, activation="silu", save_preact=True, **kw)
+    yb, y = off(n, o, 0)
+    zb, z = off(n, o, 0, pad=5)
+    L.linear_forward(x, w, bias=bias, residual=res, activation="silu", out=y, preact_out=z, **kw)
+    assert torch.equal(y, want[0]) and torch.equal(z, want[1])
+    assert yb[:, o:].isnan().all() and zb[:, o:].isnan().all()
+    # in place over the residual
+    L.linear_forward(x, w, bias=bias, residual=res, activation="silu", out=res, **kw)
+    assert torch.equal(res, want[0])
+    dxb, dx = off(n, i, 0)
+    L.linear_grad_input(dy, w, preact=pre, activation="silu", out=dx, **kw)
+    assert torch.equal(dx, L.linear_grad_input(dy0, w0, preact=pre0, activation="silu", **kw))
+    assert dxb[:, i:].isnan().all()
+    dwb, dw = off(wr, wc, 0, torch.float32)
+    db = _flat(o, 0.0, 1, torch.float32)
+    L.linear_grad_weight(x, dy, dw=dw, dbias=db, **kw)
+    want = L.linear_grad_weight(x0, dy0, dbias=True, **kw)
+    assert torch.equal(dw, want[0]) and torch.equal(db, want[1])
+    assert dwb[:, wc:].isnan().all()
+    # a second call adds the same again
+    L.linear_grad_weight(x, dy, dw=dw, dbias=db, accumulate=True, **kw)
+    assert torch.equal(dw, 2 * want[0]) and torch.equal(db, 2 * want[1])
+
+
+@pytest.mark.parametrize("size", [(300, 520, 1600), (3000, 264, 136), (2051, 768, 1024)], ids=str)
+def test_linear_accumulate(size):
+    """The gradients of two halves of a batch add up to the batch's, to the
+    sums' own rounding, in whole tiles and in pieces."""
+    n, i, o = size
+    g = _gen(n)
+    x, dy = _rand(g, (n, i), torch.float16), _rand(g, (n, o), torch.float16, std=0.1)
+    h = n // 3
+    dw, db = L.linear_grad_weight(x[:h], dy[:h], dbias=True)
+    L.linear_grad_weight(x[h:], dy[h:], dw=dw, dbias=db, accumulate=True)
+    a, b = _cpu64(x).t(), _cpu64(dy)
+    _close(dw, a @ b, _sum_tol(a, b), torch.float32)
+    ones = torch.ones(1, n, dtype=torch.float64)
+    _close(db, b.sum(0), _sum_tol(ones, b)[0], torch.float32)
+
+
+def test_no_tokens():
+    x, w = torch.empty(0, 24, dtype=torch.bfloat16, device="cuda"), torch.ones(24, 40, dtype=torch.bfloat16).cuda()
+    dy = torch.empty(0, 40, dtype=torch.bfloat16, device="cuda")
+    assert L.linear_forward(x, w).shape == (0, 40) and L.linear_grad_input(dy, w).shape == (0, 24)
+    for layout in ("in_out", "out_in"):
+        dw = torch.full((24, 40) if layout == "in_out" else (40, 24), 3.0, device="cuda")
+        db = torch.full((40,), 3.0, device="cuda")
+        L.linear_grad_weight(x, dy, dw=dw, dbias=db, accumulate=True, weight_layout=layout)
+        assert (dw == 3).all() and (db == 3).all()
+        L.linear_grad_weight(x, dy, dw=dw, dbias=db, weight_layout=layout)
+        assert (dw == 0).all() and (db == 0).all()
+    e = torch.empty(0, device="cuda")
+    dw = torch.full((40,), 3.0, device="cuda")
+    L.layernorm_backward(dy, dy, e, e, dweight=dw, dbias=True, accumulate=False)
+    assert (dw == 0).all()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_extreme_values(act):
+    """Activations and slopes at zeros, the types' largest values, infinities
+    and NaN: a product with one nonzero term carries them through exactly."""
+    v = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 2.5, -2.5, 9.0, -9.0, 40.0, -40.0, 1e30, -1e30, float("inf"),
+                      float("nan"), -3e38, 3e38]).to(torch.bfloat16)
+    z = v.double()
+    x = torch.zeros(len(v), 64, dtype=torch.bfloat16)
+    x[:, 0] = v
+    w = torch.zeros(64, 64, dtype=torch.bfloat16)
+    w[0, :] = 1
+    for rows in (len(v), 10 * len(v)):  # both product kernels
+        y = L.linear_forward(x.repeat(rows // len(v), 1).cuda(), w.cuda(), activation=act)[:len(v), 5].double().cpu()
+        want = act64(act, z)
+        ok = want.isfinite()
+        # an overflowing square is an infinity in bf16 and in float32
+        big = ok & (want.abs() > torch.finfo(torch.bfloat16).max)
+        assert (y[big] == want[big].sign() * math.inf).all()
+        ok &= ~big
+        assert ((y - want)[ok].abs() <= want[ok].abs() * 2.0 ** -8 + 2.0 ** -20 * z[ok].abs().clamp(max=40)).all()
+        assert y[13].isnan() and y[12] == math.inf
+        dy = torch.zeros(rows, 64, dtype=torch.bfloat16)
+        dy[:, 0] = 1
+        wt = torch.zeros(64, 64, dtype=torch.bfloat16)
+        wt[:, 0] = 1
+        pre = v.repeat(rows // len(v))[:, None].expand(-1, 64).contiguous()
+        s = L.linear_grad_input(dy.cuda(), wt.cuda(), preact=pre.cuda(), activation=act)[:len(v), 9].double().cpu()
+        fin = z.isfinite()
+        zs = z[fin].clamp(-1e4, 1e4)  # slopes are flat (relu2: linear) beyond, and the formulas' cubes overflow
+        want = slope64(act, zs) if act != "relu2" else 2 * z[fin].clamp(min=0)
+        over = want > torch.finfo(torch.bfloat16).max
+        assert (s[fin][over] == math.inf).all()
+        assert ((s[fin] - want)[~over].abs() <= want[~over].abs() * 2.0 ** -8 + 2.0 ** -19).all()
+        assert act == "none" or s[13].isnan()
+
+
+def test_layernorm_extreme_rows():
+    """A constant row has variance 0; a NaN or an infinity spoils its row only."""
+    g = _gen(3)
+    x = torch.randn(6, 200, generator=g)
+    x[1] = 7.0
+    x[3, 17] = float("nan")
+    x[4, 5] = float("inf")
+    y, mean, rstd = L.layernorm_forward(x.cuda(), eps=1e-5)
+    y = y.cpu()
+    assert (y[1] == 0).all() and mean[1].item() == 7.0 and abs(rstd[1].item() - 1e-5 ** -0.5) < 1e-4
+    assert y[3].isnan().all() and y[4].isnan().all() and y[[0, 1, 2, 5]].isfinite().all()
+    dy = torch.randn(6, 200, generator=g).cuda()
+    dx, dw, _ = L.layernorm_backward(dy, x.cuda(), mean, rstd, dweight=True)
+    assert dx[[0, 1, 2, 5]].isfinite().all() and dx[3].isnan().all() and dw.isnan().all()
+
+
+@pytest.mark.parametrize("cols,dtype", [(136, "bf16"), (1003, "fp32"), (2500, "fp16"), (9001, "bf16")])
+def test_layernorm_strides_and_accumulate(cols, dtype):
+    t, rows = T[dtype], 37
+    g = _gen(cols)
+    x = _rand(g, (rows, cols), t, mean=1.0, stride=cols + 3)
+    w = _flat(cols, 0.0, 1, torch.float32).copy_(torch.randn(cols, generator=g))
+    yb = torch.full((rows, cols + 5), float("nan"), dtype=t, device="cuda")
+    y, mean, rstd = L.layernorm_forward(x, w, out=yb[:, :cols])
+    ref = L.layernorm_forward(x.contiguous(), w.clone())
+    assert torch.equal(y, ref[0]) and torch.equal(mean, ref[1]) and torch.equal(rstd, ref[2])
+    assert yb[:, cols:].isnan().all()
+    dy, add = _rand(g, (rows, cols), t, stride=cols + 1), _rand(g, (rows, cols), t, stride=cols + 7)
+    want = L.layernorm_backward(dy.contiguous(), x.contiguous(), mean, rstd, weight=w, add=add.contiguous(),
+                                dweight=True, dbias=True)
+    dw, db = want[1].clone(), want[2].clone()
+    L.layernorm_backward(dy, x, mean, rstd, weight=w, add=add, out=add, dweight=dw, dbias=db, accumulate=True)
+    assert torch.equal(add, want[0]) and torch.equal(dw, 2 * want[1]) and torch.equal(db, 2 * want[2])
+    # either gradient alone, or none
+    assert torch.equal(L.layernorm_backward(dy, x, mean, rstd, weight=w, dbias=True)[2], want[2])
+    assert L.layernorm_backward(dy, x, mean, rstd, weight=w)[1:] == (None, None)
+
+
+def _tiny_block(seed):
+    """Inputs and the calls of one pre-norm feed-forward half of a layer."""
+    g = _gen(seed)
+    n, d = 70, 128
+    s = {"x": _rand(g, (n, d), torch.bfloat16), "dout": _rand(g, (n, d), torch.bfloat16, std=0.1),
+         "w1": _rand(g, (d, 4 * d), torch.bfloat16, std=d ** -0.5),
+         "w2": _rand(g, (4 * d, d), torch.bfloat16, std=(4 * d) ** -0.5),
+         "b1": torch.randn(4 * d, generator=g).cuda(), "lw": torch.randn(d, generator=g).cuda(),
+         "grads": torch.zeros(8 * d * d, device="cuda"), "small": torch.zeros(6 * d, device="cuda")}
+
+    def run():
+        # the weights' gradients lie in the flat buffer that a Muon step reads: c_fc [d, 4d], then c_proj [4d, d]
+        g1, g2 = s["grads"][:4 * d * d].view(d, 4 * d), s["grads"][4 * d * d:].view(4 * d, d)
+        db1, dlw, dlb = s["small"][:4 * d], s["small"][4 * d:5 * d], s["small"][5 * d:]
+        h, mean, rstd = L.layernorm_forward(s["x"], s["lw"])
+        a, z = L.linear_forward(h, s["w1"], bias=s["b1"], activation="gelu_tanh", save_preact=True)
+        out = L.linear_forward(a, s["w2"], residual=s["x"])
+        dz = L.linear_grad_input(s["dout"], s["w2"], preact=z, activation="gelu_tanh")
+        L.linear_grad_weight(a, s["dout"], dw=g2)
+        dh = L.linear_grad_input(dz, s["w1"])
+        L.linear_grad_weight(h, dz, dw=g1, dbias=db1)
+        dx, _, _ = L.layernorm_backward(dh, s["x"], mean, rstd, weight=s["lw"], add=s["dout"], dweight=dlw, dbias=dlb)
+        return {"h": h, "mean": mean, "rstd": rstd, "a": a, "z": z, "out": out, "dz": dz, "dh": dh, "dx": dx,
+                "g1": g1, "g2": g2, "db1": db1, "dlw": dlw, "dlb": dlb}
+
+    return s, run
+
+
+def test_block_together_with_a_muon_step():
+    """The operators as a layer uses them, each result against the formula on
+    what the call before it stored, the whole gradient against differences of
+    the layer's loss in 64 bits, and the Muon step that reads the gradients."""
+    s, run = _tiny_block(11)
+    o = {k: v.double().cpu() for k, v in run().items()}
+    d = 128
+    x, w1, w2, b1, lw, dout = (_cpu64(s[k]) for k in ("x", "w1", "w2", "b1", "lw", "dout"))
+    bf, u = torch.bfloat16, 2.0 ** -24
+    xh = (x - x.mean(1, keepdim=True)) / (x.var(1, unbiased=False, keepdim=True) + 1e-5).sqrt()
+    _close(o["h"], xh * lw, 100 * u * (1 + xh.abs()) * lw.abs(), bf)
+    z = o["h"] @ w1 + b1
+    zt = _sum_tol(o["h"], w1) + 2 * u * z.abs()
+    _close(o["z"], z, zt, bf)
+    _close(o["a"], act64("gelu_tanh", z), 1.2 * zt + 16 * u * z.abs(), bf)
+    _close(o["out"], o["a"] @ w2 + x, _sum_tol(o["a"], w2) + u * 4 * x.abs(), bf)
+    raw, sl = dout @ w2.t(), slope64("gelu_tanh", o["z"])
+    _close(o["dz"], raw * sl, _sum_tol(dout, w2.t()) * sl.abs() + 16 * u * raw.abs() * (1 + o["z"].abs()), bf)
+    _close(o["dh"], o["dz"] @ w1.t(), _sum_tol(o["dz"], w1.t()), bf)
+    _close(o["g2"], o["a"].t() @ dout, _sum_tol(o["a"].t(), dout), torch.float32)
+    _close(o["g1"], o["h"].t() @ o["dz"], _sum_tol(o["h"].t(), o["dz"]), torch.float32)
+    _close(o["db1"], o["dz"].sum(0), _sum_tol(torch.ones(1, 70, dtype=torch.float64), o["dz"])[0], torch.float32)
+
+    def loss(x, w1, w2, b1, lw):
+        xh = (x - x.mean(1, keepdim=True)) / (x.var(1, unbiased=False, keepdim=True) + 1e-5).sqrt()
+        return ((act64("gelu_tanh", xh * lw @ w1 + b1) @ w2 + x) * dout).sum()
+
+    # a directional derivative's error is at most the stored gradients' (each
+    # bf16 intermediate rounded by up to 2^-8, three on the longest way) along the
+    # direction, in root mean square far less; 2^-6 of |gradient| |direction|
+    # is four times what the roundings can add up to in one sign
+    g = _gen(5)
+    at, grads = [x, w1, w2, b1, lw], [o["dx"], o["g1"], o["g2"], o["db1"], o["dlw"]]
+    for k in range(5):
+        v = [torch.zeros_like(t) for t in at]
+        # along the gradient itself (nothing cancels) and a random way beside it
+        v[k] = grads[k] / grads[k].norm() + 0.5 * torch.randn(at[k].shape, generator=g).double() / at[k].numel() ** 0.5
+        h = 1e-4
+        diff = (loss(*[a + h * b for a, b in zip(at, v)]) - loss(*[a - h * b for a, b in zip(at, v)])) / (2 * h)
+        got = (grads[k] * v[k]).sum()
+        assert abs(got - diff) <= 2.0 ** -6 * grads[k].norm() * v[k].norm(), (k, got, diff)
+
+    table = [B.muon_matrix(d, 4 * d, 1, 0, 1.0, 1.0, 0, 0), B.muon_matrix(4 * d, d, 1, 4 * d * d, 1.0, 1.0, 0, 0)]
+    params = torch.cat([s["w1"].float().flatten(), s["w2"].float().flatten()])
+    after = []
+    for grad in (s["grads"], s["grads"].clone()):
+        H = B.MuonHandle(table, B.make_hparams())
+        p, m = params.clone(), torch.zeros_like(params)
+        H.step(p, grad, m, lr=0.02)
+        torch.cuda.synchronize()
+        assert (H.view(B.MUON_VIEW_STATUS, torch.int32) == 0).all()
+        H.close()
+        after.append(p)
+    assert torch.equal(after[0], after[1]) and after[0].isfinite().all() and not torch.equal(after[0], params)
+
+
+def test_graph_replays_match_eager_calls():
+    s, run = _tiny_block(12)
+    run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    for k in range(4):
+        fresh, fresh_run = _tiny_block(20 + k)
+        for name in ("x", "dout", "w1", "w2", "b1", "lw"):
+            s[name].copy_(fresh[name])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {n: v.clone() for n, v in held.items()}
+        want = fresh_run()  # the program's own eager work between replays
+        for n in got:
+            assert torch.equal(got[n], want[n]), (k, n)
+
+
+def test_calls_on_two_streams_at_once():
+    pairs = [_tiny_block(31), _tiny_block(32)]
+    want = []
+    for s, run in pairs:
+        want.append({k: v.clone() for k, v in run().items()})
+        s["grads"].zero_()
+        s["small"].zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [None, None]
+    for _ in range(3):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[k] = pairs[k][1]()
+    torch.cuda.synchronize()
+    for k in range(2):
+        for n in want[k]:
+            assert torch.equal(got[k][n], want[k][n]), (k, n)
+
+
+@pytest.mark.parametrize("size", [(260, 1608, 136), (33, 95, 50), (999, 1001, 777)], ids=str)
+def test_workspace_holds_nothing_between_calls(size):
+    """The C calls on a workspace full of NaN, with guard bytes behind it."""
+    n, i, o = size
+    g = _gen(n)
+    x, w, dy = (_rand(g, s, torch.bfloat16) for s in ((n, i), (i, o), (n, o)))
+    want = {B.MUON_LINEAR_FORWARD: L.linear_forward(x, w), B.MUON_LINEAR_GRAD_INPUT: L.linear_grad_input(dy, w),
+            B.MUON_LINEAR_GRAD_WEIGHT: L.linear_grad_weight(x, dy)[0]}
+    d = B.muon_linear(n, i, o, 0, 0, 0, B.MUON_TYPE_BF16, B.MUON_WEIGHT_IN_OUT)
+    st = torch.cuda.current_stream().cuda_stream
+    for op, (a, b) in ((0, (x, w)), (1, (dy, w)), (2, (x, dy))):
+        out = torch.full_like(want[op], float("nan"))
+        s, nb = B.muon_linear_workspace_bytes(d, op, a.data_ptr(), b.data_ptr())
+        assert s == B.MUON_OK
+        ws = torch.full((nb + 4096,), 0xff, dtype=torch.uint8, device="cuda")
+        args = (d, a.data_ptr(), b.data_ptr())
+        if op == 0:
+            s = B.muon_linear_forward(*args, None, out.data_ptr(), ws.data_ptr(), nb, st)
+        elif op == 1:
+            s = B.muon_linear_grad_input(*args, None, out.data_ptr(), ws.data_ptr(), nb, st)
+        else:
+            s = B.muon_linear_grad_weight(*args, out.data_ptr(), 0, 0, ws.data_ptr(), nb, st)
+        assert s == B.MUON_OK, B.muon_op_last_error()
+        assert torch.equal(out, want[op])
+        assert (ws[nb:] == 0xff).all()
+
+
+def test_offsets_past_32_bits():
+    """Outputs and inputs of more than 2^31 elements: the last rows are right."""
+    n, o = (1 << 17) + 5, (1 << 14) + 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(n, 8, generator=g, device="cuda").bfloat16()
+    w = torch.randn(8, o, generator=g, device="cuda").bfloat16()
+    y = L.linear_forward(x, w)
+    rows = torch.tensor([0, 1, n // 2, n - 260, n - 2, n - 1], device="cuda")
+    want = _cpu64(x[rows]) @ _cpu64(w)
+    _close(y[rows], want, _sum_tol(_cpu64(x[rows]), _cpu64(w)), torch.bfloat16)
+    # the way back reads all of y: as dy (K of 2^14) and, transposed, over 2^17 tokens
+    dx = L.linear_grad_input(y, w)
+    _close(dx[rows], _cpu64(y[rows]) @ _cpu64(w).t(), _sum_tol(_cpu64(y[rows]), _cpu64(w).t()), torch.bfloat16)
+    dw, db = L.linear_grad_weight(x, y, dbias=True)
+    cols = torch.tensor([0, 77, o - 129, o - 1], device="cuda")
+    yc = _cpu64(y[:, cols])
+    _close(dw[:, cols], _cpu64(x).t() @ yc, _sum_tol(_cpu64(x).t(), yc), torch.float32)
+    _close(db[cols], yc.sum(0), _sum_tol(torch.ones(1, n, dtype=torch.float64), yc)[0], torch.float32)
+    out, mean, rstd = L.layernorm_forward(y)
+    yr = _cpu64(y[rows])
+    m = yr.mean(1, keepdim=True)
+    r = 1 / (yr.var(1, unbiased=False, keepdim=True) + 1e-5).sqrt()
+    # rows of 2^14 columns are summed in strands of 64 and 14 joins
+    u = 2.0 ** -24
+    tol = r * 80 * u * yr.abs().mean(1, keepdim=True) + 100 * u * ((yr - m) * r).abs() + u * yr.abs() * r
+    _close(out[rows], (yr - m) * r, tol, torch.bfloat16)
+    dx, _, db = L.layernorm_backward(out, y, mean, rstd, dbias=True)
+    assert dx.shape == y.shape and dx[rows].isfinite().all()
+    oc = _cpu64(out[:, cols])
+    _close(db[cols], oc.sum(0), _sum_tol(torch.ones(1, n, dtype=torch.float64), oc)[0], torch.float32)
+
+
+def test_python_refusals():
+    bf = torch.bfloat16
+    x, w = torch.zeros(4, 8, dtype=bf, device="cuda"), torch.zeros(8, 16, dtype=bf, device="cuda")
+    dy = torch.zeros(4, 16, dtype=bf, device="cuda")
+    with pytest.raises(ValueError, match="weight_layout"):
+        L.linear_forward(x, w, weight_layout="oi")
+    with pytest.raises(ValueError, match="activation"):
+        L.linear_forward(x, w, activation="swish")
+    with pytest.raises(ValueError, match="x: shape"):
+        L.linear_forward(x, w, weight_layout="out_in")
+    with pytest.raises(ValueError, match="w: dtype"):
+        L.linear_forward(x, w.half())
+    with pytest.raises(ValueError, match="x: dtype"):
+        L.linear_forward(x.float(), w.float())
+    with pytest.raises(ValueError, match="w: on cpu"):
+        L.linear_forward(x, w.cpu())
+    with pytest.raises(ValueError, match="contiguous"):
+        L.linear_forward(x, torch.zeros(16, 8, dtype=bf, device="cuda").t())
+    with pytest.raises(ValueError, match="rows overlap"):
+        L.linear_forward(torch.zeros(8, dtype=bf, device="cuda").expand(4, 8), w)
+    with pytest.raises(ValueError, match="bias: dtype"):
+        L.linear_forward(x, w, bias=torch.zeros(16, dtype=bf, device="cuda"))
+    with pytest.raises(ValueError, match="bias: shape"):
+        L.linear_forward(x, w, bias=torch.zeros(8, device="cuda"))
+    with pytest.raises(ValueError, match="residual: shape"):
+        L.linear_forward(x, w, residual=x)
+    with pytest.raises(ValueError, match="preact"):
+        L.linear_grad_input(dy, w, activation="relu")
+    with pytest.raises(ValueError, match="dw: shape"):
+        L.linear_grad_weight(x, dy, dw=torch.zeros(16, 8, device="cuda"))
+    with pytest.raises(ValueError, match="accumulate"):
+        L.linear_grad_weight(x, dy, accumulate=True)
+    with pytest.raises(B.MuonError, match="overlaps"):
+        L.linear_forward(x, torch.zeros(8, 8, dtype=bf, device="cuda"), out=x)
+    with pytest.raises(ValueError, match="mean: shape"):
+        L.layernorm_backward(x, x, torch.zeros(3, device="cuda"), torch.zeros(4, device="cuda"))
+    with pytest.raises(B.MuonError, match="eps"):
+        L.layernorm_forward(x, eps=-1.0)
+    with pytest.raises(B.MuonError, match="features"):
+        L.linear_forward(x[:, :0], w[:0])
