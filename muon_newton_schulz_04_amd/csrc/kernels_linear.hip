@@ -60,14 +60,15 @@ __device__ __forceinline__ void load_lds(u32x4 r, uint32_t lds, uint32_t voff, u
 // How one operand's tile is loaded and read. KC: TILE rows of 128 bytes (whole
 // cache lines), chunk c (16 bytes) of row r stored at c ^ ((r >> 1) & 7), so
 // that the 16 rows of a phase of ds_read_b128 fall in 16 distinct 16-byte
-// slots. Otherwise BK rows of 2 TILE bytes, chunk c of row r at c ^ (4 (r & 3)),
-// so that the 4 rows x 64 bytes of a half-wave's transposing read fall in 4
-// distinct 64-byte windows.
+// slots. Otherwise BK rows of 2 TILE bytes, chunk c of row r at c ^ (4 (r & 3))
+// (128-byte rows: c ^ (4 (r >> 1 & 1))), so that the 4 rows x 64 bytes of a
+// half-wave's transposing read fall in 4 distinct 64-byte windows.
 template <typename T, int TILE, bool KC>
 struct Operand {
     static constexpr int BYTES = TILE * BK * 2;
     static constexpr int NLD = BYTES / 4096;  // load instructions a wave issues per slice
     static constexpr int BLK = TILE / 64;     // 32-wide fragment blocks of a wave
+    static __device__ __forceinline__ int turn(int row) { return 4 * (TILE == 64 ? row >> 1 & 1 : row & 3); }
     u32x4 r;           // KC: the tile's rows; else the slice's
     uint32_t range;    // bytes of a whole slice's resource (not KC)
     uint32_t tail;     // bytes of the last row (not KC)
@@ -109,7 +110,7 @@ struct Operand {
             range = (uint32_t)(BK - 1) * rowb + tail;
             r = rsrc(static_cast<const char*>(p) + (int64_t)kb * rowb + (int64_t)i0 * 2, 0u);
             const int row0 = wave * RPI + lane / XCH;
-            const int c = (lane % XCH) ^ (4 * (row0 & 3));
+            const int c = (lane % XCH) ^ turn(row0);
 #pragma unroll
             for (int q = 0; q < NLD; ++q)
                 off[q] = c * 8 < cols ? (uint32_t)(row0 + q * 4 * RPI) * rowb + (uint32_t)c * 16u : OUT;
@@ -119,7 +120,7 @@ struct Operand {
 #pragma unroll
             for (int f = 0; f < BLK; ++f) {
                 const int e = wblk * (TILE / 2) + 32 * f + 16 * (g & 1) + 4 * (s & 3);
-                rd[f] = row * (2 * TILE) + 16 * ((e >> 3) ^ (4 * (row & 3))) + 2 * (e & 7);
+                rd[f] = row * (2 * TILE) + 16 * ((e >> 3) ^ turn(row)) + 2 * (e & 7);
             }
         }
     }
@@ -200,9 +201,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
     constexpr int FRI = WM / 32, FRJ = WN / 32;
     constexpr int SROW = WN * 4 + 16;  // bytes of a staged epilogue row
     // the tall tile: two A buffers and one B buffer, so that two workgroups fit
-    // a CU; the square tile, for products too small to fill the chip, whose
+    // a CU; the square tiles, for products too small to fill the chip, whose
     // time is load latency: a ring of four buffers of both
-    constexpr bool RING = TM == 128;
+    constexpr bool RING = TM <= 128;
     constexpr int STAGE = OA::BYTES + OB::BYTES;
     constexpr int SMEM = RING ? 4 * STAGE : OA::BYTES + STAGE;
     static_assert(4 * 32 * SROW <= SMEM, "epilogue staging");
@@ -390,12 +391,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
     const int ch = lane % CPR, rr = lane / CPR;
     const int col = j0 + wj * WN + ch * 8;
     const bool inside = col < g.N;
-    const int64_t ccol = inside ? col : 0;
+    // columns of the lane's chunk: 8, or fewer at the edge
+    const int ncol = g.N - col >= 8 ? 8 : g.N - col;
+    const int64_t ccol = inside && ncol == 8 ? col : 0;
     const int row0 = i0 + wi * WM + rr;
     const bool direct = piece < 0;
     float* const part = g.partial + (int64_t)piece * (TM * TN);
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (direct && g.epi.bias) load8(g.epi.bias + ccol, 8, bias);
+    if (direct && g.epi.bias && inside) load8(g.epi.bias + col, ncol, bias);
     // this block's first8, the next one's, and the one's after that or, where
     // there is one, this block's second8
     u32x4 in0[NP], in1[NP], in2[NP];
@@ -409,7 +412,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
     };
     if (direct) {
         fetch(0, in0);
-        fetch(1, in1);
+        if (FRI > 1) fetch(1, in1);
     }
 #pragma unroll 1
     for (int fi = 0; fi < FRI; ++fi) {
@@ -446,7 +449,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
             if (row < g.M && inside) {
                 if (direct) {
                     float v[8] = {lo[0], lo[1], lo[2], lo[3], up[0], up[1], up[2], up[3]};
-                    finish8<T>(g.epi, row, col, 8, v, bias, in0[it], in2[it]);
+                    finish8<T>(g.epi, row, col, ncol, v, bias, in0[it], in2[it]);
                 } else {
                     float* p = part + (row - i0) * TN + (col - j0);
                     *reinterpret_cast<f32x4*>(p) = lo;
@@ -492,9 +495,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
 
 // The pieces of each split tile added in order, then the epilogue: GS
 // neighbouring lanes share a chunk of 8 outputs, each adding a run of pieces.
-template <typename T, int TM, int GS, int SUM>
+template <typename T, int TM, int TN, int GS, int SUM>
 __global__ __launch_bounds__(256) void k_gemm_join(const GemmArgs g) {
-    constexpr int TN = kGemmTileN;
     constexpr int PER = 256 / GS;                 // chunks a block takes
     constexpr int BLOCKS = TM * (TN / 8) / PER;   // blocks per tile
     const int t = blockIdx.x / BLOCKS, sub = blockIdx.x % BLOCKS;
@@ -722,19 +724,19 @@ __global__ __launch_bounds__(256) void k_pack(const PackArgs a, const PackArgs b
     }
 }
 
-template <typename T, int TM>
+template <typename T, int TM, int TN>
 hipError_t gemm_t(const GemmArgs& g, bool a_kc, bool b_kc, int sum, hipStream_t st) {
     const int wgs = g.whole + (g.tiles_m * g.tiles_n - g.whole) * g.splits;
     if (a_kc && b_kc)
-        k_gemm<T, TM, 128, true, true, 0><<<wgs, 256, 0, st>>>(g);
+        k_gemm<T, TM, TN, true, true, 0><<<wgs, 256, 0, st>>>(g);
     else if (a_kc)
-        k_gemm<T, TM, 128, true, false, 0><<<wgs, 256, 0, st>>>(g);
+        k_gemm<T, TM, TN, true, false, 0><<<wgs, 256, 0, st>>>(g);
     else if (sum == 0)
-        k_gemm<T, TM, 128, false, false, 0><<<wgs, 256, 0, st>>>(g);
+        k_gemm<T, TM, TN, false, false, 0><<<wgs, 256, 0, st>>>(g);
     else if (sum == 1)
-        k_gemm<T, TM, 128, false, false, 1><<<wgs, 256, 0, st>>>(g);
+        k_gemm<T, TM, TN, false, false, 1><<<wgs, 256, 0, st>>>(g);
     else
-        k_gemm<T, TM, 128, false, false, 2><<<wgs, 256, 0, st>>>(g);
+        k_gemm<T, TM, TN, false, false, 2><<<wgs, 256, 0, st>>>(g);
     return hipGetLastError();
 }
 
@@ -747,37 +749,47 @@ hipError_t skinny_t(const GemmArgs& g, bool b_kc, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <typename T, int TM, int GS>
+template <typename T, int TM, int TN, int GS>
 void join_gs(const GemmArgs& g, int sum, hipStream_t st) {
-    const int grid = (g.tiles_m * g.tiles_n - g.whole) * (TM * 16 * GS / 256);
+    const int grid = (g.tiles_m * g.tiles_n - g.whole) * (TM * (TN / 8) * GS / 256);
     if (sum == 0)
-        k_gemm_join<T, TM, GS, 0><<<grid, 256, 0, st>>>(g);
+        k_gemm_join<T, TM, TN, GS, 0><<<grid, 256, 0, st>>>(g);
     else if (sum == 1)
-        k_gemm_join<T, TM, GS, 1><<<grid, 256, 0, st>>>(g);
+        k_gemm_join<T, TM, TN, GS, 1><<<grid, 256, 0, st>>>(g);
     else
-        k_gemm_join<T, TM, GS, 2><<<grid, 256, 0, st>>>(g);
+        k_gemm_join<T, TM, TN, GS, 2><<<grid, 256, 0, st>>>(g);
 }
-template <typename T, int TM>
+template <typename T, int TM, int TN>
 hipError_t join_t(const GemmArgs& g, int sum, hipStream_t st) {
     // four lanes a chunk for eight pieces or more
     if (g.splits >= 8)
-        join_gs<T, TM, 4>(g, sum, st);
+        join_gs<T, TM, TN, 4>(g, sum, st);
     else
-        join_gs<T, TM, 1>(g, sum, st);
+        join_gs<T, TM, TN, 1>(g, sum, st);
     return hipGetLastError();
+}
+
+template <typename T>
+hipError_t gemm_tile(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int sum, hipStream_t st) {
+    return tile_m == 256   ? gemm_t<T, 256, 128>(g, a_kc, b_kc, sum, st)
+           : tile_m == 128 ? gemm_t<T, 128, 128>(g, a_kc, b_kc, sum, st)
+                           : gemm_t<T, 64, 64>(g, a_kc, b_kc, sum, st);
+}
+template <typename T>
+hipError_t join_tile(const GemmArgs& g, int tile_m, int sum, hipStream_t st) {
+    return tile_m == 256   ? join_t<T, 256, 128>(g, sum, st)
+           : tile_m == 128 ? join_t<T, 128, 128>(g, sum, st)
+                           : join_t<T, 64, 64>(g, sum, st);
 }
 
 }  // namespace
 
 hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int dtype, int sum, hipStream_t st) {
-    if (dtype == 0)
-        return tile_m == 256 ? gemm_t<bf16, 256>(g, a_kc, b_kc, sum, st) : gemm_t<bf16, 128>(g, a_kc, b_kc, sum, st);
-    return tile_m == 256 ? gemm_t<f16, 256>(g, a_kc, b_kc, sum, st) : gemm_t<f16, 128>(g, a_kc, b_kc, sum, st);
+    return dtype == 0 ? gemm_tile<bf16>(g, tile_m, a_kc, b_kc, sum, st) : gemm_tile<f16>(g, tile_m, a_kc, b_kc, sum, st);
 }
 
 hipError_t launch_gemm_join(const GemmArgs& g, int tile_m, int dtype, int sum, hipStream_t st) {
-    if (dtype == 0) return tile_m == 256 ? join_t<bf16, 256>(g, sum, st) : join_t<bf16, 128>(g, sum, st);
-    return tile_m == 256 ? join_t<f16, 256>(g, sum, st) : join_t<f16, 128>(g, sum, st);
+    return dtype == 0 ? join_tile<bf16>(g, tile_m, sum, st) : join_tile<f16>(g, tile_m, sum, st);
 }
 
 hipError_t launch_skinny(const GemmArgs& g, bool b_kc, int dtype, hipStream_t st) {

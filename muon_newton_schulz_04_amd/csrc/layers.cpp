@@ -152,51 +152,56 @@ Tensor tensor_w(const muon_linear& d, const void* p, int size) {
     return {p, r, c, d.ld_w ? d.ld_w : c, size};
 }
 
-// How an M x N x K product is cut: tile height, how many tiles run whole, and
-// in how many K pieces the others go. Each candidate is priced in clocks (2.4
-// GHz) with constants fitted to measured times (both tiles, one piece to 24,
-// 21 shapes: the choice was within 3% of the best everywhere but on shapes
-// under 20 us, within 10%): a slice of a workgroup alone on its CU and beside a
-// second one, launch and all that a workgroup does outside its main loop, the
-// join's launch and traffic, and the rate at which the whole chip multiplies
-// however it is filled. For instance 4096 x 1600 x 1600: tall tiles 33 us,
-// square ones 38; 1024 x 1600 x 1600: 29 and 20; 6400 x 1600 weight gradient
-// over 8192 tokens: 157 us with pieces beside whole tiles, 208 without.
-// direct: the product kernel can finish whole tiles (N is a multiple of 8).
-muon::GemmPlan choose_plan(int64_t M, int64_t N, int64_t K, bool direct) {
+// How an M x N x K product is cut: the tile, how many tiles run whole, and in
+// how many K pieces the others go. Each candidate is priced in clocks (2.4 GHz)
+// with constants fitted to times measured over 26 shapes, three tiles and up to
+// 24 pieces; the choice was within 5% of the best at all but two. In us, tall
+// (256 x 128), square (128) and small (64) tiles: 4096 x 1600 x 1600 32.5, 36.6,
+// -; 2048 x 1600 x 1600 31.2, 19.3, 23.4; 1024 x 1600 x 1600 29, 19.7, 12.9;
+// 2051 x 768 x 768 20.9, 13.7, 9.0; the 6400 x 1600 weight gradient over 8192
+// tokens 154 with pieces beside whole tiles, 192 without.
+muon::GemmPlan choose_plan(int64_t M, int64_t N, int64_t K) {
     int64_t slices = (K + muon::kGemmSlice - 1) / muon::kGemmSlice;
     if (slices < 1) slices = 1;
+    // per tile: a slice of a workgroup alone on its CU and beside a second one
+    // (a 128 x 128 one fills its CU: the second runs after it), what a
+    // workgroup does besides and another round of workgroups, and the chip
+    struct Tile {
+        int m, n;
+        double alone, beside, fixed, next, chip;
+        int64_t round;
+    };
+    static const Tile tiles_of[] = {{256, 128, 2200, 3700, 23000, 5000, 8.0, 512},
+                                    {128, 128, 1140, 2280, 18000, 12000, 5.5, 256},
+                                    {64, 64, 600, 900, 9500, 9000, 2.0, 512}};
     muon::GemmPlan best{};
     double best_t = 1e300;
-    for (int tm : {256, 128}) {
-        const int64_t tiles_m = (M + tm - 1) / tm, tiles_n = (N + muon::kGemmTileN - 1) / muon::kGemmTileN;
-        const int64_t tiles = tiles_m * tiles_n;
-        // two tall workgroups share a CU, a square one fills it: a second one
-        // there starts once the first is done
-        const double alone = tm == 256 ? 2200 : 1140, beside = tm == 256 ? 3700 : 2 * alone,
-                     fixed = tm == 256 ? 23000 : 18000, next = tm == 256 ? 5000 : 12000;
-        const double chip = (double)tiles * (double)slices * (tm == 256 ? 8.0 : 5.5);
+    for (const Tile& T : tiles_of) {
+        const int64_t tiles_m = (M + T.m - 1) / T.m, tiles_n = (N + T.n - 1) / T.n, tiles = tiles_m * tiles_n;
+        const double chip = (double)tiles * (double)slices * T.chip;
         auto rounds = [&](int64_t wgs, double per) {
-            const int64_t rest = wgs % 512, full = tm == 256 ? 512 : 256;
-            return fixed + next * (double)((wgs - 1) / full) + per * ((double)(wgs / 512) * beside + (rest == 0 ? 0.0 : rest > 256 ? beside : alone));
+            const int64_t rest = wgs % 512;
+            return T.fixed + T.next * (double)((wgs - 1) / T.round) +
+                   per * ((double)(wgs / 512) * T.beside + (rest == 0 ? 0.0 : rest > 256 ? T.beside : T.alone));
         };
         auto consider = [&](double t, int64_t whole, int64_t splits, int64_t per) {
             if (t < chip) t = chip;
             if (whole < tiles)
-                t += 8.0 * (double)((tiles - whole) * splits) * (double)(M < tm ? M : tm) * 128.0 / 2300.0 + 11000.0;
+                t += 8.0 * (double)((tiles - whole) * splits) * (double)((M < T.m ? M : T.m) * T.n) / 2300.0 + 11000.0;
             if (t >= best_t) return;
             best_t = t;
-            best = {tm, (int)tiles_m, (int)tiles_n, (int)slices, (int)whole, (int)splits, (int)per};
+            best = {T.m, T.n, (int)tiles_m, (int)tiles_n, (int)slices, (int)whole, (int)splits, (int)per};
         };
-        consider(rounds(tiles, (double)slices), direct ? tiles : 0, 1, slices);
+        consider(rounds(tiles, (double)slices), tiles, 1, slices);
         for (int64_t s = 2; s <= 64 && s <= slices; ++s) {
             const int64_t per = (slices + s - 1) / s;
             if ((slices + per - 1) / per != s) continue;  // every piece has work
             if (tiles * s <= 1024) consider(rounds(tiles * s, (double)per), 0, s, per);
             // one tall tile a CU and the rest of a round in pieces beside them
             const int64_t rest = tiles % 512 - 256, n = (rest * s + 255) / 256;
-            if (direct && tm == 256 && rest > 0 && n * per <= slices)
-                consider(fixed + (double)(tiles / 512 * slices + n * per) * beside + (double)(slices - n * per) * alone,
+            if (T.m == 256 && rest > 0 && n * per <= slices)
+                consider(T.fixed + (double)(tiles / 512 * slices + n * per) * T.beside +
+                             (double)(slices - n * per) * T.alone,
                          tiles - rest, s, per);
         }
     }
@@ -231,12 +236,12 @@ muon_status plan_product(const muon_linear& d, int op, const void* pa, const voi
     P->pack_a = needs_pack(P->a);
     P->pack_b = needs_pack(P->b);
     // launches hold fewer than 2^32 threads
-    if (((P->M + 127) / 128) * ((P->N + 127) / 128) >= (int64_t)1 << (P->N % 8 == 0 ? 22 : 18))
+    if (((P->M + 127) / 128) * ((P->N + 127) / 128) >= (int64_t)1 << 22)
         return fail(MUON_E_SHAPE, "linear: output too large");
     if (op != MUON_LINEAR_GRAD_WEIGHT && P->M <= muon::kSkinnyRows)
-        P->plan = {0, 0, 0, (int)((P->K + muon::kGemmSlice - 1) / muon::kGemmSlice), 0, 0, 0};
+        P->plan = {0, 0, 0, 0, (int)((P->K + muon::kGemmSlice - 1) / muon::kGemmSlice), 0, 0, 0};
     else
-        P->plan = choose_plan(P->M, P->N, P->K, P->N % 8 == 0);
+        P->plan = choose_plan(P->M, P->N, P->K);
     size_t o = 0;
     P->off_a = o;
     if (P->pack_a) o = up256(o + (size_t)P->a.rows * up8(P->a.cols) * 2);
@@ -245,7 +250,7 @@ muon_status plan_product(const muon_linear& d, int op, const void* pa, const voi
     const muon::GemmPlan& G = P->plan;
     const size_t pieces = (size_t)(G.tiles_m * G.tiles_n - G.whole) * (size_t)G.splits;
     P->off_part = o;
-    o = up256(o + pieces * (size_t)(G.tile_m * muon::kGemmTileN) * 4);
+    o = up256(o + pieces * (size_t)(G.tile_m * G.tile_n) * 4);
     P->off_sums = o;
     if (dbias) o = up256(o + pieces * 256 * 4);
     P->bytes = o;

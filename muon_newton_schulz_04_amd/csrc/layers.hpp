@@ -42,18 +42,17 @@ struct GemmArgs {
     // are `splits` pieces of `per` slices each, whose sums meet in the
     // workspace: piece p belongs to tile whole + p % (tiles - whole).
     int32_t slices, whole, splits, per;
-    float* partial;   // piece p: [tile_m][kGemmTileN] at index p
+    float* partial;   // piece p: [tile_m][tile_n] at index p
     float* sums;      // bias gradient, or null
     float* sum_part;  // its pieces: 256 floats at index p
     Epilogue epi;
 };
 
 constexpr int kGemmSlice = 64;  // K per pipeline stage
-constexpr int kGemmTileN = 128;
 constexpr int kSkinnyRows = 32;
 
 struct GemmPlan {
-    int tile_m;  // 256 or 128, tiles are 128 wide; 0: the kernel for up to kSkinnyRows rows of A
+    int tile_m, tile_n;  // 256 x 128, 128 x 128 or 64 x 64; 0: the kernel for up to kSkinnyRows rows of A
     int tiles_m, tiles_n, slices, whole, splits, per;
 };
 
