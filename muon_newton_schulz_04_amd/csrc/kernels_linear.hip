@@ -6,19 +6,31 @@
 //    weight gradient, in either weight layout): each operand may have its k
 //    index contiguous (AKC, BKC) or its other index; the latter are read from
 //    LDS with the transposing read.
-//  * A workgroup of 4 waves (one per SIMD at T = 256) computes a T x T tile,
-//    each wave a quarter, T/2 x T/2, as blocks of 32x32x16 matrix
-//    instructions. At T = 256 a wave's 128 x 128 block takes 16 products from
-//    8 fragment reads, so the tile's LDS traffic (reads and the incoming
-//    slices) is 96 bytes a clock at the matrix peak, of the 128 that LDS
-//    gives; eight waves of 128 x 64 would need all of it.
-//  * K goes by in slices of 32 through a ring of four LDS buffers filled by
-//    direct-to-LDS loads, three slices ahead of their use, with one barrier a
-//    slice. Loads past K, past a split's end or past the matrix go out with an
-//    offset beyond the buffer resource's range and land as zeros, so the loop
-//    has no tail and reads nothing outside the operands.
-//  * splits > 1: each split writes its fp32 tile to the workspace and a second
-//    kernel adds them in order and does the epilogue (the same bits every run).
+//  * A workgroup of 4 waves computes a 256 x 128, 128 x 128 or 64 x 64 tile, each
+//    wave a quarter of it, in blocks of 32x32x16 matrix instructions. K goes by
+//    in slices of 64 that direct-to-LDS loads bring in, 128 bytes of a row at
+//    a time where k is contiguous: L2 serves whole lines, and slices of 32
+//    took two requests for each (16384 x 1600 x 6400: 356 us, against 319).
+//    Loads past K, past a piece's end or past the matrix go out with an offset
+//    beyond the buffer resource's range and land as zeros, so the loop has no
+//    tail and reads nothing outside the operands.
+//  * The tall tile keeps two slices of A and one of B in LDS (80 KB) and the B
+//    fragments of its slice in registers, so that two workgroups share a CU:
+//    one multiplies while the other is in its prologue or epilogue (one 256 x
+//    256 workgroup per CU: 593 us with the epilogue of c_fc, against 335).
+//    Bound by LDS and power: both workgroups' fragment reads and incoming
+//    slices are 140 bytes a clock at the matrix peak, of the 128 that LDS
+//    gives, and the matrix unit is busy 72% of the clocks, at 1.5 GHz (8192^3:
+//    1.26 PFLOP/s on random numbers, 1.76 on zeros). A longer way for B's loads,
+//    loads and reads spread over the matrix instructions, and wave priorities
+//    changed nothing.
+//  * The square tiles keep a ring of four slices of both operands (128 and 64
+//    KB): they are for products that do not fill the chip, whose time is the
+//    latency of a few loads.
+//  * Tiles that a round of the chip leaves over go in K pieces beside whole
+//    ones: each piece leaves fp32 sums in the workspace and a second kernel adds
+//    them in order and does the epilogue (the same bits every run).
+//  * Up to 32 rows of A have a kernel of their own (k_skinny).
 
 #include "layer_device.hpp"
 
@@ -194,7 +206,8 @@ __device__ __forceinline__ float add8(f16x8 f, float v) {
 // gradient: two-element dot products with 1 on the fragments in registers, in
 // the shadow of the matrix instructions.
 template <typename T, int TM, int TN, bool AKC, bool BKC, int SUM>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ? 1 : 2, TM == 128 ? 1 : 2))) void k_gemm(const GemmArgs g) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ? 1 : 2, TM == 128 ? 1 : 2))) void
+k_gemm(const GemmArgs g) {
     using OA = Operand<T, TM, AKC>;
     using OB = Operand<T, TN, BKC>;
     constexpr int WM = TM / 2, WN = TN / 2;   // a wave's block
@@ -393,6 +406,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
     const bool inside = col < g.N;
     // columns of the lane's chunk: 8, or fewer at the edge
     const int ncol = g.N - col >= 8 ? 8 : g.N - col;
+    // lanes without a whole chunk fetch their row's first one, unused (rows of
+    // less than one fetch nothing)
     const int64_t ccol = inside && ncol == 8 ? col : 0;
     const int row0 = i0 + wi * WM + rr;
     const bool direct = piece < 0;
@@ -402,7 +417,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
     // this block's first8, the next one's, and the one's after that or, where
     // there is one, this block's second8
     u32x4 in0[NP], in1[NP], in2[NP];
-    const bool second = direct && has_second(g.epi);
+    const bool ahead = direct && g.N >= 8, second = ahead && has_second(g.epi);
     auto fetch = [&](int fi, u32x4(&x)[NP]) {
 #pragma unroll
         for (int it = 0; it < NP; ++it) {
@@ -410,7 +425,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
             x[it] = first8<T>(g.epi, row < g.M ? row : g.M - 1, ccol);
         }
     };
-    if (direct) {
+    if (ahead) {
         fetch(0, in0);
         if (FRI > 1) fetch(1, in1);
     }
@@ -438,7 +453,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ?
                 const int row = row0 + 32 * fi + it * RPI;
                 in2[it] = second8<T>(g.epi, row < g.M ? row : g.M - 1, ccol);
             }
-        } else if (direct && fi + 2 < FRI) {
+        } else if (ahead && fi + 2 < FRI) {
             fetch(fi + 2, in2);
         }
 #pragma unroll

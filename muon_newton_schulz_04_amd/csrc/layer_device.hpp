@@ -207,7 +207,7 @@ __device__ __forceinline__ u32x4 first8(const Epilogue& E, int64_t r, int64_t c)
     } else if (E.add) {
         p = static_cast<const T*>(E.add) + r * E.ld_add + c;
     }
-    return p ? *static_cast<const u32x4_mem*>(p) : u32x4{0, 0, 0, 0};
+    return p ? __builtin_nontemporal_load(static_cast<const u32x4_mem*>(p)) : u32x4{0, 0, 0, 0};
 }
 __device__ __forceinline__ bool has_second(const Epilogue& E) {
     return E.mode == EPI_GRAD_WEIGHT ? E.accumulate != 0 : E.mode == EPI_GRAD_INPUT && E.act != ACT_NONE && E.add;
@@ -217,7 +217,7 @@ __device__ __forceinline__ u32x4 second8(const Epilogue& E, int64_t r, int64_t c
     const void* p = E.mode == EPI_GRAD_WEIGHT
                         ? static_cast<const void*>(static_cast<const float*>(E.y) + r * E.ld_y + c + 4)
                         : static_cast<const void*>(static_cast<const T*>(E.add) + r * E.ld_add + c);
-    return *static_cast<const u32x4_mem*>(p);
+    return __builtin_nontemporal_load(static_cast<const u32x4_mem*>(p));
 }
 
 template <typename T>

@@ -236,7 +236,7 @@ muon_status plan_product(const muon_linear& d, int op, const void* pa, const voi
     P->pack_a = needs_pack(P->a);
     P->pack_b = needs_pack(P->b);
     // launches hold fewer than 2^32 threads
-    if (((P->M + 127) / 128) * ((P->N + 127) / 128) >= (int64_t)1 << 22)
+    if (((P->M + 127) / 128) * ((P->N + 127) / 128) >= (int64_t)1 << 21)
         return fail(MUON_E_SHAPE, "linear: output too large");
     if (op != MUON_LINEAR_GRAD_WEIGHT && P->M <= muon::kSkinnyRows)
         P->plan = {0, 0, 0, 0, (int)((P->K + muon::kGemmSlice - 1) / muon::kGemmSlice), 0, 0, 0};

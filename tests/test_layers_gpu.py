@@ -125,7 +125,7 @@ def test_linear_sizes(size, dtype, layout):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("act", ACTS)
-@pytest.mark.parametrize("size", [(70, 72, 136), (9, 50, 33), (20, 3000, 64)], ids=str)
+@pytest.mark.parametrize("size", [(70, 72, 136), (9, 50, 33), (20, 3000, 64), (140, 5, 3), (77, 2000, 11)], ids=str)
 def test_linear_epilogues(size, act, dtype):
     """Bias, activation, residual and the kept pre-activation together, in one
     launch and over K splits, and the activation's slope on the way back."""
