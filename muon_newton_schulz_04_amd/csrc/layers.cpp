@@ -187,7 +187,7 @@ muon::GemmPlan choose_plan(int64_t M, int64_t N, int64_t K) {
         auto consider = [&](double t, int64_t whole, int64_t splits, int64_t per) {
             if (t < chip) t = chip;
             if (whole < tiles)
-                t += 8.0 * (double)((tiles - whole) * splits) * (double)((M < T.m ? M : T.m) * T.n) / 2300.0 + 11000.0;
+                t += 8.0 * (double)((tiles - whole) * splits) * (double)((M < T.m ? M : T.m) * T.n) / 1700.0 + 11000.0;
             if (t >= best_t) return;
             best_t = t;
             best = {T.m, T.n, (int)tiles_m, (int)tiles_n, (int)slices, (int)whole, (int)splits, (int)per};

@@ -582,3 +582,19 @@ def test_python_refusals():
         L.layernorm_forward(x, eps=-1.0)
     with pytest.raises(B.MuonError, match="features"):
         L.linear_forward(x[:, :0], w[:0])
+
+
+@pytest.mark.parametrize("dtype,tiny,big", [("fp16", 2.0 ** -20, 1024.0), ("bf16", 2.0 ** -130, 2.0 ** 60)])
+@pytest.mark.parametrize("rows", [3, 40, 700])
+def test_subnormal_operands_count(rows, dtype, tiny, big):
+    """Subnormal inputs are not flushed, in products and in the bias gradient."""
+    t = T[dtype]
+    x = torch.full((rows, 64), tiny, dtype=t, device="cuda")
+    w = torch.full((64, 96), big, dtype=t, device="cuda")
+    assert (L.linear_forward(x, w).double() == 64 * tiny * big).all()
+    assert (L.linear_grad_input(x, w.t().contiguous()).double() == 64 * tiny * big).all()
+    for layout in ("in_out", "out_in"):
+        dw, db = L.linear_grad_weight(torch.full((rows, 40), big, dtype=t, device="cuda"), x, dbias=True,
+                                      weight_layout=layout)
+        assert (dw.double() == rows * tiny * big).all()
+        assert (db.double() == rows * tiny).all()
