@@ -112,7 +112,7 @@ struct Raw {
 };
 
 template <typename T, int NCH, int WPR, bool VEC>
-__global__ __launch_bounds__(256) void k_norm_forward(const NormArgs n) {
+__global__ __launch_bounds__(256) void k_norm_forward(const NormForward n) {
     __shared__ float red[16];
     constexpr int LPR = 64 * WPR;  // lanes per row
     const int lane = threadIdx.x % LPR;
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(256) void k_norm_forward(const NormArgs n) {
 
 // Rows of any length, one workgroup each, read three times (twice from cache).
 template <typename T>
-__global__ __launch_bounds__(256) void k_norm_forward_wide(const NormArgs n) {
+__global__ __launch_bounds__(256) void k_norm_forward_wide(const NormForward n) {
     __shared__ float red[16];
     const int64_t row = blockIdx.x;
     const T* x = static_cast<const T*>(n.x) + row * n.ld_x;
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(256) void k_norm_forward_wide(const NormArgs n) {
 // next row on the way). VEC: rows are whole chunks.
 template <typename T, int NCH, int WPR, bool VEC>
 __global__ __launch_bounds__(WPR == 8 ? 512 : 256) __attribute__((amdgpu_waves_per_eu(2))) void k_norm_backward(
-    const NormArgs n) {
+    const NormBackward n) {
     constexpr int LPR = 64 * WPR;
     constexpr int WAVES = WPR == 8 ? 8 : 4;
     constexpr int RPB = WAVES / WPR;  // rows a workgroup works on at once
@@ -374,7 +374,7 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) __attribute__((amdgpu_waves_p
 
 // dx of rows of any length, one workgroup each.
 template <typename T>
-__global__ __launch_bounds__(256) void k_norm_backward_wide(const NormArgs n) {
+__global__ __launch_bounds__(256) void k_norm_backward_wide(const NormBackward n) {
     __shared__ float red[8];
     const int64_t row = blockIdx.x;
     const T* x = static_cast<const T*>(n.x) + row * n.ld_x;
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(256) void k_norm_backward_wide(const NormArgs n) {
 // The column sums for rows of any length: 256 columns (32 lanes x 8) of every
 // n.blocks-th group of 8 rows.
 template <typename T>
-__global__ __launch_bounds__(256) void k_norm_columns(const NormArgs n) {
+__global__ __launch_bounds__(256) void k_norm_columns(const NormBackward n) {
     __shared__ float red[2][8][32][9];
     const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int c = blockIdx.x * 256 + lane * 8;
@@ -464,7 +464,7 @@ __global__ __launch_bounds__(256) void k_norm_columns(const NormArgs n) {
 
 // dweight, dbias (+)= the partial rows: 64 columns a workgroup, each of its 16
 // waves a run of the rows, added in order.
-__global__ __launch_bounds__(1024) void k_norm_join(const NormArgs n) {
+__global__ __launch_bounds__(1024) void k_norm_join(const NormSums n) {
     __shared__ float red[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int c = blockIdx.x * 64 + lane;
@@ -490,8 +490,8 @@ __global__ __launch_bounds__(1024) void k_norm_join(const NormArgs n) {
 constexpr int kBlockCols = 8192;  // longest rows that live in registers
 
 template <typename T, bool VEC>
-void forward_rows(const NormArgs& n, hipStream_t st) {
-    const unsigned g4 = (unsigned)((n.rows + 3) / 4), g1 = (unsigned)n.rows;
+void forward_rows(const NormForward& n, hipStream_t st) {
+    const unsigned g4 = ((unsigned)n.rows + 3) / 4, g1 = (unsigned)n.rows;
     if (n.cols <= 512)
         k_norm_forward<T, 1, 1, VEC><<<g4, 256, 0, st>>>(n);
     else if (n.cols <= 1024)
@@ -505,7 +505,7 @@ void forward_rows(const NormArgs& n, hipStream_t st) {
 }
 
 template <typename T, bool VEC>
-void backward_rows(const NormArgs& n, hipStream_t st) {
+void backward_rows(const NormBackward& n, hipStream_t st) {
     const unsigned b = (unsigned)n.blocks;
     if (n.cols <= 512)
         k_norm_backward<T, 1, 1, VEC><<<b, 256, 0, st>>>(n);
@@ -520,7 +520,7 @@ void backward_rows(const NormArgs& n, hipStream_t st) {
 }
 
 template <typename T>
-hipError_t forward_t(const NormArgs& n, hipStream_t st) {
+hipError_t forward_t(const NormForward& n, hipStream_t st) {
     if (n.cols > kBlockCols)
         k_norm_forward_wide<T><<<(unsigned)n.rows, 256, 0, st>>>(n);
     else if (n.cols % 8 == 0)
@@ -531,29 +531,20 @@ hipError_t forward_t(const NormArgs& n, hipStream_t st) {
 }
 
 template <typename T>
-hipError_t backward_t(const NormArgs& n, hipStream_t st) {
-    hipError_t e = hipSuccess;
-    if (n.rows > 0) {
-        if (n.cols > kBlockCols) {
-            if (n.part) {
-                k_norm_columns<T><<<dim3((unsigned)((n.cols + 255) / 256), (unsigned)n.blocks), 256, 0, st>>>(n);
-                e = hipGetLastError();
-                if (e != hipSuccess) return e;
-            }
-            k_norm_backward_wide<T><<<(unsigned)n.rows, 256, 0, st>>>(n);
-        } else if (n.cols % 8 == 0) {
-            backward_rows<T, true>(n, st);
-        } else {
-            backward_rows<T, false>(n, st);
+hipError_t backward_t(const NormBackward& n, hipStream_t st) {
+    if (n.cols > kBlockCols) {
+        if (n.part) {
+            k_norm_columns<T><<<dim3((unsigned)((n.cols + 255) / 256), (unsigned)n.blocks), 256, 0, st>>>(n);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
         }
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        k_norm_backward_wide<T><<<(unsigned)n.rows, 256, 0, st>>>(n);
+    } else if (n.cols % 8 == 0) {
+        backward_rows<T, true>(n, st);
+    } else {
+        backward_rows<T, false>(n, st);
     }
-    if (n.dweight || n.dbias) {
-        k_norm_join<<<dim3((unsigned)((n.cols + 63) / 64), 2), 1024, 0, st>>>(n);
-        e = hipGetLastError();
-    }
-    return e;
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -570,12 +561,17 @@ int norm_backward_blocks(int64_t rows, int64_t cols) {
     return (int)(b < 1 ? 1 : b < most ? b : most);
 }
 
-hipError_t launch_norm_forward(const NormArgs& n, int dtype, hipStream_t st) {
+hipError_t launch_norm_forward(const NormForward& n, int dtype, hipStream_t st) {
     return dtype == 0 ? forward_t<bf16>(n, st) : dtype == 1 ? forward_t<f16>(n, st) : forward_t<float>(n, st);
 }
 
-hipError_t launch_norm_backward(const NormArgs& n, int dtype, hipStream_t st) {
+hipError_t launch_norm_backward(const NormBackward& n, int dtype, hipStream_t st) {
     return dtype == 0 ? backward_t<bf16>(n, st) : dtype == 1 ? backward_t<f16>(n, st) : backward_t<float>(n, st);
+}
+
+hipError_t launch_norm_sums(const NormSums& n, hipStream_t st) {
+    k_norm_join<<<dim3((unsigned)((n.cols + 63) / 64), 2), 1024, 0, st>>>(n);
+    return hipGetLastError();
 }
 
 }  // namespace muon

@@ -239,7 +239,9 @@ k_gemm(const GemmArgs g) {
         s0 = piece / split * g.per;
         nk = g.slices - s0 < g.per ? g.slices - s0 : g.per;
     }
-    const int kmax = AKC || BKC ? g.kp : g.K;
+    // a k-contiguous operand's rows go on to the next multiple of 8 (zeros), the
+    // rows of the others likewise
+    const int kp = (g.K + 7) & ~7, kmax = AKC || BKC ? kp : g.K;
     int ti, tj;
     tile_at(g, tile, ti, tj);
     const int i0 = ti * TM, j0 = tj * TN;
@@ -249,8 +251,8 @@ k_gemm(const GemmArgs g) {
 
     OA A;
     OB B;
-    A.init(g.a, g.ld_a, i0, AKC ? g.M : g.mp, g.kp, kb, AKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wi);
-    B.init(g.b, g.ld_b, j0, BKC ? g.N : g.np, g.kp, kb, BKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wj);
+    A.init(g.a, g.ld_a, i0, AKC ? g.M : (g.M + 7) & ~7, kp, kb, AKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wi);
+    B.init(g.b, g.ld_b, j0, BKC ? g.N : (g.N + 7) & ~7, kp, kb, BKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wj);
 
     f32x16 acc[FRI][FRJ];
 #pragma unroll
@@ -591,7 +593,7 @@ __device__ __forceinline__ f32x4 mfma16<f16>(f16x8 a, f16x8 b, f32x4 c) {
 // each through a ring of its own in LDS (no barriers: a wave waits for its own
 // loads), 16 to 18 KB a wave on the way. Their sums meet in LDS, in wave order.
 template <typename T, bool BKC, int MT>
-__global__ __launch_bounds__(512) void k_skinny(const GemmArgs g) {
+__global__ __launch_bounds__(512) void k_skinny(const SkinnyArgs g) {
     constexpr int TNS = BKC ? 16 : 32;       // columns
     constexpr int WB = TNS * 128;            // bytes of a slice of B
     constexpr int XB = MT * 2048;            // and of A
@@ -602,6 +604,7 @@ __global__ __launch_bounds__(512) void k_skinny(const GemmArgs g) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int j0 = per_xcd(blockIdx.x, gridDim.x) * TNS;
+    const int kp = (g.K + 7) & ~7;
     char* const ring = smem + wave * R * STAGE;
     const uint32_t lring = (uint32_t)(uintptr_t)(LDS_AS char*)ring;
 
@@ -618,10 +621,10 @@ __global__ __launch_bounds__(512) void k_skinny(const GemmArgs g) {
 #pragma unroll
         for (int q = 0; q < WB / 1024; ++q)
             offw[q] = r8 + 8 * q < rows ? (uint32_t)(r8 + 8 * q) * rowb + (uint32_t)c8 * 16u : OUT;
-        rw = rsrc(static_cast<const char*>(g.b) + (int64_t)j0 * rowb, (uint32_t)(rows - 1) * rowb + (uint32_t)g.kp * 2u);
+        rw = rsrc(static_cast<const char*>(g.b) + (int64_t)j0 * rowb, (uint32_t)(rows - 1) * rowb + (uint32_t)kp * 2u);
     } else {
         const int r4 = lane >> 2, c4 = (lane & 3) ^ (2 * (r4 >> 3 & 1));
-        const int cols = g.np - j0 < TNS ? g.np - j0 : TNS;
+        const int np = (g.N + 7) & ~7, cols = np - j0 < TNS ? np - j0 : TNS;
         tail = (uint32_t)cols * 2u;
 #pragma unroll
         for (int q = 0; q < WB / 1024; ++q)
@@ -631,12 +634,12 @@ __global__ __launch_bounds__(512) void k_skinny(const GemmArgs g) {
 #pragma unroll
     for (int q = 0; q < XB / 1024; ++q)
         offx[q] = r8 + 8 * q < g.M ? (uint32_t)(r8 + 8 * q) * rowa + (uint32_t)c8 * 16u : OUT;
-    rx = rsrc(g.a, (uint32_t)(g.M - 1) * rowa + (uint32_t)g.kp * 2u);
+    rx = rsrc(g.a, (uint32_t)(g.M - 1) * rowa + (uint32_t)kp * 2u);
 
     auto load = [&](int slice, uint32_t dst) {
         const int k0 = slice * BK;
-        const uint32_t so = k0 < g.kp ? (uint32_t)k0 * 2u : 0u;
-        const uint32_t dead = c8 * 8 < g.kp - k0 ? 0u : OUT;
+        const uint32_t so = k0 < kp ? (uint32_t)k0 * 2u : 0u;
+        const uint32_t dead = c8 * 8 < kp - k0 ? 0u : OUT;
         if constexpr (BKC) {
 #pragma unroll
             for (int q = 0; q < WB / 1024; ++q) load_lds(rw, dst + q * 1024, offw[q] | dead, so);
@@ -770,7 +773,7 @@ hipError_t gemm_t(const GemmArgs& g, bool a_kc, bool b_kc, int sum, hipStream_t 
 }
 
 template <typename T, int MT>
-hipError_t skinny_t(const GemmArgs& g, bool b_kc, hipStream_t st) {
+hipError_t skinny_t(const SkinnyArgs& g, bool b_kc, hipStream_t st) {
     if (b_kc)
         k_skinny<T, true, MT><<<(g.N + 15) / 16, 512, 0, st>>>(g);
     else
@@ -821,7 +824,7 @@ hipError_t launch_gemm_join(const GemmArgs& g, int tile_m, int dtype, int sum, h
     return dtype == 0 ? join_tile<bf16>(g, tile_m, sum, st) : join_tile<f16>(g, tile_m, sum, st);
 }
 
-hipError_t launch_skinny(const GemmArgs& g, bool b_kc, int dtype, hipStream_t st) {
+hipError_t launch_skinny(const SkinnyArgs& g, bool b_kc, int dtype, hipStream_t st) {
     if (dtype == 0) return g.M <= 16 ? skinny_t<bf16, 1>(g, b_kc, st) : skinny_t<bf16, 2>(g, b_kc, st);
     return g.M <= 16 ? skinny_t<f16, 1>(g, b_kc, st) : skinny_t<f16, 2>(g, b_kc, st);
 }

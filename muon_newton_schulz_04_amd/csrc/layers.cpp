@@ -271,6 +271,10 @@ muon_status run_product(Product& P, int dtype, muon::Epilogue& E, float* sums, i
     }
     if (n) TRY(hip_status(muon::launch_pack(packs, n, st), "pack kernel"));
     const muon::GemmPlan& G = P.plan;
+    if (G.tile_m == 0) {
+        const muon::SkinnyArgs k{P.a.p, P.b.p, (int)P.a.ld, (int)P.b.ld, (int)P.M, (int)P.N, (int)P.K, G.slices, E};
+        return hip_status(muon::launch_skinny(k, P.b_kc, dtype, st), "product kernel");
+    }
     muon::GemmArgs g{};
     g.a = P.a.p;
     g.b = P.b.p;
@@ -279,9 +283,6 @@ muon_status run_product(Product& P, int dtype, muon::Epilogue& E, float* sums, i
     g.M = (int)P.M;
     g.N = (int)P.N;
     g.K = (int)P.K;
-    g.kp = (int)((P.a_kc || P.b_kc) ? up8(P.K) : P.K);
-    g.mp = (int)up8(P.M);
-    g.np = (int)up8(P.N);
     g.tiles_m = G.tiles_m;
     g.tiles_n = G.tiles_n;
     g.slices = G.slices;
@@ -292,7 +293,6 @@ muon_status run_product(Product& P, int dtype, muon::Epilogue& E, float* sums, i
     g.sums = sums;
     g.sum_part = reinterpret_cast<float*>(ws + P.off_sums);
     g.epi = E;
-    if (G.tile_m == 0) return hip_status(muon::launch_skinny(g, P.b_kc, dtype, st), "product kernel");
     TRY(hip_status(muon::launch_gemm(g, G.tile_m, P.a_kc, P.b_kc, dtype, sum, st), "product kernel"));
     if (G.whole < G.tiles_m * G.tiles_n) TRY(hip_status(muon::launch_gemm_join(g, G.tile_m, dtype, sum, st), "join kernel"));
     return MUON_OK;
@@ -354,14 +354,14 @@ muon_status run_layer(const muon_linear* d, int op, const void* a, const void* w
     TRY(check_device());
     muon::Epilogue E{};
     E.mode = fwd ? muon::EPI_FORWARD : muon::EPI_GRAD_INPUT;
-    E.act = e->activation;
+    E.act = (int8_t)e->activation;
     E.bias = e->bias;
     E.add = e->add;
     E.z = e->z && Z.p ? e->z : nullptr;
     E.y = y;
-    E.ld_add = R.ld;
-    E.ld_z = Z.ld;
-    E.ld_y = Y.ld;
+    E.ld_add = (int)R.ld;
+    E.ld_z = (int)Z.ld;
+    E.ld_y = (int)Y.ld;
     return run_product(P, d->dtype, E, nullptr, 0, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
 }
 
@@ -380,17 +380,7 @@ muon_status check_norm(const muon_layernorm* d) {
     return MUON_OK;
 }
 
-muon::NormArgs norm_args(const muon_layernorm& d) {
-    muon::NormArgs n{};
-    n.rows = d.rows;
-    n.cols = (int)d.cols;
-    n.ld_x = d.ld_x ? d.ld_x : d.cols;
-    n.ld_y = d.ld_y ? d.ld_y : d.cols;
-    n.ld_dx = d.ld_dx ? d.ld_dx : d.cols;
-    n.ld_r = d.ld_add ? d.ld_add : d.cols;
-    n.eps = d.eps;
-    return n;
-}
+int64_t stride_of(int64_t ld, int64_t cols) { return ld ? ld : cols; }
 
 size_t norm_workspace(const muon_layernorm& d) {
     return up256((size_t)muon::norm_backward_blocks(d.rows, d.cols) * 2 * (size_t)d.cols * 4);
@@ -452,7 +442,7 @@ muon_status muon_linear_grad_weight(const muon_linear* d, const void* x, const v
         muon::Epilogue E{};
         E.mode = muon::EPI_GRAD_WEIGHT;
         E.y = dw;
-        E.ld_y = W.ld;
+        E.ld_y = (int)W.ld;
             E.accumulate = accumulate != 0;
         // dy is the second operand of an [in, out] gradient, else the first
         const int sum = !dbias ? 0 : d->weight_layout == MUON_WEIGHT_IN_OUT ? 1 : 2;
@@ -467,8 +457,8 @@ muon_status muon_layernorm_forward(const muon_layernorm* d, const void* x, const
         if (d->rows == 0) return MUON_OK;
         if (!x || !y || !mean || !rstd) return fail(MUON_E_INVALID_ARG, "null tensor");
         const int size = d->dtype == MUON_TYPE_FP32 ? 4 : 2;
-        muon::NormArgs n = norm_args(*d);
-        const Tensor X{x, d->rows, d->cols, n.ld_x, size}, Y{y, d->rows, d->cols, n.ld_y, size};
+        const Tensor X{x, d->rows, d->cols, stride_of(d->ld_x, d->cols), size},
+            Y{y, d->rows, d->cols, stride_of(d->ld_y, d->cols), size};
         const Tensor W{weight, 1, d->cols, d->cols, 4}, Bi{bias, 1, d->cols, d->cols, 4};
         const Tensor M{mean, 1, d->rows, d->rows, 4}, S{rstd, 1, d->rows, d->rows, 4};
         for (const Tensor& t : {X, Y}) TRY(check_align(t.p, size, "x or y"));
@@ -477,13 +467,9 @@ muon_status muon_layernorm_forward(const muon_layernorm* d, const void* x, const
         TRY(check_disjoint(M, {X, W, Bi, S}, nullptr));
         TRY(check_disjoint(S, {X, W, Bi}, nullptr));
         TRY(check_device());
-        n.x = x;
-        n.weight = weight;
-        n.bias = bias;
-        n.y = y;
-        n.mean = mean;
-        n.rstd = rstd;
-            return hip_status(muon::launch_norm_forward(n, d->dtype, static_cast<hipStream_t>(stream)),
+        const muon::NormForward n{x,  weight, bias, y, mean, rstd, (int)d->rows, (int)d->cols, (int)X.ld, (int)Y.ld,
+                                  d->eps};
+        return hip_status(muon::launch_norm_forward(n, d->dtype, static_cast<hipStream_t>(stream)),
                           "layer norm kernel");
     });
 }
@@ -504,9 +490,10 @@ muon_status muon_layernorm_backward(const muon_layernorm* d, const void* dy, con
         TRY(check_norm(d));
         if (d->rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return fail(MUON_E_INVALID_ARG, "null tensor");
         const int size = d->dtype == MUON_TYPE_FP32 ? 4 : 2;
-        muon::NormArgs n = norm_args(*d);
-        const Tensor DY{dy, d->rows, d->cols, n.ld_y, size}, X{x, d->rows, d->cols, n.ld_x, size},
-            DX{dx, d->rows, d->cols, n.ld_dx, size}, R{add, d->rows, d->cols, n.ld_r, size};
+        const Tensor DY{dy, d->rows, d->cols, stride_of(d->ld_y, d->cols), size},
+            X{x, d->rows, d->cols, stride_of(d->ld_x, d->cols), size},
+            DX{dx, d->rows, d->cols, stride_of(d->ld_dx, d->cols), size},
+            R{add, d->rows, d->cols, stride_of(d->ld_add, d->cols), size};
         const Tensor W{weight, 1, d->cols, d->cols, 4}, DW{dweight, 1, d->cols, d->cols, 4},
             DB{dbias, 1, d->cols, d->cols, 4};
         const Tensor M{mean, 1, d->rows, d->rows, 4}, S{rstd, 1, d->rows, d->rows, 4};
@@ -522,20 +509,17 @@ muon_status muon_layernorm_backward(const muon_layernorm* d, const void* dy, con
         TRY(check_disjoint(K, {DY, X, R, W, M, S}, nullptr));
         if (d->rows == 0 && (!sums || accumulate)) return MUON_OK;
         TRY(check_device());
-        n.dy = dy;
-        n.x = x;
-        n.weight = weight;
-        n.mean = const_cast<float*>(mean);
-        n.rstd = const_cast<float*>(rstd);
-        n.add = add;
-        n.dx = dx;
-        n.dweight = dweight;
-        n.dbias = dbias;
-        n.accumulate = accumulate != 0;
-        n.part = sums ? static_cast<float*>(workspace) : nullptr;
-        n.blocks = muon::norm_backward_blocks(d->rows, d->cols);
-        return hip_status(muon::launch_norm_backward(n, d->dtype, static_cast<hipStream_t>(stream)),
-                          "layer norm gradient kernels");
+        const int blocks = muon::norm_backward_blocks(d->rows, d->cols);
+        float* part = sums ? static_cast<float*>(workspace) : nullptr;
+        hipStream_t st = static_cast<hipStream_t>(stream);
+        if (d->rows > 0) {
+            const muon::NormBackward n{dy, x, weight, mean, rstd, add, dx, part, (int)d->rows, (int)d->cols, (int)X.ld,
+                                       (int)DY.ld, (int)DX.ld, (int)R.ld, blocks};
+            TRY(hip_status(muon::launch_norm_backward(n, d->dtype, st), "layer norm gradient kernels"));
+        }
+        if (!sums) return MUON_OK;
+        const muon::NormSums k{part, dweight, dbias, (int)d->cols, blocks, accumulate != 0};
+        return hip_status(muon::launch_norm_sums(k, st), "layer norm gradient sums");
     });
 }
 

@@ -15,27 +15,27 @@ enum EpiMode {
     EPI_GRAD_WEIGHT = 2  // w (+)= v, float32
 };
 
+// (The arguments of kernels are kept small: a launch costs the host 2.7 us with
+// 8 bytes of them and 3.7 us with 216.)
 struct Epilogue {
-    int32_t mode, act;
     const float* bias;  // [N] or null
     const void* add;    // [M, N] of the 16-bit type, or null
     void* z;            // forward: written if not null; grad input: read if act != none
     void* y;            // 16-bit output, or float32 for the weight gradient
-    int64_t ld_add, ld_z, ld_y;
-    int32_t accumulate;  // weight gradient: add to what is there
+    int32_t ld_add, ld_z, ld_y;
+    int8_t mode, act;
+    int8_t accumulate;  // weight gradient: add to what is there
 };
 
 // C[M, N] = sum_k A(m, k) B(k, n) over 16-bit operands, each stored with its k
 // index contiguous ([M, K], [N, K]) or its other index contiguous ([K, M],
 // [K, N]). Every operand's rows start 16-byte aligned and hold a multiple of
-// 8 elements (others are packed first); kp is K rounded up to 8 where a
-// k-contiguous operand is zero-padded to it, else K.
+// 8 elements (others are packed first, zero-padded to the next multiple).
 struct GemmArgs {
     const void* a;
     const void* b;
     int32_t ld_a, ld_b;  // elements
-    int32_t M, N, K, kp;
-    int32_t mp, np;      // row lengths of operands stored with k outermost (M, N rounded up to 8 when packed)
+    int32_t M, N, K;
     int32_t tiles_m, tiles_n;
     // K is `slices` slices of kGemmSlice. The first `whole` tiles (a multiple
     // of 8, or all) are one workgroup each, which finishes them; the others
@@ -60,7 +60,14 @@ struct GemmPlan {
 hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int dtype, int sum, hipStream_t st);
 hipError_t launch_gemm_join(const GemmArgs& g, int tile_m, int dtype, int sum, hipStream_t st);
 // M <= kSkinnyRows, A k-contiguous
-hipError_t launch_skinny(const GemmArgs& g, bool b_kc, int dtype, hipStream_t st);
+struct SkinnyArgs {
+    const void* a;
+    const void* b;
+    int32_t ld_a, ld_b;
+    int32_t M, N, K, slices;
+    Epilogue epi;
+};
+hipError_t launch_skinny(const SkinnyArgs& g, bool b_kc, int dtype, hipStream_t st);
 // dst [rows, 8 chunks] <- src [rows, cols] of 16-bit elements with row stride
 // ld, zero-padded; n (1 or 2) of them in a launch
 struct PackArgs {
@@ -71,29 +78,40 @@ struct PackArgs {
 };
 hipError_t launch_pack(const PackArgs* p, int n, hipStream_t st);
 
-struct NormArgs {
-    int64_t rows;
-    int32_t cols;
-    int64_t ld_x, ld_y, ld_dx, ld_r;
-    float eps;
+struct NormForward {
     const void* x;
     const float* weight;
     const float* bias;
     void* y;
     float* mean;
     float* rstd;
+    int32_t rows, cols, ld_x, ld_y;
+    float eps;
+};
+
+struct NormBackward {
     const void* dy;
+    const void* x;
+    const float* weight;
+    const float* mean;
+    const float* rstd;
     const void* add;
     void* dx;
+    float* part;  // [blocks][2][cols], or null: no column sums
+    int32_t rows, cols, ld_x, ld_y, ld_dx, ld_r, blocks;
+};
+
+// what the column sums of NormBackward's workgroups become
+struct NormSums {
+    const float* part;
     float* dweight;
     float* dbias;
-    int32_t accumulate;
-    float* part;   // [blocks][2][cols]
-    int32_t blocks;
+    int32_t cols, blocks, accumulate;
 };
 
 int norm_backward_blocks(int64_t rows, int64_t cols);
-hipError_t launch_norm_forward(const NormArgs& n, int dtype, hipStream_t st);
-hipError_t launch_norm_backward(const NormArgs& n, int dtype, hipStream_t st);
+hipError_t launch_norm_forward(const NormForward& n, int dtype, hipStream_t st);
+hipError_t launch_norm_backward(const NormBackward& n, int dtype, hipStream_t st);
+hipError_t launch_norm_sums(const NormSums& n, hipStream_t st);
 
 }  // namespace muon

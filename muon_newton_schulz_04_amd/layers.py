@@ -133,9 +133,9 @@ def linear_forward(x, w, bias=None, residual=None, activation="none", weight_lay
     n = x.shape[0]
     z = preact_out
     if z is None and save_preact:
-        z = torch.empty((n, fout), dtype=dtype, device=device)
+        z = x.new_empty((n, fout))
     if out is None:
-        out = torch.empty((n, fout), dtype=dtype, device=device)
+        out = x.new_empty((n, fout))
         ld_y = fout
     else:
         ld_y = _matrix("out", out, dtype, dev, n, fout)
@@ -165,7 +165,7 @@ def linear_grad_input(dy, w, preact=None, activation="none", add=None, weight_la
     ld_w = _matrix("w", w, dtype, dev)
     n = dy.shape[0]
     if out is None:
-        out = torch.empty((n, fin), dtype=dtype, device=device)
+        out = dy.new_empty((n, fin))
         ld_x = fin
     else:
         ld_x = _matrix("out", out, dtype, dev, n, fin)
@@ -185,13 +185,19 @@ def linear_grad_input(dy, w, preact=None, activation="none", add=None, weight_la
     return out
 
 
+def _odd(d):
+    return (d.ld_x | d.ld_w | d.ld_y | d.in_features | d.out_features) & 7
+
+
 def _run_linear(op, call, what, d, a, w, e, out, device, dev):
     pa, pw, po = a.data_ptr(), w.data_ptr(), out.data_ptr()
-    s, nbytes = B.muon_linear_workspace_bytes(d, op, pa, pw)
-    if s:
+    # most calls on sizes and strides of whole 16-byte chunks need no workspace
+    s = B.MUON_E_WORKSPACE if _odd(d) else _on(dev, call, d, pa, pw, e, po, 0, 0)
+    if s == B.MUON_E_WORKSPACE:
+        s, nbytes = B.muon_linear_workspace_bytes(d, op, pa, pw)
         _check(s, what)
-    ws, pws = _workspace(nbytes, device)
-    s = _on(dev, call, d, pa, pw, e, po, pws, nbytes)
+        ws, pws = _workspace(nbytes, device)
+        s = _on(dev, call, d, pa, pw, e, po, pws, nbytes)
     if s:
         _check(s, what)
 
@@ -218,11 +224,12 @@ def linear_grad_weight(x, dy, dw=None, dbias=None, accumulate=False, weight_layo
     pb = 0 if dbias is None else _vector("dbias", dbias, fout, dev)
     d = B.muon_linear(n, fin, fout, ld_x, ld_w, ld_y, code, lay)
     px, py, pd = x.data_ptr(), dy.data_ptr(), dw.data_ptr()
-    s, nbytes = B.muon_linear_workspace_bytes(d, B.MUON_LINEAR_GRAD_WEIGHT, px, py)
-    if s:
+    s = B.MUON_E_WORKSPACE if _odd(d) else _on(dev, B.muon_linear_grad_weight, d, px, py, pd, pb, int(accumulate), 0, 0)
+    if s == B.MUON_E_WORKSPACE:
+        s, nbytes = B.muon_linear_workspace_bytes(d, B.MUON_LINEAR_GRAD_WEIGHT, px, py)
         _check(s, "linear_grad_weight")
-    ws, pws = _workspace(nbytes, device)
-    s = _on(dev, B.muon_linear_grad_weight, d, px, py, pd, pb, int(accumulate), pws, nbytes)
+        ws, pws = _workspace(nbytes, device)
+        s = _on(dev, B.muon_linear_grad_weight, d, px, py, pd, pb, int(accumulate), pws, nbytes)
     if s:
         _check(s, "linear_grad_weight")
     return dw, dbias
@@ -242,7 +249,7 @@ def layernorm_forward(x, weight=None, bias=None, eps=1e-5, out=None):
     ld_x = _matrix("x", x, dtype, dev)
     rows, cols = x.shape
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=device)
+        out = x.new_empty((rows, cols))
         ld_y = cols
     else:
         ld_y = _matrix("out", out, dtype, dev, rows, cols)
@@ -277,7 +284,7 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, add=None, dweight=None, d
     pdw = 0 if dweight is None else _vector("dweight", dweight, cols, dev)
     pdb = 0 if dbias is None else _vector("dbias", dbias, cols, dev)
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=device)
+        out = dy.new_empty((rows, cols))
         ld_o = cols
     else:
         ld_o = _matrix("out", out, dtype, dev, rows, cols)
