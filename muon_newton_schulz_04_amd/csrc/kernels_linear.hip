@@ -736,22 +736,23 @@ __global__ __launch_bounds__(512) void k_skinny(const SkinnyArgs g) {
     finish8<T>(g.epi, row, col, left, v, bias, in, in2);
 }
 
-// Rows of any alignment and length to 16-byte aligned, zero-padded ones: one
-// 16-byte chunk per thread; one operand or both in a launch.
+// Rows of any alignment and length to 16-byte aligned, zero-padded ones: a
+// wave a row, a 16-byte chunk a lane; one operand or both in a launch.
 __global__ __launch_bounds__(256) void k_pack(const PackArgs a, const PackArgs b) {
     const PackArgs& p = blockIdx.y ? b : a;
-    const int64_t n = p.rows * p.chunks;
-    for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < n; id += (int64_t)gridDim.x * 256) {
-        const int64_t r = id / p.chunks, c = (id - r * p.chunks) * 8;
-        const uint16_t* s = static_cast<const uint16_t*>(p.src) + r * p.ld + c;
-        u32x4* d = static_cast<u32x4*>(p.dst) + id;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= p.rows) return;
+    const uint16_t* s = static_cast<const uint16_t*>(p.src) + row * p.ld;
+    u32x4* d = static_cast<u32x4*>(p.dst) + row * p.chunks;
+    for (int k = threadIdx.x & 63; k < p.chunks; k += 64) {
+        const int c = k * 8;
         if (c + 8 <= p.cols) {
-            *d = *reinterpret_cast<const u32x4_mem*>(s);
+            d[k] = *reinterpret_cast<const u32x4_mem*>(s + c);
         } else {
             uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = c + e < p.cols ? s[e] : 0u;
-            *d = u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
+            for (int e = 0; e < 8; ++e) w[e] = c + e < p.cols ? s[c + e] : 0u;
+            d[k] = u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16};
         }
     }
 }
@@ -830,11 +831,9 @@ hipError_t launch_skinny(const SkinnyArgs& g, bool b_kc, int dtype, hipStream_t 
 }
 
 hipError_t launch_pack(const PackArgs* p, int n, hipStream_t st) {
-    int64_t most = 0;
-    for (int k = 0; k < n; ++k) most = p[k].rows * p[k].chunks > most ? p[k].rows * p[k].chunks : most;
-    if (most == 0) return hipSuccess;
-    const int64_t blocks = (most + 255) / 256;
-    k_pack<<<dim3((unsigned)(blocks < 32768 ? blocks : 32768), (unsigned)n), 256, 0, st>>>(p[0], p[n - 1]);
+    const int rows = p[0].rows > p[n - 1].rows ? p[0].rows : p[n - 1].rows;
+    if (rows == 0) return hipSuccess;
+    k_pack<<<dim3(((unsigned)rows + 3) / 4, (unsigned)n), 256, 0, st>>>(p[0], p[n - 1]);
     return hipGetLastError();
 }
 

@@ -265,7 +265,7 @@ muon_status run_product(Product& P, int dtype, muon::Epilogue& E, float* sums, i
         Tensor& t = k ? P.b : P.a;
         if (!(k ? P.pack_b : P.pack_a)) continue;
         char* dst = ws + (k ? P.off_b : P.off_a);
-        packs[n++] = {t.p, t.ld, t.rows, t.cols, dst, up8(t.cols) / 8};
+        packs[n++] = {t.p, dst, (int)t.ld, (int)t.rows, (int)t.cols, (int)(up8(t.cols) / 8)};
         t.p = dst;
         t.ld = up8(t.cols);
     }

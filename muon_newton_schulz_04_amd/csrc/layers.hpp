@@ -72,9 +72,8 @@ hipError_t launch_skinny(const SkinnyArgs& g, bool b_kc, int dtype, hipStream_t 
 // ld, zero-padded; n (1 or 2) of them in a launch
 struct PackArgs {
     const void* src;
-    int64_t ld, rows, cols;
     void* dst;
-    int64_t chunks;
+    int32_t ld, rows, cols, chunks;
 };
 hipError_t launch_pack(const PackArgs* p, int n, hipStream_t st);
 
