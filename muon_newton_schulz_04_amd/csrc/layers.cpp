@@ -80,7 +80,13 @@ bool overlap(const Tensor& a, const Tensor& b) {
     const int64_t na = a.bytes(), nb = b.bytes();
     if (!a.p || !b.p || na == 0 || nb == 0) return false;
     const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+    if (x >= y + (uintptr_t)nb || y >= x + (uintptr_t)na) return false;
+    // column ranges of one buffer's rows may lie side by side
+    const uintptr_t pitch = (uintptr_t)(a.ld * a.size), ca = (uintptr_t)(a.cols * a.size),
+                    cb = (uintptr_t)(b.cols * b.size);
+    if (pitch != (uintptr_t)(b.ld * b.size)) return true;
+    const uintptr_t d = x >= y ? (x - y) % pitch : (pitch - (y - x) % pitch) % pitch;  // a's column in b's rows
+    return !(d >= cb && d + ca <= pitch);
 }
 
 bool same_tensor(const Tensor& a, const Tensor& b) { return a.p == b.p && (a.ld == b.ld || a.rows <= 1); }

@@ -131,6 +131,22 @@ int main(int argc, char** argv) {
     EXPECT(muon_linear_forward(&d, AT(1), AT(2), &e, AT(3), ws, wsn, NULL) == MUON_E_INVALID_ARG);
     e.z = AT(1);
     EXPECT(muon_linear_forward(&d, AT(1), AT(2), &e, AT(3), ws, wsn, NULL) == MUON_E_INVALID_ARG);
+    {
+        /* column ranges of one buffer of rows of 512: side by side they are apart */
+        muon_linear b = d;
+        b.ld_x = b.ld_y = 512;
+        char* const buf = AT(8);
+        EXPECT(muon_linear_forward(&b, buf, AT(2), NULL, buf + 96 * 2, ws, wsn, NULL) == reached);
+        EXPECT(muon_linear_forward(&b, buf + 128 * 2, AT(2), NULL, buf, ws, wsn, NULL) == reached);
+        EXPECT(muon_linear_forward(&b, buf, AT(2), NULL, buf + 95 * 2, ws, wsn, NULL) == MUON_E_INVALID_ARG);
+        EXPECT(muon_linear_forward(&b, buf + 127 * 2, AT(2), NULL, buf, ws, wsn, NULL) == MUON_E_INVALID_ARG);
+        /* past the row's end the range goes on in the next row */
+        EXPECT(muon_linear_forward(&b, buf, AT(2), NULL, buf + 400 * 2, ws, wsn, NULL) == MUON_E_INVALID_ARG);
+        EXPECT(muon_linear_forward(&b, buf, AT(2), NULL, buf + 384 * 2, ws, wsn, NULL) == reached);
+        EXPECT(muon_linear_forward(&b, buf + 512 * 2 * 3, AT(2), NULL, buf + 96 * 2, ws, wsn, NULL) == reached);
+        b.ld_y = 520; /* another pitch: refused */
+        EXPECT(muon_linear_forward(&b, buf, AT(2), NULL, buf + 96 * 2, ws, wsn, NULL) == MUON_E_INVALID_ARG);
+    }
     EXPECT(muon_linear_grad_weight(&d, NULL, AT(2), AT(3), NULL, 0, ws, wsn, NULL) == MUON_E_INVALID_ARG);
     EXPECT(muon_linear_grad_weight(&d, AT(1), AT(2), NULL, NULL, 0, ws, wsn, NULL) == MUON_E_INVALID_ARG);
     EXPECT(muon_linear_grad_weight(&d, AT(1), AT(2), (float*)((char*)AT(3) + 2), NULL, 0, ws, wsn, NULL) ==

@@ -542,6 +542,26 @@ def test_offsets_past_32_bits():
     _close(db[cols], oc.sum(0), _sum_tol(torch.ones(1, n, dtype=torch.float64), oc)[0], torch.float32)
 
 
+def test_column_ranges_of_one_buffer():
+    """Input, residual and output side by side in the rows of one buffer."""
+    g = _gen(4)
+    buf = _rand(g, (50, 400), torch.bfloat16)
+    keep = buf.clone()
+    w = _rand(g, (64, 96), torch.bfloat16, std=0.1)
+    x, res, y = buf[:, :64], buf[:, 64:160], buf[:, 160:256]
+    L.linear_forward(x, w, residual=res, out=y)
+    assert torch.equal(y, L.linear_forward(x.contiguous(), w, residual=res.contiguous()))
+    assert torch.equal(buf[:, :160], keep[:, :160]) and torch.equal(buf[:, 256:], keep[:, 256:])
+
+
+@pytest.mark.parametrize("act", ["relu", "relu2"])
+def test_rectifiers_of_minus_infinity(act):
+    x = torch.tensor([[float("-inf"), 0.0], [float("nan"), 0.0]]).bfloat16().cuda()
+    w = torch.tensor([[1.0], [1.0]]).bfloat16().cuda()
+    y = L.linear_forward(x, w, activation=act).cpu()
+    assert y[0].item() == 0 and y[1].isnan().all()
+
+
 def test_python_refusals():
     bf = torch.bfloat16
     x, w = torch.zeros(4, 8, dtype=bf, device="cuda"), torch.zeros(8, 16, dtype=bf, device="cuda")
