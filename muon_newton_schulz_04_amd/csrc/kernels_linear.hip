@@ -414,8 +414,12 @@ k_gemm(const GemmArgs g) {
     const int ncol = g.N - col >= 8 ? 8 : g.N - col;
     // lanes without a whole chunk fetch their row's first one, unused (rows of
     // less than one fetch nothing)
-    const int64_t ccol = inside && ncol == 8 ? col : 0;
     const int row0 = i0 + wi * WM + rr;
+    const LaneAt at(g.epi, rr, ch * 8);
+    const int wcol = j0 + wj * WN;  // the wave's first column
+    // a tile at the matrix's edge
+    const bool edge = i0 + TM > g.M || j0 + TN > g.N;
+    const int64_t ccol = inside && ncol == 8 ? col : 0;
     const bool direct = piece < 0;
     float* const part = g.partial + (int64_t)piece * (TM * TN);
     float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -428,7 +432,8 @@ k_gemm(const GemmArgs g) {
 #pragma unroll
         for (int it = 0; it < NP; ++it) {
             const int row = row0 + 32 * fi + it * RPI;
-            x[it] = first8<T>(g.epi, row < g.M ? row : g.M - 1, ccol);
+            x[it] = edge ? first8<T>(g.epi, row < g.M ? row : g.M - 1, ccol, LaneAt())
+                         : first8<T>(g.epi, row - rr, wcol, at);
         }
     };
     if (ahead) {
@@ -457,7 +462,8 @@ k_gemm(const GemmArgs g) {
 #pragma unroll
             for (int it = 0; it < NP; ++it) {
                 const int row = row0 + 32 * fi + it * RPI;
-                in2[it] = second8<T>(g.epi, row < g.M ? row : g.M - 1, ccol);
+                in2[it] = edge ? second8<T>(g.epi, row < g.M ? row : g.M - 1, ccol, LaneAt())
+                               : second8<T>(g.epi, row - rr, wcol, at);
             }
         } else if (ahead && fi + 2 < FRI) {
             fetch(fi + 2, in2);
@@ -470,7 +476,7 @@ k_gemm(const GemmArgs g) {
             if (row < g.M && inside) {
                 if (direct) {
                     float v[8] = {lo[0], lo[1], lo[2], lo[3], up[0], up[1], up[2], up[3]};
-                    finish8<T>(g.epi, row, col, ncol, v, bias, in0[it], in2[it]);
+                    finish8<T>(g.epi, row - rr, wcol, at, ncol, v, bias, in0[it], in2[it]);
                 } else {
                     float* p = part + (row - i0) * TN + (col - j0);
                     *reinterpret_cast<f32x4*>(p) = lo;
@@ -570,10 +576,10 @@ __global__ __launch_bounds__(256) void k_gemm_join(const GemmArgs g) {
     if (g.epi.bias) load8(g.epi.bias + col, left, bias);
     u32x4 in = {0, 0, 0, 0}, in2 = in;
     if (left >= 8) {
-        in = first8<T>(g.epi, row, col);
-        if (has_second(g.epi)) in2 = second8<T>(g.epi, row, col);
+        in = first8<T>(g.epi, row, col, LaneAt());
+        if (has_second(g.epi)) in2 = second8<T>(g.epi, row, col, LaneAt());
     }
-    finish8<T>(g.epi, row, col, left, v, bias, in, in2);
+    finish8<T>(g.epi, row, col, LaneAt(), left, v, bias, in, in2);
 }
 
 template <typename T>
@@ -730,10 +736,10 @@ __global__ __launch_bounds__(512) void k_skinny(const SkinnyArgs g) {
     if (g.epi.bias) load8(g.epi.bias + col, left, bias);
     u32x4 in = {0, 0, 0, 0}, in2 = in;
     if (left >= 8) {
-        in = first8<T>(g.epi, row, col);
-        if (has_second(g.epi)) in2 = second8<T>(g.epi, row, col);
+        in = first8<T>(g.epi, row, col, LaneAt());
+        if (has_second(g.epi)) in2 = second8<T>(g.epi, row, col, LaneAt());
     }
-    finish8<T>(g.epi, row, col, left, v, bias, in, in2);
+    finish8<T>(g.epi, row, col, LaneAt(), left, v, bias, in, in2);
 }
 
 // Rows of any alignment and length to 16-byte aligned, zero-padded ones: a

@@ -93,8 +93,14 @@ __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
 }
 
-constexpr float kGeluTwoK = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-constexpr float kGeluCubic = 0.044715f;
+// gelu_tanh's sigmoid(2u) = 1 / (1 + 2^(z (A + B z^2))), and 2u' = C + D z^2
+constexpr float kGeluA = -2.3022081985f;   // -2 sqrt(2 / pi) log2 e
+constexpr float kGeluB = -0.1029432397f;   // 0.044715 A
+constexpr float kGeluC = 1.5957691216f;    // 2 sqrt(2 / pi)
+constexpr float kGeluD = 0.2140644488f;    // 3 * 0.044715 C
+__device__ __forceinline__ float gelu_gate(float z, float z2) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * fmaf(kGeluB, z2, kGeluA)));
+}
 
 // gelu(z) = z Phi(z) with the normal distribution's lower tail as
 // Phi(-a) = e^(-a^2/2) t p(t), t = 1 / (1 + a / 4), a >= 0: p of degree 9 fitted
@@ -127,42 +133,41 @@ __device__ __forceinline__ float normal_cdf(float z, float& e) {
 template <int act>
 __device__ __forceinline__ float act_value(float z) {
     switch (act) {
-        case ACT_RELU: return z > 0.f ? z : z * 0.f;
+        case ACT_RELU: return z < 0.f ? 0.f : z;  // a NaN stays one
         case ACT_RELU2: {
-            const float r = z > 0.f ? z : z * 0.f;
+            const float r = z < 0.f ? 0.f : z;
             return r * r;
         }
         case ACT_GELU: {
             float e;
             return z * normal_cdf(z, e);
         }
-        case ACT_GELU_TANH: return z * sigmoid(kGeluTwoK * z * fmaf(kGeluCubic * z, z, 1.f));
+        case ACT_GELU_TANH: return z * gelu_gate(z, z * z);
         case ACT_SILU: return z * sigmoid(z);
         default: return z;
     }
 }
 
-// The derivative at z. relu'(0) = 0. Factors z times a vanishing term are
-// taken at z clamped to +-30, where that term is 0 already, so that no
-// inf * 0 comes up for a large finite z; a NaN stays one through the first term.
+// The derivative at z. relu'(0) = 0. Products of z with a vanishing term are
+// grouped, and z^2 bounded where the term is 0 already, so that no inf * 0 comes
+// up for a large finite z.
 template <int act>
 __device__ __forceinline__ float act_slope(float z) {
-    const float zc = fminf(fmaxf(z, -30.f), 30.f);
     switch (act) {
         case ACT_RELU: return z > 0.f ? 1.f : z != z ? z : 0.f;
         case ACT_RELU2: return z > 0.f ? 2.f * z : z != z ? z : 0.f;
         case ACT_GELU: {
             float e;
             const float q = normal_cdf(z, e);
-            return fmaf(zc * 0.3989422804014327f, e, q);
+            return fmaf(z * e, 0.3989422804014327f, q);
         }
         case ACT_GELU_TANH: {
-            const float q = sigmoid(kGeluTwoK * z * fmaf(kGeluCubic * z, z, 1.f));
-            return fmaf(zc * q * (1.f - q) * kGeluTwoK, fmaf(3.f * kGeluCubic * zc, zc, 1.f), q);
+            const float z2 = fminf(z * z, 900.f), q = gelu_gate(z, z2);
+            return fmaf(z * q, (1.f - q) * fmaf(kGeluD, z2, kGeluC), q);
         }
         case ACT_SILU: {
             const float q = sigmoid(z);
-            return fmaf(zc * q, 1.f - q, q);
+            return fmaf(z * q, 1.f - q, q);
         }
         default: return 1.f;
     }
@@ -193,19 +198,37 @@ __device__ __forceinline__ void act_slopes(int act, float (&v)[8]) {
 }
 #undef MUON_ACT_CASE
 
+// Where a lane's chunk lies in each tensor from an element (row, column) that
+// is the same for the whole wave: bytes, computed once, so that a chunk's
+// address is a scalar one plus a register.
+struct LaneAt {
+    uint32_t y = 0, z = 0, add = 0;
+    __device__ __forceinline__ LaneAt() {}
+    // r rows down, c columns along
+    __device__ __forceinline__ LaneAt(const Epilogue& E, int r, int c) {
+        y = (uint32_t)(r * E.ld_y + c) * (E.mode == EPI_GRAD_WEIGHT ? 4u : 2u);
+        z = (uint32_t)(r * E.ld_z + c) * 2u;
+        add = (uint32_t)(r * E.ld_add + c) * 2u;
+    }
+};
+template <typename U>
+__device__ __forceinline__ U* chunk_at(const void* p, int64_t r, int ld, int64_t c, uint32_t lane) {
+    return reinterpret_cast<U*>(const_cast<char*>(static_cast<const char*>(p)) + (r * ld + c) * (int64_t)sizeof(U) + lane);
+}
+
 // What the epilogue reads of a chunk of 8 outputs, fetched ahead of its use as
 // 16-byte vectors: first8 is z on the way back through an activation, else
 // add, or the lower half of a weight gradient to add to; second8 is add where
 // first8 is z, or the upper half.
 template <typename T>
-__device__ __forceinline__ u32x4 first8(const Epilogue& E, int64_t r, int64_t c) {
+__device__ __forceinline__ u32x4 first8(const Epilogue& E, int64_t r, int64_t c, const LaneAt& l) {
     const void* p = nullptr;
     if (E.mode == EPI_GRAD_WEIGHT) {
-        if (E.accumulate) p = static_cast<const float*>(E.y) + r * E.ld_y + c;
+        if (E.accumulate) p = chunk_at<float>(E.y, r, E.ld_y, c, l.y);
     } else if (E.mode == EPI_GRAD_INPUT && E.act != ACT_NONE) {
-        p = static_cast<const T*>(E.z) + r * E.ld_z + c;
+        p = chunk_at<T>(E.z, r, E.ld_z, c, l.z);
     } else if (E.add) {
-        p = static_cast<const T*>(E.add) + r * E.ld_add + c;
+        p = chunk_at<T>(E.add, r, E.ld_add, c, l.add);
     }
     return p ? __builtin_nontemporal_load(static_cast<const u32x4_mem*>(p)) : u32x4{0, 0, 0, 0};
 }
@@ -213,10 +236,9 @@ __device__ __forceinline__ bool has_second(const Epilogue& E) {
     return E.mode == EPI_GRAD_WEIGHT ? E.accumulate != 0 : E.mode == EPI_GRAD_INPUT && E.act != ACT_NONE && E.add;
 }
 template <typename T>
-__device__ __forceinline__ u32x4 second8(const Epilogue& E, int64_t r, int64_t c) {
-    const void* p = E.mode == EPI_GRAD_WEIGHT
-                        ? static_cast<const void*>(static_cast<const float*>(E.y) + r * E.ld_y + c + 4)
-                        : static_cast<const void*>(static_cast<const T*>(E.add) + r * E.ld_add + c);
+__device__ __forceinline__ u32x4 second8(const Epilogue& E, int64_t r, int64_t c, const LaneAt& l) {
+    const void* p = E.mode == EPI_GRAD_WEIGHT ? static_cast<const void*>(chunk_at<float>(E.y, r, E.ld_y, c, l.y) + 4)
+                                              : static_cast<const void*>(chunk_at<T>(E.add, r, E.ld_add, c, l.add));
     return __builtin_nontemporal_load(static_cast<const u32x4_mem*>(p));
 }
 
@@ -227,15 +249,15 @@ __device__ __forceinline__ void widen8(const u32x4& u, float (&v)[8]) {
     for (int e = 0; e < 8; ++e) v[e] = (float)t[e];
 }
 
-// The epilogue of 8 consecutive accumulators of row r from column c on, n of
-// them inside the matrix. bias: their bias values (forward). in, in2: first8's
+// The epilogue of 8 consecutive accumulators from row r, column c (and the
+// lane's place from there) on, n of them inside the matrix. bias: their bias values (forward). in, in2: first8's
 // and second8's if n is 8 or more; a chunk at the matrix's edge is read in place.
 template <typename T>
-__device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c, int n, float (&v)[8],
+__device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c, const LaneAt& l, int n, float (&v)[8],
                                         const float (&bias)[8], const u32x4& in, const u32x4& in2) {
     float t[8];
     if (E.mode == EPI_GRAD_WEIGHT) {
-        float* y = static_cast<float*>(E.y) + r * E.ld_y + c;
+        float* y = chunk_at<float>(E.y, r, E.ld_y, c, l.y);
         if (E.accumulate) {
             if (n >= 8) {
                 const f32x4 lo = __builtin_bit_cast(f32x4, in), up = __builtin_bit_cast(f32x4, in2);
@@ -257,14 +279,14 @@ __device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c,
     if (E.mode == EPI_FORWARD) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += bias[e];
-        if (E.z) stream8(static_cast<T*>(E.z) + r * E.ld_z + c, n, v);
+        if (E.z) stream8(chunk_at<T>(E.z, r, E.ld_z, c, l.z), n, v);
         act_values(E.act, v);
     } else if (E.act != ACT_NONE) {
         fetched = true;
         if (n >= 8)
             widen8<T>(in, t);
         else
-            load8(static_cast<const T*>(E.z) + r * E.ld_z + c, n, t);
+            load8(chunk_at<const T>(E.z, r, E.ld_z, c, l.z), n, t);
         act_slopes(E.act, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= t[e];
@@ -275,11 +297,11 @@ __device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c,
         else if (n >= 8)
             widen8<T>(in, t);
         else
-            load8(static_cast<const T*>(E.add) + r * E.ld_add + c, n, t);
+            load8(chunk_at<const T>(E.add, r, E.ld_add, c, l.add), n, t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += t[e];
     }
-    stream8(static_cast<T*>(E.y) + r * E.ld_y + c, n, v);
+    stream8(chunk_at<T>(E.y, r, E.ld_y, c, l.y), n, v);
 }
 
 }  // namespace muon
