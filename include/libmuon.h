@@ -295,7 +295,8 @@ enum { MUON_LINEAR_FORWARD = 0, MUON_LINEAR_GRAD_INPUT = 1, MUON_LINEAR_GRAD_WEI
 
 /* One linear layer on one batch. dtype (bf16 or fp16) is the type of X, W, Y
  * and of their gradients dX, dY; bias and the weight gradients are float32.
- * tokens < 2^24, features and strides at most 2^21. */
+ * tokens < 2^24, features and strides at most 2^21, and an output holds fewer
+ * than 2^35 elements (MUON_E_SHAPE). */
 typedef struct muon_linear {
     int64_t tokens;
     int64_t in_features;

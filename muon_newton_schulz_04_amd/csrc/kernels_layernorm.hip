@@ -550,14 +550,17 @@ hipError_t backward_t(const NormBackward& n, hipStream_t st) {
 }  // namespace
 
 // Workgroups of the backward pass (each leaves one partial row of column
-// sums): of at least 8 rows, up to three a CU of 4 waves (one of 8 beyond 4096
-// columns). 16384 x 1600 bf16: 512 workgroups 56 us, 768 51, 1024 51; 4099 x
-// 1003 fp32: 512 18.5 us, 768 21. For rows longer than registers hold, runs of
-// at least 64 rows.
-int norm_backward_blocks(int64_t rows, int64_t cols) {
+// sums), of at least 8 rows: as many as are on the chip at once, since one more
+// takes a whole pass of its own. 16-bit rows of whole chunks leave room for
+// three a CU of 4 waves (16384 x 1600: 512 workgroups 56 us, 768 51, 1024 51),
+// the others' registers for two (512 workgroups against 750 or 768: 6000 x 1003
+// fp32 20.0 us and 27.0, 16384 x 1600 fp32 64.0 and 77.2, 16384 x 1601 bf16 52.1
+// and 66.4); beyond 4096 columns one of 8 waves. For rows longer than registers
+// hold, runs of at least 64 rows.
+int norm_backward_blocks(int64_t rows, int64_t cols, int dtype) {
     if (rows == 0) return 0;
     const int64_t b = cols <= kBlockCols ? rows / 8 : rows / 64;
-    const int64_t most = cols <= 4096 ? 768 : cols <= kBlockCols ? 256 : 64;
+    const int64_t most = cols > kBlockCols ? 64 : cols > 4096 ? 256 : dtype != 2 && cols % 8 == 0 ? 768 : 512;
     return (int)(b < 1 ? 1 : b < most ? b : most);
 }
 

@@ -389,7 +389,7 @@ muon_status check_norm(const muon_layernorm* d) {
 int64_t stride_of(int64_t ld, int64_t cols) { return ld ? ld : cols; }
 
 size_t norm_workspace(const muon_layernorm& d) {
-    return up256((size_t)muon::norm_backward_blocks(d.rows, d.cols) * 2 * (size_t)d.cols * 4);
+    return up256((size_t)muon::norm_backward_blocks(d.rows, d.cols, d.dtype) * 2 * (size_t)d.cols * 4);
 }
 
 }  // namespace
@@ -515,7 +515,7 @@ muon_status muon_layernorm_backward(const muon_layernorm* d, const void* dy, con
         TRY(check_disjoint(K, {DY, X, R, W, M, S}, nullptr));
         if (d->rows == 0 && (!sums || accumulate)) return MUON_OK;
         TRY(check_device());
-        const int blocks = muon::norm_backward_blocks(d->rows, d->cols);
+        const int blocks = muon::norm_backward_blocks(d->rows, d->cols, d->dtype);
         float* part = sums ? static_cast<float*>(workspace) : nullptr;
         hipStream_t st = static_cast<hipStream_t>(stream);
         if (d->rows > 0) {

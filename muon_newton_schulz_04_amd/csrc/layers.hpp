@@ -108,7 +108,7 @@ struct NormSums {
     int32_t cols, blocks, accumulate;
 };
 
-int norm_backward_blocks(int64_t rows, int64_t cols);
+int norm_backward_blocks(int64_t rows, int64_t cols, int dtype);
 hipError_t launch_norm_forward(const NormForward& n, int dtype, hipStream_t st);
 hipError_t launch_norm_backward(const NormBackward& n, int dtype, hipStream_t st);
 hipError_t launch_norm_sums(const NormSums& n, hipStream_t st);
