@@ -30,6 +30,8 @@
 //  * Tiles that a round of the chip leaves over go in K pieces beside whole
 //    ones: each piece leaves fp32 sums in the workspace and a second kernel adds
 //    them in order and does the epilogue (the same bits every run).
+//  * Rows off 16-byte borders go through registers for the small tile
+//    (RawOperand) and are packed first for the others.
 //  * Up to 32 rows of A have a kernel of their own (k_skinny).
 
 #include "layer_device.hpp"
@@ -167,6 +169,85 @@ struct Operand {
     }
 };
 
+// An operand whose rows start anywhere and end anywhere (8 elements at least),
+// through registers: 16 bytes a lane, then to where Operand's loads put them. In
+// the last slice, a chunk that would pass its row's end holds the row's last 8
+// elements, which are moved down on the way to LDS, and zeros fill the k values
+// past the end; in the others it reads on, up to 7 elements towards the next row
+// (moved down there too, the tiles at the edge were the last to end: weight
+// gradient of 999 x 1001 x 777 15.5 us). A tile's rows or columns past the
+// matrix hold anything: nothing of their products is stored.
+template <typename T, int TILE, bool KC>
+struct RawOperand : Operand<T, TILE, KC> {
+    using Base = Operand<T, TILE, KC>;
+    static constexpr int NLD = Base::NLD;
+    static constexpr int STEP = KC ? 32 : 32 * 64 / TILE;  // rows from one chunk of a lane to its next
+    const char* p;             // KC: the tile's first row; else the next slice's (from the end on the last one's)
+    uint32_t roff[NLD];        // byte offsets of the lane's rows
+    uint32_t col, whole;       // not KC: byte offsets of the lane's chunk, and of one that is wholly in its row
+    int row, at, end;          // the lane's first row; KC: its chunk's first k in a slice, and one past the last k
+    int over;                  // not KC: elements from `whole` to the chunk
+    int put_left;              // k values from the next slice to put to the end
+
+    __device__ __forceinline__ void init(const void* src, int stride, int i0, int n, int kb, int kend, int wave,
+                                         int lane, int wblk) {
+        Base::init(src, stride, i0, n, 0, kb, kend, wave, lane, wblk);
+        put_left = this->left;
+        end = kend;
+        p = static_cast<const char*>(src) + (int64_t)(KC ? i0 : kb) * this->rowb;
+        if constexpr (KC) {
+            row = wave * 8 + (lane >> 3);
+            at = this->kch;
+        } else {
+            constexpr int XCH = TILE / 8;
+            row = wave * (64 / XCH) + lane / XCH;
+            const int c = i0 + 8 * ((lane % XCH) ^ Base::turn(row));
+            over = c + 8 > n && c < n ? c + 8 - n : 0;
+            whole = 2u * (uint32_t)(c + 8 <= n ? c : n - 8);
+            col = c < n ? 2u * (uint32_t)c : whole;
+        }
+#pragma unroll
+        for (int q = 0; q < NLD; ++q) {
+            int r = row + q * STEP;
+            if (KC && r > n - i0 - 1) r = n - i0 - 1;
+            roff[q] = (uint32_t)r * this->rowb;
+        }
+    }
+    // the next slice's chunks
+    __device__ __forceinline__ void fetch(u32x4 (&v)[NLD]) {
+        const int left = this->left;
+        uint32_t o, last = ~0u;
+        if constexpr (KC) {
+            const int k = end - left + at;
+            o = 2u * (uint32_t)(k < end - 8 ? k : end - 8);
+        } else {
+            const int rows = left < 1 ? 1 : left < BK ? left : BK;
+            last = (uint32_t)(rows - 1) * this->rowb;
+            o = left > BK ? col : whole;
+        }
+#pragma unroll
+        for (int q = 0; q < NLD; ++q)
+            v[q] = *reinterpret_cast<const u32x4_mem*>(p + ((roff[q] < last ? roff[q] : last) + o));
+        if (!KC) p += left > BK ? (int64_t)BK * this->rowb : 0;
+        this->left -= BK;
+    }
+    // fetched chunks to LDS
+    __device__ __forceinline__ void put(char* S, int lane, u32x4 (&v)[NLD]) {
+        if (put_left <= BK) {
+            const int o = KC ? at + 8 - put_left : over;
+#pragma unroll
+            for (int q = 0; q < NLD; ++q) {
+                const unsigned __int128 w = __builtin_bit_cast(unsigned __int128, v[q]);
+                if (o > 0) v[q] = __builtin_bit_cast(u32x4, o < 8 ? w >> (16 * o) : (unsigned __int128)0);
+                if (!KC && row + q * STEP >= put_left) v[q] = u32x4{0, 0, 0, 0};
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < NLD; ++q) *reinterpret_cast<u32x4*>(S + this->lds_row + q * 4096 + lane * 16) = v[q];
+        put_left -= BK;
+    }
+};
+
 // Workgroups go round-robin over the 8 XCDs: of `total` of them, each XCD takes
 // one contiguous run of the logical order, so what it works on at once shares
 // operand panels in its L2.
@@ -204,12 +285,12 @@ __device__ __forceinline__ float add8(f16x8 f, float v) {
 
 // SUM: also the sums over k of the B (1) or A (2) operand's rows, for the bias
 // gradient: two-element dot products with 1 on the fragments in registers, in
-// the shadow of the matrix instructions.
-template <typename T, int TM, int TN, bool AKC, bool BKC, int SUM>
+// the shadow of the matrix instructions. RAW: operands as RawOperand has them.
+template <typename T, int TM, int TN, bool AKC, bool BKC, int SUM, bool RAW>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ? 1 : 2, TM == 128 ? 1 : 2))) void
 k_gemm(const GemmArgs g) {
-    using OA = Operand<T, TM, AKC>;
-    using OB = Operand<T, TN, BKC>;
+    using OA = std::conditional_t<RAW, RawOperand<T, TM, AKC>, Operand<T, TM, AKC>>;
+    using OB = std::conditional_t<RAW, RawOperand<T, TN, BKC>, Operand<T, TN, BKC>>;
     constexpr int WM = TM / 2, WN = TN / 2;   // a wave's block
     constexpr int FRI = WM / 32, FRJ = WN / 32;
     constexpr int SROW = WN * 4 + 16;  // bytes of a staged epilogue row
@@ -218,7 +299,7 @@ k_gemm(const GemmArgs g) {
     // time is load latency: a ring of four buffers of both
     constexpr bool RING = TM <= 128;
     constexpr int STAGE = OA::BYTES + OB::BYTES;
-    constexpr int SMEM = RING ? 4 * STAGE : OA::BYTES + STAGE;
+    constexpr int SMEM = RAW ? 2 * STAGE : RING ? 4 * STAGE : OA::BYTES + STAGE;
     static_assert(4 * 32 * SROW <= SMEM, "epilogue staging");
     __shared__ __attribute__((aligned(16))) char smem[SMEM];
 
@@ -241,7 +322,7 @@ k_gemm(const GemmArgs g) {
     }
     // a k-contiguous operand's rows go on to the next multiple of 8 (zeros), the
     // rows of the others likewise
-    const int kp = (g.K + 7) & ~7, kmax = AKC || BKC ? kp : g.K;
+    const int kp = (g.K + 7) & ~7, kmax = (AKC || BKC) && !RAW ? kp : g.K;
     int ti, tj;
     tile_at(g, tile, ti, tj);
     const int i0 = ti * TM, j0 = tj * TN;
@@ -251,8 +332,13 @@ k_gemm(const GemmArgs g) {
 
     OA A;
     OB B;
-    A.init(g.a, g.ld_a, i0, AKC ? g.M : (g.M + 7) & ~7, kp, kb, AKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wi);
-    B.init(g.b, g.ld_b, j0, BKC ? g.N : (g.N + 7) & ~7, kp, kb, BKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wj);
+    if constexpr (RAW) {
+        A.init(g.a, g.ld_a, i0, g.M, kb, ke, wave, lane, wi);
+        B.init(g.b, g.ld_b, j0, g.N, kb, ke, wave, lane, wj);
+    } else {
+        A.init(g.a, g.ld_a, i0, AKC ? g.M : (g.M + 7) & ~7, kp, kb, AKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wi);
+        B.init(g.b, g.ld_b, j0, BKC ? g.N : (g.N + 7) & ~7, kp, kb, BKC ? ke : (ke < g.K ? ke : g.K), wave, lane, wj);
+    }
 
     f32x16 acc[FRI][FRJ];
 #pragma unroll
@@ -307,7 +393,58 @@ k_gemm(const GemmArgs g) {
     using CH = std::integral_constant<int, FRI * FRJ / 2>;
 
     const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)smem;
-    if constexpr (!RING) {
+    if constexpr (RAW) {
+        // two slices in LDS, the three after the current one in registers or
+        // on their way there
+        u32x4 ra[3][OA::NLD], rb[3][OB::NLD];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            A.fetch(ra[k]);
+            B.fetch(rb[k]);
+        }
+        A.put(smem, lane, ra[0]);
+        B.put(smem + OA::BYTES, lane, rb[0]);
+        __syncthreads();
+        read_b(smem + OA::BYTES, 0);
+        read_a(smem, 0);
+        // slice kt: the one three on goes into registers F (kt's own were put in
+        // the slice before), the next one's P into LDS, where every wave had
+        // read slice kt - 1 before the last barrier
+        auto slice = [&](int kt, auto f_c, auto p_c) __attribute__((always_inline)) {
+            constexpr int F = decltype(f_c)::value, P = decltype(p_c)::value;
+            char* const S = smem + (kt & 1) * STAGE;
+            char* const N = smem + (~kt & 1) * STAGE;
+            A.fetch(ra[F]);
+            B.fetch(rb[F]);
+            __builtin_amdgcn_sched_barrier(0);
+            static_for<0, NKS>([&](auto k_c) {
+                constexpr int KS = decltype(k_c)::value;
+                if constexpr (KS + 1 < NKS) {
+                    read_b(S + OA::BYTES, KS + 1);
+                    read_a(S, KS + 1);
+                }
+                products(KS, 0, FRI);
+                add_sums(KS);
+                if constexpr (KS == 0) {
+                    A.put(N, lane, ra[P]);
+                    B.put(N + OA::BYTES, lane, rb[P]);
+                }
+            });
+            __syncthreads();
+            read_b(N + OA::BYTES, 0);
+            read_a(N, 0);
+        };
+        using I0 = std::integral_constant<int, 0>;
+        using I1 = std::integral_constant<int, 1>;
+        using I2 = std::integral_constant<int, 2>;
+        for (int kt = 0; kt < nk; kt += 3) {
+            slice(kt, I0{}, I1{});
+            if (kt + 1 == nk) break;
+            slice(kt + 1, I1{}, I2{});
+            if (kt + 2 == nk) break;
+            slice(kt + 2, I2{}, I0{});
+        }
+    } else if constexpr (!RING) {
         char* const SB = smem + 2 * OA::BYTES;
         A.load(lds0);
         B.load(lds0 + 2 * OA::BYTES);
@@ -763,19 +900,19 @@ __global__ __launch_bounds__(256) void k_pack(const PackArgs a, const PackArgs b
     }
 }
 
-template <typename T, int TM, int TN>
+template <typename T, int TM, int TN, bool RAW>
 hipError_t gemm_t(const GemmArgs& g, bool a_kc, bool b_kc, int sum, hipStream_t st) {
     const int wgs = g.whole + (g.tiles_m * g.tiles_n - g.whole) * g.splits;
     if (a_kc && b_kc)
-        k_gemm<T, TM, TN, true, true, 0><<<wgs, 256, 0, st>>>(g);
+        k_gemm<T, TM, TN, true, true, 0, RAW><<<wgs, 256, 0, st>>>(g);
     else if (a_kc)
-        k_gemm<T, TM, TN, true, false, 0><<<wgs, 256, 0, st>>>(g);
+        k_gemm<T, TM, TN, true, false, 0, RAW><<<wgs, 256, 0, st>>>(g);
     else if (sum == 0)
-        k_gemm<T, TM, TN, false, false, 0><<<wgs, 256, 0, st>>>(g);
+        k_gemm<T, TM, TN, false, false, 0, RAW><<<wgs, 256, 0, st>>>(g);
     else if (sum == 1)
-        k_gemm<T, TM, TN, false, false, 1><<<wgs, 256, 0, st>>>(g);
+        k_gemm<T, TM, TN, false, false, 1, RAW><<<wgs, 256, 0, st>>>(g);
     else
-        k_gemm<T, TM, TN, false, false, 2><<<wgs, 256, 0, st>>>(g);
+        k_gemm<T, TM, TN, false, false, 2, RAW><<<wgs, 256, 0, st>>>(g);
     return hipGetLastError();
 }
 
@@ -809,10 +946,11 @@ hipError_t join_t(const GemmArgs& g, int sum, hipStream_t st) {
 }
 
 template <typename T>
-hipError_t gemm_tile(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int sum, hipStream_t st) {
-    return tile_m == 256   ? gemm_t<T, 256, 128>(g, a_kc, b_kc, sum, st)
-           : tile_m == 128 ? gemm_t<T, 128, 128>(g, a_kc, b_kc, sum, st)
-                           : gemm_t<T, 64, 64>(g, a_kc, b_kc, sum, st);
+hipError_t gemm_tile(const GemmArgs& g, int tile_m, bool raw, bool a_kc, bool b_kc, int sum, hipStream_t st) {
+    return tile_m == 256   ? gemm_t<T, 256, 128, false>(g, a_kc, b_kc, sum, st)
+           : tile_m == 128 ? gemm_t<T, 128, 128, false>(g, a_kc, b_kc, sum, st)
+           : raw           ? gemm_t<T, 64, 64, true>(g, a_kc, b_kc, sum, st)
+                           : gemm_t<T, 64, 64, false>(g, a_kc, b_kc, sum, st);
 }
 template <typename T>
 hipError_t join_tile(const GemmArgs& g, int tile_m, int sum, hipStream_t st) {
@@ -823,8 +961,10 @@ hipError_t join_tile(const GemmArgs& g, int tile_m, int sum, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int dtype, int sum, hipStream_t st) {
-    return dtype == 0 ? gemm_tile<bf16>(g, tile_m, a_kc, b_kc, sum, st) : gemm_tile<f16>(g, tile_m, a_kc, b_kc, sum, st);
+hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool raw, bool a_kc, bool b_kc, int dtype, int sum,
+                       hipStream_t st) {
+    return dtype == 0 ? gemm_tile<bf16>(g, tile_m, raw, a_kc, b_kc, sum, st)
+                      : gemm_tile<f16>(g, tile_m, raw, a_kc, b_kc, sum, st);
 }
 
 hipError_t launch_gemm_join(const GemmArgs& g, int tile_m, int dtype, int sum, hipStream_t st) {

@@ -220,6 +220,7 @@ struct Product {
     Tensor a, b;
     bool a_kc, b_kc;  // k is the contiguous index
     bool pack_a, pack_b;
+    bool raw;  // the small tiles read rows as they are
     muon::GemmPlan plan;
     size_t off_a, off_b, off_part, off_sums, bytes;
 };
@@ -248,6 +249,12 @@ muon_status plan_product(const muon_linear& d, int op, const void* pa, const voi
         P->plan = {0, 0, 0, 0, (int)((P->K + muon::kGemmSlice - 1) / muon::kGemmSlice), 0, 0, 0};
     else
         P->plan = choose_plan(P->M, P->N, P->K);
+    // Copies to aligned rows are a launch of their own, 3 to 6 us of the chip
+    // and 3 of the host, which only the larger tiles' loads need (us, copied and
+    // as they are: 60 x 333 x 257 14.3, 8.3; 999 x 1001 x 777 14.8, 10.6; 1024 x
+    // 1601 x 1599 26.7, 20.7; weight gradient 4099 x 1001 x 1003 31.5, 29.0).
+    P->raw = (P->pack_a || P->pack_b) && P->plan.tile_m == 64 && P->a.cols >= 8 && P->b.cols >= 8;
+    if (P->raw) P->pack_a = P->pack_b = false;
     size_t o = 0;
     P->off_a = o;
     if (P->pack_a) o = up256(o + (size_t)P->a.rows * up8(P->a.cols) * 2);
@@ -299,7 +306,7 @@ muon_status run_product(Product& P, int dtype, muon::Epilogue& E, float* sums, i
     g.sums = sums;
     g.sum_part = reinterpret_cast<float*>(ws + P.off_sums);
     g.epi = E;
-    TRY(hip_status(muon::launch_gemm(g, G.tile_m, P.a_kc, P.b_kc, dtype, sum, st), "product kernel"));
+    TRY(hip_status(muon::launch_gemm(g, G.tile_m, P.raw, P.a_kc, P.b_kc, dtype, sum, st), "product kernel"));
     if (G.whole < G.tiles_m * G.tiles_n) TRY(hip_status(muon::launch_gemm_join(g, G.tile_m, dtype, sum, st), "join kernel"));
     return MUON_OK;
 }

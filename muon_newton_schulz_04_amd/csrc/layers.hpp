@@ -30,7 +30,8 @@ struct Epilogue {
 // C[M, N] = sum_k A(m, k) B(k, n) over 16-bit operands, each stored with its k
 // index contiguous ([M, K], [N, K]) or its other index contiguous ([K, M],
 // [K, N]). Every operand's rows start 16-byte aligned and hold a multiple of
-// 8 elements (others are packed first, zero-padded to the next multiple).
+// 8 elements (others are packed first, zero-padded to the next multiple), or,
+// for a raw product (64 x 64 tiles), start anywhere and hold 8 or more.
 struct GemmArgs {
     const void* a;
     const void* b;
@@ -57,7 +58,8 @@ struct GemmPlan {
 };
 
 // sum: the bias gradient is the sums over k of neither (0), B's (1) or A's (2) rows
-hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool a_kc, bool b_kc, int dtype, int sum, hipStream_t st);
+hipError_t launch_gemm(const GemmArgs& g, int tile_m, bool raw, bool a_kc, bool b_kc, int dtype, int sum,
+                       hipStream_t st);
 hipError_t launch_gemm_join(const GemmArgs& g, int tile_m, int dtype, int sum, hipStream_t st);
 // M <= kSkinnyRows, A k-contiguous
 struct SkinnyArgs {

@@ -185,14 +185,15 @@ def linear_grad_input(dy, w, preact=None, activation="none", add=None, weight_la
     return out
 
 
-def _odd(d):
-    return (d.ld_x | d.ld_w | d.ld_y | d.in_features | d.out_features) & 7
+def _few_odd(d):
+    """Few tokens, and rows that start or end off a 16-byte border: packed first."""
+    return d.tokens <= 32 and (d.ld_x | d.ld_w | d.ld_y | d.in_features | d.out_features) & 7
 
 
 def _run_linear(op, call, what, d, a, w, e, out, device, dev):
     pa, pw, po = a.data_ptr(), w.data_ptr(), out.data_ptr()
-    # most calls on sizes and strides of whole 16-byte chunks need no workspace
-    s = B.MUON_E_WORKSPACE if _odd(d) else _on(dev, call, d, pa, pw, e, po, 0, 0)
+    # most other calls need no workspace
+    s = B.MUON_E_WORKSPACE if _few_odd(d) else _on(dev, call, d, pa, pw, e, po, 0, 0)
     if s == B.MUON_E_WORKSPACE:
         s, nbytes = B.muon_linear_workspace_bytes(d, op, pa, pw)
         _check(s, what)
@@ -224,7 +225,7 @@ def linear_grad_weight(x, dy, dw=None, dbias=None, accumulate=False, weight_layo
     pb = 0 if dbias is None else _vector("dbias", dbias, fout, dev)
     d = B.muon_linear(n, fin, fout, ld_x, ld_w, ld_y, code, lay)
     px, py, pd = x.data_ptr(), dy.data_ptr(), dw.data_ptr()
-    s = B.MUON_E_WORKSPACE if _odd(d) else _on(dev, B.muon_linear_grad_weight, d, px, py, pd, pb, int(accumulate), 0, 0)
+    s = _on(dev, B.muon_linear_grad_weight, d, px, py, pd, pb, int(accumulate), 0, 0)
     if s == B.MUON_E_WORKSPACE:
         s, nbytes = B.muon_linear_workspace_bytes(d, B.MUON_LINEAR_GRAD_WEIGHT, px, py)
         _check(s, "linear_grad_weight")

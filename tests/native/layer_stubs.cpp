@@ -3,7 +3,7 @@
 #include "layers.hpp"
 
 namespace muon {
-hipError_t launch_gemm(const GemmArgs&, int, bool, bool, int, int, hipStream_t) { return hipSuccess; }
+hipError_t launch_gemm(const GemmArgs&, int, bool, bool, bool, int, int, hipStream_t) { return hipSuccess; }
 hipError_t launch_gemm_join(const GemmArgs&, int, int, int, hipStream_t) { return hipSuccess; }
 hipError_t launch_skinny(const SkinnyArgs&, bool, int, hipStream_t) { return hipSuccess; }
 hipError_t launch_pack(const PackArgs*, int, hipStream_t) { return hipSuccess; }

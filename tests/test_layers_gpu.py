@@ -618,3 +618,39 @@ def test_subnormal_operands_count(rows, dtype, tiny, big):
                                       weight_layout=layout)
         assert (dw.double() == rows * tiny * big).all()
         assert (db.double() == rows * tiny).all()
+
+
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+@pytest.mark.parametrize("size", [(65, 9, 15), (64, 65, 8), (100, 129, 71), (700, 1001, 333), (4099, 95, 103)], ids=str)
+def test_linear_rows_off_borders(size, layout):
+    """Small products of rows that start and end off 16-byte borders: rows of one
+    chunk and a little, an edge one column into a tile, k tails, K pieces."""
+    test_linear_sizes(size, "fp16", layout)
+
+
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+@pytest.mark.parametrize("size", [(70, 73, 67), (700, 1001, 75)], ids=str)
+def test_linear_values_beside_the_operands(size, layout):
+    """NaN right before, between and behind an operand's rows reaches nothing,
+    and the results do not depend on where the rows start."""
+    n, i, o = size
+    g = _gen(i)
+    wr, wc = (i, o) if layout == "in_out" else (o, i)
+    x0, w0 = _rand(g, (n, i), torch.bfloat16), _rand(g, (wr, wc), torch.bfloat16, std=i ** -0.5)
+    dy0 = _rand(g, (n, o), torch.bfloat16, std=0.1)
+    kw = {"weight_layout": layout}
+    want = (L.linear_forward(x0, w0, **kw), L.linear_grad_input(dy0, w0, **kw),
+            *L.linear_grad_weight(x0, dy0, dbias=True, **kw))
+    for first, pad in ((0, 8), (3, 0), (1, 7), (5, 2)):
+        def off(s):
+            r, c = s.shape
+            buf = _flat(first + r * (c + pad) + 16, float("nan"), 0, s.dtype)
+            v = buf[first:first + r * (c + pad)].view(r, c + pad)[:, :c]
+            v.copy_(s)
+            return v
+
+        x, w, dy = off(x0), off(w0), off(dy0)
+        got = (L.linear_forward(x, w, **kw), L.linear_grad_input(dy, w, **kw),
+               *L.linear_grad_weight(x, dy, dbias=True, **kw))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
