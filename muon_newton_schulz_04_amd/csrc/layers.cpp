@@ -252,7 +252,8 @@ muon_status plan_product(const muon_linear& d, int op, const void* pa, const voi
     // Copies to aligned rows are a launch of their own, 3 to 6 us of the chip
     // and 3 of the host, which only the larger tiles' loads need (us, copied and
     // as they are: 60 x 333 x 257 14.3, 8.3; 999 x 1001 x 777 14.8, 10.6; 1024 x
-    // 1601 x 1599 26.7, 20.7; weight gradient 4099 x 1001 x 1003 31.5, 29.0).
+    // 1601 x 1599 26.7, 20.7; weight gradient 4099 x 1001 x 1003 31.5, 29.0; with
+    // 128 x 128 tiles, that of 2048 x 1601 x 1599 31.5, 37.6).
     P->raw = (P->pack_a || P->pack_b) && P->plan.tile_m == 64 && P->a.cols >= 8 && P->b.cols >= 8;
     if (P->raw) P->pack_a = P->pack_b = false;
     size_t o = 0;
