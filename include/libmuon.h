@@ -327,8 +327,9 @@ typedef struct muon_epilogue {
  * x, w; grad input: dy, w; grad weight: x, dy), of which only the alignment is
  * looked at: operands whose rows do not start 16-byte aligned or whose length
  * is no multiple of 8 are first copied to aligned rows in the workspace, except
- * for small products, which read them as they are (and up to 7 elements of the
- * gap between two rows, whose values do not matter). Host-only. */
+ * for small products and few tokens, which read them as they are (and up to 7
+ * elements of the gap between two rows, whose values do not matter).
+ * Host-only. */
 muon_status muon_linear_workspace_bytes(const muon_linear* d, int32_t op, const void* a, const void* b,
                                         size_t* out_bytes);
 

@@ -32,7 +32,8 @@
 //    them in order and does the epilogue (the same bits every run).
 //  * Rows off 16-byte borders go through registers for the small tile
 //    (RawOperand) and are packed first for the others.
-//  * Up to 32 rows of A have a kernel of their own (k_skinny).
+//  * Up to 32 rows of A, unless through registers, have a kernel of their own
+//    (k_skinny).
 
 #include "layer_device.hpp"
 

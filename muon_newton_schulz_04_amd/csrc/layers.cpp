@@ -245,16 +245,19 @@ muon_status plan_product(const muon_linear& d, int op, const void* pa, const voi
     // launches hold fewer than 2^32 threads
     if (((P->M + 127) / 128) * ((P->N + 127) / 128) >= (int64_t)1 << 21)
         return fail(MUON_E_SHAPE, "linear: output too large");
-    if (op != MUON_LINEAR_GRAD_WEIGHT && P->M <= muon::kSkinnyRows)
-        P->plan = {0, 0, 0, 0, (int)((P->K + muon::kGemmSlice - 1) / muon::kGemmSlice), 0, 0, 0};
-    else
-        P->plan = choose_plan(P->M, P->N, P->K);
     // Copies to aligned rows are a launch of their own, 3 to 6 us of the chip
     // and 3 of the host, which only the larger tiles' loads need (us, copied and
     // as they are: 60 x 333 x 257 14.3, 8.3; 999 x 1001 x 777 14.8, 10.6; 1024 x
     // 1601 x 1599 26.7, 20.7; weight gradient 4099 x 1001 x 1003 31.5, 29.0; with
-    // 128 x 128 tiles, that of 2048 x 1601 x 1599 31.5, 37.6).
-    P->raw = (P->pack_a || P->pack_b) && P->plan.tile_m == 64 && P->a.cols >= 8 && P->b.cols >= 8;
+    // 128 x 128 tiles, that of 2048 x 1601 x 1599 31.5, 37.6). So few tokens on
+    // such rows leave their own kernel, too (1 x 1001 x 777 13.0, 9.6; 24 x 6401 x
+    // 1599 29.6, 14.6; 8 x 1600 x 50257 127, 32).
+    const bool few = op != MUON_LINEAR_GRAD_WEIGHT && P->M <= muon::kSkinnyRows;
+    const bool can = (P->pack_a || P->pack_b) && P->a.cols >= 8 && P->b.cols >= 8;
+    if (!few || can) P->plan = choose_plan(P->M, P->N, P->K);
+    P->raw = can && P->plan.tile_m == 64;
+    if (few && !P->raw)
+        P->plan = {0, 0, 0, 0, (int)((P->K + muon::kGemmSlice - 1) / muon::kGemmSlice), 0, 0, 0};
     if (P->raw) P->pack_a = P->pack_b = false;
     size_t o = 0;
     P->off_a = o;

@@ -185,15 +185,10 @@ def linear_grad_input(dy, w, preact=None, activation="none", add=None, weight_la
     return out
 
 
-def _few_odd(d):
-    """Few tokens, and rows that start or end off a 16-byte border: packed first."""
-    return d.tokens <= 32 and (d.ld_x | d.ld_w | d.ld_y | d.in_features | d.out_features) & 7
-
-
 def _run_linear(op, call, what, d, a, w, e, out, device, dev):
     pa, pw, po = a.data_ptr(), w.data_ptr(), out.data_ptr()
-    # most other calls need no workspace
-    s = B.MUON_E_WORKSPACE if _few_odd(d) else _on(dev, call, d, pa, pw, e, po, 0, 0)
+    # most calls need no workspace
+    s = _on(dev, call, d, pa, pw, e, po, 0, 0)
     if s == B.MUON_E_WORKSPACE:
         s, nbytes = B.muon_linear_workspace_bytes(d, op, pa, pw)
         _check(s, what)

@@ -154,9 +154,9 @@ int main(int argc, char** argv) {
     EXPECT(muon_linear_grad_weight(&d, AT(1), AT(2), AT(3), AT(3), 0, ws, wsn, NULL) == MUON_E_INVALID_ARG);
     EXPECT(muon_linear_grad_weight(&d, AT(1), AT(2), AT(3), AT(4), 1, ws, wsn, NULL) == reached);
 
-    /* workspaces: an odd length of few tokens needs a packed copy */
-    d = lin(24, 95, 128);
-    EXPECT(muon_linear_workspace_bytes(&d, MUON_LINEAR_FORWARD, AT(1), AT(2), &n) == MUON_OK && n >= 24 * 96 * 2);
+    /* workspaces: rows shorter than a chunk need a packed copy */
+    d = lin(24, 7, 128);
+    EXPECT(muon_linear_workspace_bytes(&d, MUON_LINEAR_FORWARD, AT(1), AT(2), &n) == MUON_OK && n >= 24 * 8 * 2);
     EXPECT(muon_linear_forward(&d, AT(1), AT(2), NULL, AT(3), NULL, 0, NULL) == MUON_E_WORKSPACE);
     EXPECT(muon_linear_forward(&d, AT(1), AT(2), NULL, AT(3), ws, n - 1, NULL) == MUON_E_WORKSPACE);
     EXPECT(muon_linear_forward(&d, AT(1), AT(2), NULL, AT(3), ws + 128, n, NULL) == MUON_E_WORKSPACE);
@@ -167,7 +167,10 @@ int main(int argc, char** argv) {
     d = lin(8, 96, 128);
     EXPECT(muon_linear_workspace_bytes(&d, MUON_LINEAR_FORWARD, AT(1), AT(2), &n) == MUON_OK && n == 0);
     EXPECT(muon_linear_forward(&d, AT(1), AT(2), NULL, AT(3), NULL, 0, NULL) == reached);
-    EXPECT(muon_linear_workspace_bytes(&d, MUON_LINEAR_FORWARD, (char*)AT(1) + 2, AT(2), &n) == MUON_OK && n > 0);
+    EXPECT(muon_linear_workspace_bytes(&d, MUON_LINEAR_FORWARD, (char*)AT(1) + 2, AT(2), &n) == MUON_OK && n == 0);
+    d = lin(16384, 1600, 1600);
+    EXPECT(muon_linear_workspace_bytes(&d, MUON_LINEAR_FORWARD, (char*)AT(1) + 2, AT(2), &n) == MUON_OK &&
+           n >= (size_t)16384 * 1600 * 2);
 
     /* no tokens: nothing to do, whatever the pointers; a weight gradient still is */
     d = lin(0, 96, 128);

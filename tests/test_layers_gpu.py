@@ -621,15 +621,17 @@ def test_subnormal_operands_count(rows, dtype, tiny, big):
 
 
 @pytest.mark.parametrize("layout", ["in_out", "out_in"])
-@pytest.mark.parametrize("size", [(65, 9, 15), (64, 65, 8), (100, 129, 71), (700, 1001, 333), (4099, 95, 103)], ids=str)
+@pytest.mark.parametrize("size", [(65, 9, 15), (64, 65, 8), (100, 129, 71), (700, 1001, 333), (4099, 95, 103),
+                                  (1, 1001, 777), (8, 9, 4103), (31, 4105, 67)], ids=str)
 def test_linear_rows_off_borders(size, layout):
-    """Small products of rows that start and end off 16-byte borders: rows of one
-    chunk and a little, an edge one column into a tile, k tails, K pieces."""
+    """Small products and few tokens of rows that start and end off 16-byte
+    borders: rows of one chunk and a little, an edge one column into a tile, k
+    tails, K pieces."""
     test_linear_sizes(size, "fp16", layout)
 
 
 @pytest.mark.parametrize("layout", ["in_out", "out_in"])
-@pytest.mark.parametrize("size", [(70, 73, 67), (700, 1001, 75)], ids=str)
+@pytest.mark.parametrize("size", [(70, 73, 67), (700, 1001, 75), (3, 1001, 75)], ids=str)
 def test_linear_values_beside_the_operands(size, layout):
     """NaN right before, between and behind an operand's rows reaches nothing,
     and the results do not depend on where the rows start."""
