@@ -271,9 +271,10 @@ float muon_momentum_warmup(int64_t step, int64_t warmup_steps, float start, floa
  * weights are then 0, or unchanged when accumulating, and tensors without
  * elements may be NULL). Outputs may not overlap inputs, other outputs or the
  * workspace, except that y / dx may be the very tensor of `add` (same address
- * and stride): the sum then replaces it. (Column ranges side by side in one
- * buffer's rows do not overlap; with unlike strides their extents must not.) Elements between rows (stride beyond
- * the row length) are left as they were. Products and sums are held in fp32
+ * and stride) where no other input lies: the sum then replaces it. (Column
+ * ranges side by side in one buffer's rows do not overlap; with unlike strides
+ * their extents must not.) Elements between rows (stride beyond the row length)
+ * are left as they were. Products and sums are held in fp32
  * and rounded once to each output's type; no atomics are used, so the same
  * call gives the same bits. Errors are muon_status codes, with the detail in
  * muon_op_last_error; validation comes before any HIP call. */

@@ -91,15 +91,17 @@ bool overlap(const Tensor& a, const Tensor& b) {
 
 bool same_tensor(const Tensor& a, const Tensor& b) { return a.p == b.p && (a.ld == b.ld || a.rows <= 1); }
 
-// `out` against every input, other output and the workspace; `may` is the one
-// input it may coincide with.
-muon_status check_disjoint(const Tensor& out, std::initializer_list<Tensor> others, const Tensor* may) {
-    for (const Tensor& o : others) {
-        if (!overlap(out, o)) continue;
-        if (may && o.p == may->p && same_tensor(out, o)) continue;
-        return fail(MUON_E_INVALID_ARG, "an output overlaps another tensor or the workspace");
-    }
+// `out` against inputs, other outputs and the workspace
+muon_status check_disjoint(const Tensor& out, std::initializer_list<Tensor> others) {
+    for (const Tensor& o : others)
+        if (overlap(out, o)) return fail(MUON_E_INVALID_ARG, "an output overlaps another tensor or the workspace");
     return MUON_OK;
+}
+
+// ... and against the tensor added to it, which it may replace. (An operand at
+// that address is check_disjoint's: others still read it while `out` is stored.)
+muon_status check_add(const Tensor& out, const Tensor& add) {
+    return same_tensor(out, add) ? MUON_OK : check_disjoint(out, {add});
 }
 
 muon_status check_align(const void* p, int size, const char* what) {
@@ -364,8 +366,9 @@ muon_status run_layer(const muon_linear* d, int op, const void* a, const void* w
     TRY(plan_product(*d, op, a, w, false, &P));
     TRY(check_workspace(ws, ws_bytes, P.bytes));
     const Tensor S{ws, 1, (int64_t)P.bytes, (int64_t)P.bytes, 1};
-    TRY(check_disjoint(Y, {A, W, R, Z, Bi, S}, &R));
-    if (fwd) TRY(check_disjoint(Z, {A, W, R, Bi, S}, nullptr));
+    TRY(check_disjoint(Y, {A, W, Z, Bi, S}));
+    TRY(check_add(Y, R));
+    if (fwd) TRY(check_disjoint(Z, {A, W, R, Bi, S}));
     for (const Tensor& t : {A, W, R, Z, Bi})
         if (overlap(S, t)) return fail(MUON_E_INVALID_ARG, "the workspace overlaps a tensor");
     TRY(check_device());
@@ -450,8 +453,8 @@ muon_status muon_linear_grad_weight(const muon_linear* d, const void* x, const v
         TRY(plan_product(*d, MUON_LINEAR_GRAD_WEIGHT, x, dy, dbias != nullptr, &P));
         TRY(check_workspace(workspace, ws_bytes, P.bytes));
         const Tensor S{workspace, 1, (int64_t)P.bytes, (int64_t)P.bytes, 1};
-        TRY(check_disjoint(W, {X, Y, Bi, S}, nullptr));
-        TRY(check_disjoint(Bi, {X, Y, S}, nullptr));
+        TRY(check_disjoint(W, {X, Y, Bi, S}));
+        TRY(check_disjoint(Bi, {X, Y, S}));
         if (overlap(S, X) || overlap(S, Y)) return fail(MUON_E_INVALID_ARG, "the workspace overlaps a tensor");
         TRY(check_device());
         char* ws = static_cast<char*>(workspace);
@@ -480,9 +483,9 @@ muon_status muon_layernorm_forward(const muon_layernorm* d, const void* x, const
         const Tensor M{mean, 1, d->rows, d->rows, 4}, S{rstd, 1, d->rows, d->rows, 4};
         for (const Tensor& t : {X, Y}) TRY(check_align(t.p, size, "x or y"));
         for (const Tensor& t : {W, Bi, M, S}) TRY(check_align(t.p, 4, "a float32 tensor"));
-        TRY(check_disjoint(Y, {X, W, Bi, M, S}, nullptr));
-        TRY(check_disjoint(M, {X, W, Bi, S}, nullptr));
-        TRY(check_disjoint(S, {X, W, Bi}, nullptr));
+        TRY(check_disjoint(Y, {X, W, Bi, M, S}));
+        TRY(check_disjoint(M, {X, W, Bi, S}));
+        TRY(check_disjoint(S, {X, W, Bi}));
         TRY(check_device());
         const muon::NormForward n{x,  weight, bias, y, mean, rstd, (int)d->rows, (int)d->cols, (int)X.ld, (int)Y.ld,
                                   d->eps};
@@ -520,10 +523,11 @@ muon_status muon_layernorm_backward(const muon_layernorm* d, const void* dy, con
         const size_t need = sums ? norm_workspace(*d) : 0;
         TRY(check_workspace(workspace, ws_bytes, need));
         const Tensor K{workspace, 1, (int64_t)need, (int64_t)need, 1};
-        TRY(check_disjoint(DX, {DY, X, R, W, DW, DB, M, S, K}, &R));
-        TRY(check_disjoint(DW, {DY, X, R, W, DB, M, S, K}, nullptr));
-        TRY(check_disjoint(DB, {DY, X, R, W, M, S, K}, nullptr));
-        TRY(check_disjoint(K, {DY, X, R, W, M, S}, nullptr));
+        TRY(check_disjoint(DX, {DY, X, W, DW, DB, M, S, K}));
+        TRY(check_add(DX, R));
+        TRY(check_disjoint(DW, {DY, X, R, W, DB, M, S, K}));
+        TRY(check_disjoint(DB, {DY, X, R, W, M, S, K}));
+        TRY(check_disjoint(K, {DY, X, R, W, M, S}));
         if (d->rows == 0 && (!sums || accumulate)) return MUON_OK;
         TRY(check_device());
         const int blocks = muon::norm_backward_blocks(d->rows, d->cols, d->dtype);

@@ -123,7 +123,8 @@ def linear_forward(x, w, bias=None, residual=None, activation="none", weight_lay
                    out=None, preact_out=None):
     """y = act(x w + bias) + residual; with save_preact (or preact_out) also
     z = x w + bias rounded to x's type, for linear_grad_input of the next
-    layer: returns y, or (y, z). `out` may be `residual` itself."""
+    layer: returns y, or (y, z). `out` may be `residual` itself, unless that
+    is x or w too."""
     dtype, device, dev = _first("x", x)
     code = _linear_type("x", dtype)
     act = _choice(ACTIVATIONS, activation, "activation")
@@ -156,7 +157,7 @@ def linear_forward(x, w, bias=None, residual=None, activation="none", weight_lay
 def linear_grad_input(dy, w, preact=None, activation="none", add=None, weight_layout="in_out", out=None):
     """dx = (dy w^T) * act'(preact) + add. With an activation, `preact` is the
     pre-activation that made this layer's x (x = act(preact)), and dx is its
-    gradient. `out` may be `add` itself."""
+    gradient. `out` may be `add` itself, unless that is another input too."""
     dtype, device, dev = _first("dy", dy)
     code = _linear_type("dy", dtype)
     act = _choice(ACTIVATIONS, activation, "activation")
@@ -262,7 +263,8 @@ def layernorm_forward(x, weight=None, bias=None, eps=1e-5, out=None):
 def layernorm_backward(dy, x, mean, rstd, weight=None, add=None, dweight=None, dbias=None, accumulate=False, out=None):
     """(dx, dweight, dbias): the gradient of x, plus `add`, and the float32
     gradients of weight and bias, written to (or with accumulate added to) the
-    tensors given; True allocates one, None leaves it out. `out` may be `add`."""
+    tensors given; True allocates one, None leaves it out. `out` may be `add`
+    itself, unless that is dy or x too."""
     dtype, device, dev = _first("dy", dy)
     code = _norm_type("dy", dtype)
     ld_y = _matrix("dy", dy, dtype, dev)
