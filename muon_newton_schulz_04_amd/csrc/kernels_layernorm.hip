@@ -93,6 +93,20 @@ struct Raw {
             __builtin_memcpy(w, t, sizeof(w));
         }
     }
+    // the elements from n on become v
+    __device__ __forceinline__ void fill(int n, T v) {
+        constexpr int PER = 4 / sizeof(T);
+        uint32_t u = 0;
+        __builtin_memcpy(&u, &v, sizeof(T));
+        if constexpr (PER == 2) u |= u << 16;
+#pragma unroll
+        for (int k = 0; k < 8 / PER; ++k) {
+            if (PER * k >= n)
+                w[k] = u;
+            else if (PER * k + 1 >= n && PER == 2)
+                w[k] = (w[k] & 0xffffu) | (u & 0xffff0000u);
+        }
+    }
     // the compiler takes the words as new: it widens them again rather than
     // keep the float values across
     __device__ __forceinline__ void renew() {
@@ -285,11 +299,20 @@ __global__ __launch_bounds__(WPR == 8 ? 512 : 256) __attribute__((amdgpu_waves_p
         const bool live = row < n.rows;
         if (row + step < n.rows) fetch(nxt, row + step);
         const float rstd = cur.rstd, shift = -cur.mean;
+        // x and dy are 0 past the row's end, which adds nothing to any sum as long
+        // as the xhat there, -mean rstd, is finite. For an all but constant row far
+        // from 0 it is not: the row's first element takes the place of x then. (A
+        // masked second copy of the sums, or loads that always put an element of
+        // the row there, take more registers: 16384 x 1601 bf16 87 us, against 79)
+        if (live && !(fabsf(shift * rstd) < __builtin_inff())) {
+            const T first = static_cast<const T*>(n.x)[row * n.ld_x];
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) cur.x[i].fill(n.cols - (i * LPR + lane) * 8, first);
+        }
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             if (!live) break;
-            // columns past the row's end have dy = 0, so they add nothing to any sum
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float xh = (cur.x[i].get(e) + shift) * rstd, d = cur.dy[i].get(e);
@@ -389,7 +412,7 @@ __global__ __launch_bounds__(256) void k_norm_backward_wide(const NormBackward n
         if (n.weight) load8(n.weight + c, left, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            xh[e] = (xh[e] - mean) * rstd;
+            xh[e] = (e < left ? xh[e] - mean : 0.f) * rstd;  // 0 past the row's end, where g is
             if (n.weight) g[e] *= w[e];
         }
     };

@@ -33,9 +33,9 @@ def _within(got, want, tol, dtype):
 @pytest.mark.parametrize("cols", [1, 5, 8, 520, 1003, 1600, 2049, 8192, 9001])
 @pytest.mark.parametrize("dtype,mean,std", [("bf16", 2.0 ** 100, 1e15), ("bf16", -1e30, 1e12), ("fp32", 1e25, 1e15)])
 def test_backward_where_the_mean_over_the_spread_overflows(cols, dtype, mean, std):
-    """Rows that are constant but for nothing: (0 - mean) rstd would overflow
-    float32, and no element of the row is 0. What lies past a row's end (lanes
-    without a chunk, the rest of a chunk) must not come in as such a 0."""
+    """Constant rows for which (0 - mean) rstd would overflow float32, though no
+    element of the row is 0. What lies past a row's end (lanes without a chunk,
+    the rest of a chunk) must not come in as such a 0."""
     t = T[dtype]
     g = torch.Generator().manual_seed(cols)
     c = torch.tensor(mean).to(t).double()
