@@ -7,7 +7,8 @@
 //    one of up to 8192, in chunks of 8 consecutive elements a lane. Longer rows
 //    are read again from cache (k_norm_*_wide).
 //  * Statistics in fp32, centred: the mean first, then the squares of x - mean
-//    (both from registers), so that a mean far from 0 costs no digits.
+//    (both from registers). Where the mean is far from 0 against the spread, what
+//    its rounding left in x - mean is taken off too (row_is_far).
 //  * Weight gradients: a wave keeps the sums of dy xhat and dy of its own
 //    columns in registers over all the rows it goes through, the workgroup
 //    adds its waves' sums in wave order through LDS and writes one partial
@@ -125,8 +126,28 @@ struct Raw {
     }
 };
 
+// A row's first mean is off by up to about 46 2^-24 of its mean |x| (a lane's
+// strand and the joins), which counts in xhat times mean |x| / spread: at most
+// 190 2^-24 up to a mean of four times the spread, and without bound beyond (a
+// constant row of 1e5 came out as +-1). Rows beyond take one more sum, of x - mean
+// (for every row it cost 16384 x 1600 bf16 19.7 -> 20.5 us). q: the mean square of
+// x - mean. No NaN is far, nor a row whose squares overflow.
+__device__ __forceinline__ bool row_is_far(float mean, float q) { return mean * mean > 16.f * q; }
+// r: the mean of x - mean. xhat = (x - mean) rstd + off.
+struct Stats {
+    float mean, rstd, off;
+};
+__device__ __forceinline__ Stats row_stats(float mean, float r, float q, float eps) {
+    const float var = q - r * r;
+    const float rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);  // a NaN stays one
+    return {mean + r, rstd, -r * rstd};
+}
+
+// 16-bit rows of up to 2048 columns within 64 registers, 8 waves a SIMD (with 66,
+// 16384 x 1601 bf16 25.0 us, against 24.2).
 template <typename T, int NCH, int WPR, bool VEC>
-__global__ __launch_bounds__(256) void k_norm_forward(const NormForward n) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(sizeof(T) == 2 && WPR == 1 ? 8 : 1))) void
+k_norm_forward(const NormForward n) {
     __shared__ float red[16];
     constexpr int LPR = 64 * WPR;  // lanes per row
     const int lane = threadIdx.x % LPR;
@@ -165,7 +186,18 @@ __global__ __launch_bounds__(256) void k_norm_forward(const NormForward n) {
             }
         }
     }
-    const float rstd = 1.f / sqrtf(row_sum<WPR>(q, red + 8) * inv + n.eps);
+    q = row_sum<WPR>(q, red + 8) * inv;
+    float r = 0.f;
+    if (row_is_far(mean, q)) {  // for all lanes of the row alike
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int left = n.cols - (i * LPR + lane) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r += (VEC ? left > 0 : e < left) ? v[i].get(e) - mean : 0.f;
+        }
+        r = row_sum<WPR>(r, red) * inv;
+    }
+    const Stats st = row_stats(mean, r, q, n.eps);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
         const int c = (i * LPR + lane) * 8;
@@ -173,7 +205,11 @@ __global__ __launch_bounds__(256) void k_norm_forward(const NormForward n) {
         if (left <= 0) continue;
         float t[8], u[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = (v[i].get(e) - mean) * rstd;
+        for (int e = 0; e < 8; ++e) t[e] = (v[i].get(e) - mean) * st.rstd;
+        if (st.off != 0.f) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] += st.off;
+        }
         if (n.weight) {
             load8(n.weight + c, left, u);
 #pragma unroll
@@ -187,12 +223,13 @@ __global__ __launch_bounds__(256) void k_norm_forward(const NormForward n) {
         stream8(y + c, VEC ? 8 : left, t);
     }
     if (lane == 0) {
-        n.mean[row] = mean;
-        n.rstd[row] = rstd;
+        n.mean[row] = st.mean;
+        n.rstd[row] = st.rstd;
     }
 }
 
-// Rows of any length, one workgroup each, read three times (twice from cache).
+// Rows of any length, one workgroup each, read three times (twice from cache;
+// four times where row_is_far).
 template <typename T>
 __global__ __launch_bounds__(256) void k_norm_forward_wide(const NormForward n) {
     __shared__ float red[16];
@@ -218,7 +255,18 @@ __global__ __launch_bounds__(256) void k_norm_forward_wide(const NormForward n) 
             q = fmaf(d, d, q);
         }
     }
-    const float rstd = 1.f / sqrtf(row_sum<4>(q, red + 8) * inv + n.eps);
+    q = row_sum<4>(q, red + 8) * inv;
+    float r = 0.f;
+    if (row_is_far(mean, q)) {
+        for (int c = threadIdx.x * 8; c < n.cols; c += 2048) {
+            float v[8];
+            load8(x + c, n.cols - c, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r += c + e < n.cols ? v[e] - mean : 0.f;
+        }
+        r = row_sum<4>(r, red) * inv;
+    }
+    const Stats st = row_stats(mean, r, q, n.eps);
     for (int c = threadIdx.x * 8; c < n.cols; c += 2048) {
         const int left = n.cols - c;
         float v[8], w[8], b[8];
@@ -227,15 +275,15 @@ __global__ __launch_bounds__(256) void k_norm_forward_wide(const NormForward n) 
         if (n.bias) load8(n.bias + c, left, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            v[e] = (v[e] - mean) * rstd;
+            v[e] = fmaf(v[e] - mean, st.rstd, st.off);
             if (n.weight) v[e] *= w[e];
             if (n.bias) v[e] += b[e];
         }
         store8(y + c, left, v);
     }
     if (threadIdx.x == 0) {
-        n.mean[row] = mean;
-        n.rstd[row] = rstd;
+        n.mean[row] = st.mean;
+        n.rstd[row] = st.rstd;
     }
 }
 

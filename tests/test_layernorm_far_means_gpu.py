@@ -54,3 +54,39 @@ def test_backward_where_the_mean_over_the_spread_overflows(cols, dtype, mean, st
     _within(dx, r64 * (gg - s0), tol, t)
     assert (dw == 0).all()
     _within(db, dy.double().sum(0), 3 * U * dy.double().abs().sum(0), torch.float32)
+
+
+@pytest.mark.parametrize("cols", [1, 7, 200, 1003, 1600, 2049, 8192, 9001, 20001])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_forward_of_nearly_constant_rows(cols, dtype):
+    """Rows of one large value, and of a few neighbouring ones: what the float32
+    mean is off by must not come out as a deviation."""
+    t = T[dtype]
+    g = torch.Generator().manual_seed(cols + 1)
+    base = torch.tensor([1e5, 12345.678, -777.77, 3.3e4, 0.1, 1.0, 6e4, -4.1e4]).clamp(max=6e4 if dtype == "fp16" else 1e9)
+    x = base[:, None].expand(-1, cols).to(t).clone()
+    # in the last rows some elements a step or two of the type away
+    step = x[4:, :1].double().abs() * torch.finfo(t).eps
+    x[4:] = (x[4:].double() + step * torch.randint(-2, 3, (4, cols), generator=g).double()).to(t)
+    w, b = torch.randn(cols, generator=g), torch.randn(cols, generator=g)
+    y, mean, rstd = L.layernorm_forward(x.cuda(), w.cuda(), b.cuda(), eps=1e-5)
+    x64 = x.double()
+    m = x64.mean(1, keepdim=True)
+    v = ((x64 - m) ** 2).mean(1, keepdim=True) + 1e-5
+    n = _terms(cols)
+    # the first mean is off by at most D; from there on deviations d count: their
+    # mean, which corrects it, is off by er, and their mean square, less the
+    # square of that correction, by ev
+    D = (n + 2) * U * x64.abs().mean(1, keepdim=True)
+    d = (x64 - m).abs() + D
+    er = (n + 2) * U * d.mean(1, keepdim=True)
+    ev = (n + 4) * U * (d * d).mean(1, keepdim=True) + 2 * D * er + 4 * U * D * D
+    assert (ev < v).all()
+    rel = (1 - ev / v) ** -0.5 - 1 + 4 * U
+    r = v ** -0.5
+    _within(mean, m[:, 0], er[:, 0] + U * m.abs()[:, 0], torch.float32)
+    _within(rstd, r[:, 0], (r * rel)[:, 0], torch.float32)
+    xh = (x64 - m) * r
+    tol = (1 + rel) * r * (er + 3 * U * d) + xh.abs() * rel
+    w64, b64 = w.double(), b.double()
+    _within(y, xh * w64 + b64, tol * w64.abs() + 2 * U * ((xh * w64).abs() + b64.abs()), t)
