@@ -2,10 +2,12 @@
 // forward pass reads x once and writes y once, the backward pass reads dy, x
 // (and the residual's gradient) once and writes dx once.
 //
-//  * A row lives in registers between its sums and its output: one wave holds
-//    a row of up to 2048 columns (4 rows a workgroup), a workgroup of 4 waves
-//    one of up to 8192, in chunks of 8 consecutive elements a lane. Longer rows
-//    are read again from cache (k_norm_*_wide).
+//  * A row lives in registers between its sums and its output, in chunks of 8
+//    consecutive elements a lane: forward one wave holds a row of up to 2048
+//    columns and four one of up to 8192; backward, which also holds dy and the
+//    next row, one wave 1024, two 2048, four 4096 and eight 8192. Longer rows are
+//    read again (k_norm_*_wide): from cache as far as it holds them (bf16, 4096 x
+//    8192 and x 8200: forward 23 and 43 us, backward 62 and 105).
 //  * Statistics in fp32, centred: the mean first, then the squares of x - mean
 //    (both from registers). Where the mean is far from 0 against the spread, what
 //    its rounding left in x - mean is taken off too (row_is_far).
@@ -126,12 +128,13 @@ struct Raw {
     }
 };
 
-// A row's first mean is off by up to about 46 2^-24 of its mean |x| (a lane's
-// strand and the joins), which counts in xhat times mean |x| / spread: at most
-// 190 2^-24 up to a mean of four times the spread, and without bound beyond (a
-// constant row of 1e5 came out as +-1). Rows beyond take one more sum, of x - mean
-// (for every row it cost 16384 x 1600 bf16 19.7 -> 20.5 us). q: the mean square of
-// x - mean. No NaN is far, nor a row whose squares overflow.
+// The first mean of a row of up to 8192 columns is off by up to about 46 2^-24 of
+// its mean |x| (a lane's strand and the joins), which counts in xhat times mean
+// |x| / spread: at most 190 2^-24 up to a mean of four times the spread, and
+// without bound beyond (a constant row of 1e5 came out as +-1). Rows beyond take
+// one more sum, of x - mean (16384 x 1600 bf16 19.6 -> 19.8 us; taken for every
+// row it cost all of them 20.5). q: the mean square of x - mean. No NaN is far,
+// nor a row whose squares overflow.
 __device__ __forceinline__ bool row_is_far(float mean, float q) { return mean * mean > 16.f * q; }
 // r: the mean of x - mean. xhat = (x - mean) rstd + off.
 struct Stats {
@@ -228,8 +231,7 @@ k_norm_forward(const NormForward n) {
     }
 }
 
-// Rows of any length, one workgroup each, read three times (twice from cache;
-// four times where row_is_far).
+// Rows of any length, one workgroup each, read three times (twice from cache).
 template <typename T>
 __global__ __launch_bounds__(256) void k_norm_forward_wide(const NormForward n) {
     __shared__ float red[16];
@@ -245,27 +247,22 @@ __global__ __launch_bounds__(256) void k_norm_forward_wide(const NormForward n) 
         for (int e = 0; e < 8; ++e) s += v[e];
     }
     const float mean = row_sum<4>(s, red) * inv;
-    float q = 0.f;
+    // the reads take the time here, and strands are longer: every row takes the
+    // sum that row_is_far asks for, unless its squares overflow
+    float q = 0.f, r = 0.f;
     for (int c = threadIdx.x * 8; c < n.cols; c += 2048) {
         float v[8];
         load8(x + c, n.cols - c, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float d = c + e < n.cols ? v[e] - mean : 0.f;
+            r += d;
             q = fmaf(d, d, q);
         }
     }
-    q = row_sum<4>(q, red + 8) * inv;
-    float r = 0.f;
-    if (row_is_far(mean, q)) {
-        for (int c = threadIdx.x * 8; c < n.cols; c += 2048) {
-            float v[8];
-            load8(x + c, n.cols - c, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) r += c + e < n.cols ? v[e] - mean : 0.f;
-        }
-        r = row_sum<4>(r, red) * inv;
-    }
+    row_sum2<4>(r, q, red + 8);
+    q *= inv;
+    r = q < __builtin_inff() ? r * inv : 0.f;
     const Stats st = row_stats(mean, r, q, n.eps);
     for (int c = threadIdx.x * 8; c < n.cols; c += 2048) {
         const int left = n.cols - c;
@@ -620,14 +617,15 @@ hipError_t backward_t(const NormBackward& n, hipStream_t st) {
 
 }  // namespace
 
-// Workgroups of the backward pass (each leaves one partial row of column
-// sums), of at least 8 rows: as many as are on the chip at once, since one more
-// takes a whole pass of its own. 16-bit rows of whole chunks leave room for
-// three a CU of 4 waves (16384 x 1600: 512 workgroups 56 us, 768 51, 1024 51),
-// the others' registers for two (512 workgroups against 750 or 768: 6000 x 1003
-// fp32 20.0 us and 27.0, 16384 x 1600 fp32 64.0 and 77.2, 16384 x 1601 bf16 52.1
-// and 66.4); beyond 4096 columns one of 8 waves. For rows longer than registers
-// hold, runs of at least 64 rows.
+// Workgroups of the backward pass (each leaves one partial row of column sums),
+// of at least 8 rows. More of them hide more latency as long as all run at once,
+// but each brings a row to the join. us of both at 16384 rows with at most 512,
+// 768, 1024 and 1536: bf16 x 1600 42.6, 40.5, 47.6, 46.8; x 512 17.2, 17.9, 18.7,
+// 21.2; x 4096 84, 87, 92, 95; bf16 x 1601 79, 102, 85, 92; fp32 x 1600 63, 74,
+// 69, 73; x 512 24.8, 26.9, 28.8, 30.9. So three a CU for 16-bit rows of whole
+// chunks and two for the others, whose registers leave room for no more (rows of
+// up to 512 columns do, without a gain); beyond 4096 columns one of 8 waves. For
+// rows longer than registers hold, runs of at least 64 rows.
 int norm_backward_blocks(int64_t rows, int64_t cols, int dtype) {
     if (rows == 0) return 0;
     const int64_t b = cols <= kBlockCols ? rows / 8 : rows / 64;

@@ -90,3 +90,25 @@ def test_forward_of_nearly_constant_rows(cols, dtype):
     tol = (1 + rel) * r * (er + 3 * U * d) + xh.abs() * rel
     w64, b64 = w.double(), b.double()
     _within(y, xh * w64 + b64, tol * w64.abs() + 2 * U * ((xh * w64).abs() + b64.abs()), t)
+
+
+@pytest.mark.parametrize("cols", [8, 200, 1003, 1600, 4100, 8192, 9001])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_rows_that_are_not_finite_stay_alone(cols, dtype):
+    """A NaN or an infinity makes its row NaN (and an infinite row's mean
+    infinite), forward and backward, and leaves the rows around it as they are."""
+    t = T[dtype]
+    g = torch.Generator().manual_seed(cols)
+    x = (torch.randn(9, cols, generator=g) + 30).to(t)
+    dy = torch.randn(9, cols, generator=g).to(t)
+    ref = L.layernorm_forward(x.cuda())
+    want = L.layernorm_backward(dy.cuda(), x.cuda(), *ref[1:])[0]
+    bad, good = [1, 4, 5, 8], [0, 2, 3, 6, 7]
+    x[1, 0], x[4, cols - 1], x[5, cols // 2], x[8, 3] = float("nan"), float("inf"), -float("inf"), float("nan")
+    y, mean, rstd = L.layernorm_forward(x.cuda())
+    for a, b in zip((y, mean, rstd), ref):
+        assert torch.equal(a[good], b[good])
+    assert y[bad].isnan().all() and rstd[bad].isnan().all()
+    assert mean[4].item() == float("inf") and mean[5].item() == -float("inf") and mean[[1, 8]].isnan().all()
+    dx = L.layernorm_backward(dy.cuda(), x.cuda(), mean, rstd)[0]
+    assert torch.equal(dx[good], want[good]) and dx[bad].isnan().all()
