@@ -250,8 +250,9 @@ __device__ __forceinline__ void widen8(const u32x4& u, float (&v)[8]) {
 }
 
 // The epilogue of 8 consecutive accumulators from row r, column c (and the
-// lane's place from there) on, n of them inside the matrix. bias: their bias values (forward). in, in2: first8's
-// and second8's if n is 8 or more; a chunk at the matrix's edge is read in place.
+// lane's place from there) on, n of them inside the matrix. bias: their bias
+// values (forward). in, in2: first8's and second8's if n is 8 or more; a chunk at
+// the matrix's edge is read in place.
 template <typename T>
 __device__ __forceinline__ void finish8(const Epilogue& E, int64_t r, int64_t c, const LaneAt& l, int n, float (&v)[8],
                                         const float (&bias)[8], const u32x4& in, const u32x4& in2) {

@@ -463,7 +463,7 @@ muon_status muon_linear_grad_weight(const muon_linear* d, const void* x, const v
         E.mode = muon::EPI_GRAD_WEIGHT;
         E.y = dw;
         E.ld_y = (int)W.ld;
-            E.accumulate = accumulate != 0;
+        E.accumulate = accumulate != 0;
         // dy is the second operand of an [in, out] gradient, else the first
         const int sum = !dbias ? 0 : d->weight_layout == MUON_WEIGHT_IN_OUT ? 1 : 2;
         return run_product(P, d->dtype, E, dbias, sum, ws, st);
