@@ -259,8 +259,9 @@ float muon_momentum_warmup(int64_t step, int64_t warmup_steps, float start, floa
 /* ---- layer operators ------------------------------------------------------
  * The pass that makes the gradients muon_step reads, for the weight matrices
  * its table holds: the linear layer (matrix product with bias, activation and
- * residual in its epilogue) with its two gradients, and layer norm with its
- * backward pass. Library plumbing, not defined by the pages.
+ * residual in its epilogue) with its two gradients, on 16-bit and on 8-bit
+ * operands and for the experts of a mixture, and layer norm and root-mean-square
+ * norm with their backward passes. Library plumbing, not defined by the pages.
  *
  * These calls take no handle and keep no state: everything they need is in
  * their arguments, and they only enqueue kernels on `stream` of the current
@@ -381,6 +382,125 @@ muon_status muon_layernorm_workspace_bytes(const muon_layernorm* d, size_t* out_
 muon_status muon_layernorm_backward(const muon_layernorm* d, const void* dy, const void* x, const float* weight,
                                     const float* mean, const float* rstd, const void* add, void* dx, float* dweight,
                                     float* dbias, int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
+
+/* One root-mean-square norm on one batch of rows. dtype (any of the three) is the
+ * type of x, residual, sum, y and of their gradients; weight, its gradient and the
+ * row statistics are float32. rows < 2^24, cols and strides at most 2^21. */
+typedef struct muon_rmsnorm {
+    int64_t rows;
+    int64_t cols;
+    int64_t ld_x;   /* x; backward: what the norm was taken of */
+    int64_t ld_add; /* residual; backward: add */
+    int64_t ld_sum; /* sum */
+    int64_t ld_y;   /* y, dy */
+    int64_t ld_dx;  /* dx */
+    int32_t dtype;
+    float eps;
+} muon_rmsnorm;
+
+/* A matrix [rows, cols] in 8-bit floating point, its values in blocks of 128 columns
+ * that share a float32 scale: an element stands for its 8-bit value times its block's
+ * scale. Rows start 16-byte aligned: data, and ld in bytes (a multiple of 16; 0: the
+ * row length rounded up to one); what writes such a matrix writes zeros from cols to
+ * the next multiple of 16, what reads one may read these bytes, whose values do not
+ * matter. Activations and gradients have a scale for each 128 columns of each row,
+ * scale [ceil(cols / 128), rows] (one block's scales of all rows side by side, as the
+ * products read them); weights for each 128 x 128, scale [ceil(rows / 128),
+ * ceil(cols / 128)]. A scale is the largest magnitude of its block, taken as 2^-110 at
+ * least, divided by the format's largest number; values are rounded to nearest, ties
+ * to even. A block that holds an infinity or a NaN has it for a scale, and so stands
+ * for no finite number anywhere. */
+enum { MUON_EIGHT_E4M3 = 0 /* up to 448 */, MUON_EIGHT_E5M2 = 1 /* up to 57344 */ };
+typedef struct muon_eight {
+    void* data;
+    float* scale;
+    int64_t ld;
+    int32_t format;   /* weights: MUON_EIGHT_E4M3 */
+    int32_t reserved; /* must be 0 */
+} muon_eight;
+
+/* y = r rstd weight per row, rstd = 1 / sqrt(mean(r^2) + eps), of r = x, or with a
+ * residual of r = sum = x + residual rounded to dtype, which is written as the new
+ * residual stream (residual and sum come together; sum may be the very tensor of x
+ * or residual, same address and stride). y: in dtype, or NULL; q: in 8 bits, from
+ * the unrounded values, or NULL (one of the two is given, or both). weight [cols] or
+ * NULL (1); rstd [rows] is written. Squares beyond float32 make y 0. */
+muon_status muon_rmsnorm_forward(const muon_rmsnorm* d, const void* x, const void* residual, const float* weight,
+                                 void* sum, void* y, const muon_eight* q, float* rstd, void* stream);
+
+/* Bytes of device workspace muon_rmsnorm_backward needs when it reduces a weight
+ * gradient. Host-only. */
+muon_status muon_rmsnorm_workspace_bytes(const muon_rmsnorm* d, size_t* out_bytes);
+
+/* dx = the gradient of x (what the norm was taken of) from dy, + add (or NULL);
+ * dweight [cols] (+)= the sums over rows of dy x rstd, or NULL (then no workspace is
+ * needed). rstd as the forward pass wrote it. */
+muon_status muon_rmsnorm_backward(const muon_rmsnorm* d, const void* dy, const void* x, const float* weight,
+                                  const float* rstd, const void* add, void* dx, float* dweight, int32_t accumulate,
+                                  void* workspace, size_t ws_bytes, void* stream);
+
+/* x [rows, cols] (row stride ld_x, any of the three types) to 8 bits, activations' or
+ * gradients' blocks. */
+muon_status muon_quantize(int64_t rows, int64_t cols, int64_t ld_x, int32_t dtype, const void* x, const muon_eight* q,
+                          void* stream);
+
+/* A weight [rows, cols] (any of the three types; muon_step's params as they are) to
+ * 8 bits, weights' blocks: q in its own order, q_t the other one [cols, rows], with
+ * the same values and scales; either NULL. */
+muon_status muon_quantize_weight(int64_t rows, int64_t cols, int64_t ld_w, int32_t dtype, const void* w,
+                                 const muon_eight* q, const muon_eight* q_t, void* stream);
+
+/* The linear layer on 8-bit operands: Y = act(X W^T + bias) + add with X [tokens, in]
+ * and W [out, in] (d->weight_layout MUON_WEIGHT_OUT_IN), and dX = (dY W^T) * act'(z) +
+ * add with dY [tokens, out] and W [in, out] (MUON_WEIGHT_IN_OUT): both operands lie
+ * with the sum's index contiguous, so a layer that is trained keeps its weight in both
+ * orders (muon_quantize_weight writes them). d->dtype is the type of the output, add
+ * and z; of d's strides only the output's is looked at (ld_y; ld_x), the operands'
+ * must be 0, as their own are in the muon_eight. Each block's products are summed in
+ * fp32 and multiplied by the product of its two scales. The weight's gradient is
+ * muon_linear_grad_weight's, of the 16-bit tensors. */
+muon_status muon_linear_scaled_forward(const muon_linear* d, const muon_eight* x, const muon_eight* w,
+                                       const muon_epilogue* e, void* y, void* stream);
+muon_status muon_linear_scaled_grad_input(const muon_linear* d, const muon_eight* dy, const muon_eight* w,
+                                          const muon_epilogue* e, void* dx, void* stream);
+
+/* The linear layers of a mixture of experts on rows that lie grouped by expert:
+ * expert e has rows offsets[e] .. offsets[e + 1] - 1 of X, Y and their gradients, and
+ * weight e of W, `stride_w` elements after the one before (0: back to back, as `count`
+ * matrices of one table entry are). bias and dbias are [experts, out_features].
+ * offsets [experts + 1] are int32 on the device, ascending, in [0, rows]; they are read
+ * there, so that a captured call serves later offsets. Others are taken as the nearest
+ * that are in range and ascending: rows are then of unspecified values, and nothing
+ * outside the tensors is read or written. Rows before the first and behind the last
+ * expert's are not read and left as they are. rows < 2^24, experts at most 2^16,
+ * features from 8 to 2^21. */
+typedef struct muon_grouped {
+    int64_t rows;
+    int64_t experts;
+    int64_t in_features;
+    int64_t out_features;
+    int64_t ld_x; /* X, dX [rows, in_features] */
+    int64_t ld_w; /* each expert's W, dW in weight_layout */
+    int64_t ld_y; /* Y, dY [rows, out_features] */
+    int64_t stride_w;
+    int32_t dtype; /* bf16 or fp16, as muon_linear's */
+    int32_t weight_layout;
+} muon_grouped;
+
+/* Y = act(X W_e + bias_e) + add per expert. */
+muon_status muon_grouped_linear_forward(const muon_grouped* d, const void* x, const void* w, const int32_t* offsets,
+                                        const muon_epilogue* e, void* y, void* stream);
+
+/* dX = (dY W_e^T) * act'(z) + add per expert. */
+muon_status muon_grouped_linear_grad_input(const muon_grouped* d, const void* dy, const void* w,
+                                           const int32_t* offsets, const muon_epilogue* e, void* dx, void* stream);
+
+/* dW_e (+)= the product of X and dY over the expert's rows, float32, and dbias_e (+)=
+ * the sum of dY over them, or NULL: zeros (or unchanged, when accumulating) for an
+ * expert without rows. */
+muon_status muon_grouped_linear_grad_weight(const muon_grouped* d, const void* x, const void* dy,
+                                            const int32_t* offsets, float* dw, float* dbias, int32_t accumulate,
+                                            void* stream);
 
 /* Detail of the last failed layer operator call on this thread ("" if none). */
 const char* muon_op_last_error(void);

@@ -65,6 +65,8 @@ MUON_ACT_RELU2 = 2
 MUON_ACT_GELU = 3
 MUON_ACT_GELU_TANH = 4
 MUON_ACT_SILU = 5
+MUON_EIGHT_E4M3 = 0
+MUON_EIGHT_E5M2 = 1
 MUON_LINEAR_FORWARD = 0
 MUON_LINEAR_GRAD_INPUT = 1
 MUON_LINEAR_GRAD_WEIGHT = 2
@@ -164,6 +166,45 @@ class muon_layernorm(ctypes.Structure):
     ]
 
 
+class muon_rmsnorm(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("ld_add", ctypes.c_int64),
+        ("ld_sum", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64),
+        ("ld_dx", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class muon_eight(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("ld", ctypes.c_int64),
+        ("format", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class muon_grouped(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("experts", ctypes.c_int64),
+        ("in_features", ctypes.c_int64),
+        ("out_features", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("ld_w", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64),
+        ("stride_w", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("weight_layout", ctypes.c_int32),
+    ]
+
+
 _P = ctypes.c_void_p
 _SIGS = {
     "muon_hparams_default": (None, [ctypes.POINTER(muon_hparams)]),
@@ -198,6 +239,26 @@ _SIGS = {
                                                       ctypes.POINTER(ctypes.c_size_t)]),
     "muon_layernorm_backward": (ctypes.c_int, [ctypes.POINTER(muon_layernorm), _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                                ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "muon_rmsnorm_forward": (ctypes.c_int, [ctypes.POINTER(muon_rmsnorm), _P, _P, _P, _P, _P,
+                                            ctypes.POINTER(muon_eight), _P, _P]),
+    "muon_rmsnorm_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(muon_rmsnorm), ctypes.POINTER(ctypes.c_size_t)]),
+    "muon_rmsnorm_backward": (ctypes.c_int, [ctypes.POINTER(muon_rmsnorm), _P, _P, _P, _P, _P, _P, _P, ctypes.c_int32,
+                                             _P, ctypes.c_size_t, _P]),
+    "muon_quantize": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P,
+                                     ctypes.POINTER(muon_eight), _P]),
+    "muon_quantize_weight": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P,
+                                            ctypes.POINTER(muon_eight), ctypes.POINTER(muon_eight), _P]),
+    "muon_linear_scaled_forward": (ctypes.c_int, [ctypes.POINTER(muon_linear), ctypes.POINTER(muon_eight),
+                                                  ctypes.POINTER(muon_eight), ctypes.POINTER(muon_epilogue), _P, _P]),
+    "muon_linear_scaled_grad_input": (ctypes.c_int, [ctypes.POINTER(muon_linear), ctypes.POINTER(muon_eight),
+                                                     ctypes.POINTER(muon_eight), ctypes.POINTER(muon_epilogue), _P,
+                                                     _P]),
+    "muon_grouped_linear_forward": (ctypes.c_int, [ctypes.POINTER(muon_grouped), _P, _P, _P,
+                                                   ctypes.POINTER(muon_epilogue), _P, _P]),
+    "muon_grouped_linear_grad_input": (ctypes.c_int, [ctypes.POINTER(muon_grouped), _P, _P, _P,
+                                                      ctypes.POINTER(muon_epilogue), _P, _P]),
+    "muon_grouped_linear_grad_weight": (ctypes.c_int, [ctypes.POINTER(muon_grouped), _P, _P, _P, _P, _P,
+                                                       ctypes.c_int32, _P]),
     "muon_op_last_error": (ctypes.c_char_p, []),
     "muon_lr_wsd": (ctypes.c_float, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
     "muon_lr_cooldown_floor": (ctypes.c_float, [ctypes.c_int64, ctypes.c_int64, ctypes.c_float, ctypes.c_float]),
@@ -381,6 +442,60 @@ def muon_layernorm_backward(d: muon_layernorm, dy_ptr: int, x_ptr: int, weight_p
                             workspace_ptr: int, ws_bytes: int, stream_ptr: int) -> int:
     return load().muon_layernorm_backward(d, dy_ptr, x_ptr, weight_ptr, mean_ptr, rstd_ptr, add_ptr, dx_ptr,
                                           dweight_ptr, dbias_ptr, accumulate, workspace_ptr, ws_bytes, stream_ptr)
+
+
+def muon_rmsnorm_forward(d: muon_rmsnorm, x_ptr: int, residual_ptr: int, weight_ptr: int, sum_ptr: int, y_ptr: int,
+                         q: Optional[muon_eight], rstd_ptr: int, stream_ptr: int) -> int:
+    return load().muon_rmsnorm_forward(d, x_ptr, residual_ptr, weight_ptr, sum_ptr, y_ptr, q, rstd_ptr, stream_ptr)
+
+
+def muon_rmsnorm_workspace_bytes(d: muon_rmsnorm) -> tuple:
+    out = ctypes.c_size_t(0)
+    s = load().muon_rmsnorm_workspace_bytes(d, out)
+    return s, out.value
+
+
+def muon_rmsnorm_backward(d: muon_rmsnorm, dy_ptr: int, x_ptr: int, weight_ptr: int, rstd_ptr: int, add_ptr: int,
+                          dx_ptr: int, dweight_ptr: int, accumulate: int, workspace_ptr: int, ws_bytes: int,
+                          stream_ptr: int) -> int:
+    return load().muon_rmsnorm_backward(d, dy_ptr, x_ptr, weight_ptr, rstd_ptr, add_ptr, dx_ptr, dweight_ptr,
+                                        accumulate, workspace_ptr, ws_bytes, stream_ptr)
+
+
+def muon_quantize(rows: int, cols: int, ld_x: int, dtype: int, x_ptr: int, q: Optional[muon_eight],
+                  stream_ptr: int) -> int:
+    return load().muon_quantize(rows, cols, ld_x, dtype, x_ptr, q, stream_ptr)
+
+
+def muon_quantize_weight(rows: int, cols: int, ld_w: int, dtype: int, w_ptr: int, q: Optional[muon_eight],
+                         q_t: Optional[muon_eight], stream_ptr: int) -> int:
+    return load().muon_quantize_weight(rows, cols, ld_w, dtype, w_ptr, q, q_t, stream_ptr)
+
+
+def muon_linear_scaled_forward(d: muon_linear, x: muon_eight, w: muon_eight, e: Optional[muon_epilogue], y_ptr: int,
+                               stream_ptr: int) -> int:
+    return load().muon_linear_scaled_forward(d, x, w, e, y_ptr, stream_ptr)
+
+
+def muon_linear_scaled_grad_input(d: muon_linear, dy: muon_eight, w: muon_eight, e: Optional[muon_epilogue],
+                                  dx_ptr: int, stream_ptr: int) -> int:
+    return load().muon_linear_scaled_grad_input(d, dy, w, e, dx_ptr, stream_ptr)
+
+
+def muon_grouped_linear_forward(d: muon_grouped, x_ptr: int, w_ptr: int, offsets_ptr: int, e: Optional[muon_epilogue],
+                                y_ptr: int, stream_ptr: int) -> int:
+    return load().muon_grouped_linear_forward(d, x_ptr, w_ptr, offsets_ptr, e, y_ptr, stream_ptr)
+
+
+def muon_grouped_linear_grad_input(d: muon_grouped, dy_ptr: int, w_ptr: int, offsets_ptr: int,
+                                   e: Optional[muon_epilogue], dx_ptr: int, stream_ptr: int) -> int:
+    return load().muon_grouped_linear_grad_input(d, dy_ptr, w_ptr, offsets_ptr, e, dx_ptr, stream_ptr)
+
+
+def muon_grouped_linear_grad_weight(d: muon_grouped, x_ptr: int, dy_ptr: int, offsets_ptr: int, dw_ptr: int,
+                                    dbias_ptr: int, accumulate: int, stream_ptr: int) -> int:
+    return load().muon_grouped_linear_grad_weight(d, x_ptr, dy_ptr, offsets_ptr, dw_ptr, dbias_ptr, accumulate,
+                                                  stream_ptr)
 
 
 def muon_op_last_error() -> str:

@@ -24,7 +24,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cpp", "plan.cpp", "schedule.cpp", "kernels_elementwise.hip", "kernels_ns.hip",
            "kernels_ns_mfma.hip", "kernels_ns_small.hip", "kernels_ns_panel.hip", "static_scratch.hip",
-           "layers.cpp", "kernels_linear.hip", "kernels_layernorm.hip"]
+           "layers.cpp", "layers_scaled.cpp", "layers_grouped.cpp", "kernels_linear.hip", "kernels_layernorm.hip",
+           "kernels_rmsnorm.hip", "kernels_quantize.hip", "kernels_scaled.hip", "kernels_grouped.hip"]
 ARCH = "gfx950"
 
 

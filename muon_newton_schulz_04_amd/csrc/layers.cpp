@@ -2,23 +2,17 @@
 // packing and workspace layout, the choice of tile and K split, and the
 // launches on the caller's stream.
 
-#include <hip/hip_runtime.h>
+#include "layer_checks.hpp"
 
-#include <atomic>
-#include <cmath>
-#include <cstring>
-#include <exception>
-#include <new>
-#include <string>
-
-#include "../../include/libmuon.h"
-#include "layers.hpp"
+using namespace muon::checks;
 
 namespace {
 
 thread_local std::string g_error;
 
-muon_status fail(muon_status s, const char* msg) noexcept {
+}  // namespace
+
+muon_status muon::checks::fail(muon_status s, const char* msg) noexcept {
     try {
         g_error = msg;
     } catch (...) {
@@ -26,112 +20,7 @@ muon_status fail(muon_status s, const char* msg) noexcept {
     return s;
 }
 
-// No exception crosses the ABI.
-template <typename F>
-muon_status guarded(F&& body) noexcept {
-    try {
-        return body();
-    } catch (const std::bad_alloc&) {
-        return fail(MUON_E_HOST, "out of host memory");
-    } catch (const std::exception& ex) {
-        return fail(MUON_E_HOST, ex.what());
-    } catch (...) {
-        return fail(MUON_E_HOST, "unknown exception");
-    }
-}
-
-muon_status hip_status(hipError_t e, const char* where) {
-    if (e == hipSuccess) return MUON_OK;
-    return fail(MUON_E_HIP, (std::string(where) + ": " + hipGetErrorString(e)).c_str());
-}
-
-// The current device must be a gfx950; asked once per device.
-muon_status check_device() {
-    constexpr int kMax = 64;
-    static std::atomic<int> known[kMax];
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) {
-        (void)hipGetLastError();
-        return fail(MUON_E_NO_DEVICE, "no HIP device");
-    }
-    if (dev < kMax && known[dev].load(std::memory_order_relaxed) == 1) return MUON_OK;
-    hipDeviceProp_t prop;
-    hipError_t e = hipGetDeviceProperties(&prop, dev);
-    if (e != hipSuccess) return hip_status(e, "hipGetDeviceProperties");
-    if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
-        return fail(MUON_E_NO_DEVICE, (std::string("device is ") + prop.gcnArchName + ", need gfx950").c_str());
-    if (dev < kMax) known[dev].store(1, std::memory_order_relaxed);
-    return MUON_OK;
-}
-
-constexpr int64_t kMaxRows = (int64_t)1 << 24;
-constexpr int64_t kMaxCols = (int64_t)1 << 21;
-
-// A [rows, cols] tensor with a row stride, and the bytes from its first to
-// its last element.
-struct Tensor {
-    const void* p;
-    int64_t rows, cols, ld;
-    int size;
-    int64_t bytes() const { return rows == 0 ? 0 : ((rows - 1) * ld + cols) * size; }
-};
-
-bool overlap(const Tensor& a, const Tensor& b) {
-    const int64_t na = a.bytes(), nb = b.bytes();
-    if (!a.p || !b.p || na == 0 || nb == 0) return false;
-    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-    if (x >= y + (uintptr_t)nb || y >= x + (uintptr_t)na) return false;
-    // column ranges of one buffer's rows may lie side by side
-    const uintptr_t pitch = (uintptr_t)(a.ld * a.size), ca = (uintptr_t)(a.cols * a.size),
-                    cb = (uintptr_t)(b.cols * b.size);
-    if (pitch != (uintptr_t)(b.ld * b.size)) return true;
-    const uintptr_t d = x >= y ? (x - y) % pitch : (pitch - (y - x) % pitch) % pitch;  // a's column in b's rows
-    return !(d >= cb && d + ca <= pitch);
-}
-
-bool same_tensor(const Tensor& a, const Tensor& b) { return a.p == b.p && (a.ld == b.ld || a.rows <= 1); }
-
-// `out` against inputs, other outputs and the workspace
-muon_status check_disjoint(const Tensor& out, std::initializer_list<Tensor> others) {
-    for (const Tensor& o : others)
-        if (overlap(out, o)) return fail(MUON_E_INVALID_ARG, "an output overlaps another tensor or the workspace");
-    return MUON_OK;
-}
-
-// ... and against the tensor added to it, which it may replace. (An operand at
-// that address is check_disjoint's: others still read it while `out` is stored.)
-muon_status check_add(const Tensor& out, const Tensor& add) {
-    return same_tensor(out, add) ? MUON_OK : check_disjoint(out, {add});
-}
-
-muon_status check_align(const void* p, int size, const char* what) {
-    if ((uintptr_t)p % (uintptr_t)size == 0) return MUON_OK;
-    return fail(MUON_E_LAYOUT, (std::string(what) + " is not aligned to its element size").c_str());
-}
-
-muon_status check_ld(int64_t ld, int64_t cols, const char* what) {
-    if (ld == 0 || (ld >= cols && ld <= kMaxCols)) return MUON_OK;
-    return fail(MUON_E_LAYOUT, (std::string(what) + " must be 0 or from the row length to 2^21").c_str());
-}
-
-muon_status check_workspace(const void* ws, size_t have, size_t need) {
-    if (need == 0) return MUON_OK;
-    if (!ws) return fail(MUON_E_WORKSPACE, "null workspace");
-    if ((uintptr_t)ws % 256 != 0) return fail(MUON_E_WORKSPACE, "workspace not 256-byte aligned");
-    if (have < need)
-        return fail(MUON_E_WORKSPACE, ("workspace too small: need " + std::to_string(need) + " bytes").c_str());
-    return MUON_OK;
-}
-
-#define TRY(expr)                          \
-    do {                                   \
-        const muon_status s_ = (expr);     \
-        if (s_ != MUON_OK) return s_;      \
-    } while (0)
-
-bool aligned16(const void* p, int64_t ld, int size) { return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0; }
-int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+namespace {
 
 muon_status check_linear(const muon_linear* d) {
     if (!d) return fail(MUON_E_INVALID_ARG, "null descriptor");
@@ -317,33 +206,6 @@ muon_status run_product(Product& P, int dtype, muon::Epilogue& E, float* sums, i
     return MUON_OK;
 }
 
-muon_status check_epilogue(const muon_linear& d, int op, const muon_epilogue& e) {
-    const bool fwd = op == MUON_LINEAR_FORWARD;
-    const int64_t cols = fwd ? d.out_features : d.in_features;
-    if (e.activation < MUON_ACT_NONE || e.activation > MUON_ACT_SILU)
-        return fail(MUON_E_INVALID_ARG, "epilogue: unknown activation");
-    if (e.reserved != 0) return fail(MUON_E_INVALID_ARG, "epilogue: reserved must be 0");
-    if (!fwd && e.bias) return fail(MUON_E_INVALID_ARG, "grad input: takes no bias");
-    TRY(check_ld(e.ld_add, cols, "ld_add"));
-    return check_ld(e.ld_z, cols, "ld_z");
-}
-
-// What a product's epilogue reads and writes (e NULL: only the output).
-struct Outputs {
-    Tensor y, add, z;
-};
-
-Outputs outputs_of(const muon_linear& d, int op, const muon_epilogue* e, const void* y) {
-    const bool fwd = op == MUON_LINEAR_FORWARD;
-    const int64_t cols = fwd ? d.out_features : d.in_features;
-    Outputs o{fwd ? tensor_y(d, y) : tensor_x(d, y), {}, {}};
-    if (!e) return o;
-    o.add = {e->add, d.tokens, cols, e->ld_add ? e->ld_add : cols, 2};
-    // the way back reads z only for an activation
-    if (fwd || e->activation != MUON_ACT_NONE) o.z = {e->z, d.tokens, cols, e->ld_z ? e->ld_z : cols, 2};
-    return o;
-}
-
 // forward and grad input
 muon_status run_layer(const muon_linear* d, int op, const void* a, const void* w, const muon_epilogue* e, void* y,
                       void* ws, size_t ws_bytes, void* stream) {
@@ -351,13 +213,14 @@ muon_status run_layer(const muon_linear* d, int op, const void* a, const void* w
     const bool fwd = op == MUON_LINEAR_FORWARD;
     muon_epilogue none{};
     if (!e) e = &none;
-    TRY(check_epilogue(*d, op, *e));
+    const int64_t cols = fwd ? d->out_features : d->in_features;
+    TRY(check_epilogue(fwd, cols, *e));
     if (d->tokens == 0) return MUON_OK;
     if (!a || !w || !y) return fail(MUON_E_INVALID_ARG, "null tensor");
     if (!fwd && e->activation != MUON_ACT_NONE && !e->z)
         return fail(MUON_E_INVALID_ARG, "grad input: an activation needs its pre-activation z");
     const Tensor A = fwd ? tensor_x(*d, a) : tensor_y(*d, a), W = tensor_w(*d, w, 2);
-    const Outputs o = outputs_of(*d, op, e, y);
+    const Outputs o = outputs_of(fwd, d->tokens, cols, fwd ? d->ld_y : d->ld_x, *e, y);
     const Tensor &Y = o.y, &R = o.add, &Z = o.z;
     const Tensor Bi{e->bias, 1, d->out_features, d->out_features, 4};
     for (const Tensor& t : {A, W, Y, R, Z}) TRY(check_align(t.p, 2, "a 16-bit tensor"));
@@ -372,16 +235,7 @@ muon_status run_layer(const muon_linear* d, int op, const void* a, const void* w
     for (const Tensor& t : {A, W, R, Z, Bi})
         if (overlap(S, t)) return fail(MUON_E_INVALID_ARG, "the workspace overlaps a tensor");
     TRY(check_device());
-    muon::Epilogue E{};
-    E.mode = fwd ? muon::EPI_FORWARD : muon::EPI_GRAD_INPUT;
-    E.act = (int8_t)e->activation;
-    E.bias = e->bias;
-    E.add = e->add;
-    E.z = e->z && Z.p ? e->z : nullptr;
-    E.y = y;
-    E.ld_add = (int)R.ld;
-    E.ld_z = (int)Z.ld;
-    E.ld_y = (int)Y.ld;
+    muon::Epilogue E = epilogue_args(fwd, *e, o);
     return run_product(P, d->dtype, E, nullptr, 0, static_cast<char*>(ws), static_cast<hipStream_t>(stream));
 }
 
@@ -399,8 +253,6 @@ muon_status check_norm(const muon_layernorm* d) {
     TRY(check_ld(d->ld_add, d->cols, "ld_add"));
     return MUON_OK;
 }
-
-int64_t stride_of(int64_t ld, int64_t cols) { return ld ? ld : cols; }
 
 size_t norm_workspace(const muon_layernorm& d) {
     return up256((size_t)muon::norm_backward_blocks(d.rows, d.cols, d.dtype) * 2 * (size_t)d.cols * 4);

@@ -110,6 +110,99 @@ struct NormSums {
     int32_t cols, blocks, accumulate;
 };
 
+// A linear layer of each of `experts` over rows grouped by expert. Forward and input
+// gradient: A [rows, K] k-contiguous, B an expert's weight; weight gradient: A
+// [rows, M], B [rows, N], the sum over the expert's rows.
+struct GroupedArgs {
+    const void* a;
+    const void* b;
+    const int32_t* offsets;  // [experts + 1]
+    int64_t stride_w;        // elements from one expert's weight (or its gradient) to the next
+    float* sums;             // bias gradients [experts][], or null
+    int32_t ld_a, ld_b;
+    int32_t rows, experts, M, N, K;
+    int32_t tiles_m, tiles_n;  // of an expert's output (tiles_m: weight gradient)
+    Epilogue epi;
+};
+// tile: rows of a tile (256 x 128, 128 x 128, 64 x 64), or of a block of the kernel for
+// few rows (16, 32)
+hipError_t launch_grouped(const GroupedArgs& p, int tile, bool raw, bool b_kc, int dtype, unsigned grid,
+                          hipStream_t st);
+hipError_t launch_grouped_weight(const GroupedArgs& p, int tile, bool raw, int dtype, int sum, unsigned grid,
+                                 hipStream_t st);
+
+// 8-bit floating point with a float32 scale for each block of 128: what a format's
+// kernels are called by.
+enum { EIGHT_NONE = -1, EIGHT_E4M3 = 0, EIGHT_E5M2 = 1 };
+constexpr int kScaleBlock = 128;
+
+struct RmsForward {
+    const void* x;
+    const void* add;  // residual, or null: then no sum
+    const float* weight;
+    void* sum;
+    void* y;       // or null
+    void* q;       // 8-bit output, or null
+    float* scale;  // [blocks][rows]
+    float* rstd;
+    int32_t rows, cols, ld_x, ld_add, ld_sum, ld_y, ld_q;
+    float eps;
+};
+
+struct RmsBackward {
+    const void* dy;
+    const void* x;
+    const float* weight;
+    const float* rstd;
+    const void* add;
+    void* dx;
+    float* part;  // [blocks][cols], or null: no column sums
+    int32_t rows, cols, ld_x, ld_y, ld_dx, ld_add, blocks;
+};
+
+// what the column sums of RmsBackward's workgroups become
+struct RmsSums {
+    const float* part;
+    float* dweight;
+    int32_t cols, blocks, accumulate;
+};
+
+int rms_backward_blocks(int64_t rows, int64_t cols, int dtype);
+hipError_t launch_rms_forward(const RmsForward& n, int dtype, int format, hipStream_t st);
+hipError_t launch_rms_backward(const RmsBackward& n, int dtype, hipStream_t st);
+hipError_t launch_rms_sums(const RmsSums& n, hipStream_t st);
+
+// x [rows, cols] to 8 bits with a scale for each 128 columns of a row
+struct Quantize {
+    const void* x;
+    void* q;
+    float* scale;  // [blocks][rows]
+    int32_t rows, cols, ld_x, ld_q;
+};
+// w [rows, cols] to E4M3 with a scale for each 128 x 128 of it, in its own order
+// and the other one (either null)
+struct QuantizeWeight {
+    const void* w;
+    void* q;
+    float* scale;  // [row blocks][column blocks]
+    void* qt;
+    float* scale_t;
+    int32_t rows, cols, ld_w, ld_q, ld_qt;
+};
+hipError_t launch_quantize(const Quantize& a, int dtype, int format, hipStream_t st);
+hipError_t launch_quantize_weight(const QuantizeWeight& a, int dtype, hipStream_t st);
+
+// C[M, N] over 8-bit operands, k-contiguous (a: X [M, K], b: W [N, K], strides and K
+// in bytes, rows 16-byte aligned); K goes by in `slices` blocks of 128
+struct ScaledArgs {
+    GemmArgs g;
+    const float* scale_x;  // [slices][M]
+    const float* scale_w;  // [N's blocks][slices]
+};
+// tile: rows of a tile (256 x 128, 128 x 128, 64 x 64), or 0 for up to kSkinnyRows rows
+// against columns in groups of 16
+hipError_t launch_scaled(const ScaledArgs& p, int tile, int dtype, int format, hipStream_t st);
+
 int norm_backward_blocks(int64_t rows, int64_t cols, int dtype);
 hipError_t launch_norm_forward(const NormForward& n, int dtype, hipStream_t st);
 hipError_t launch_norm_backward(const NormBackward& n, int dtype, hipStream_t st);

@@ -1,7 +1,9 @@
 """The layer operators of libmuon on torch tensors: the linear layer (matrix
 product with bias, activation and residual in its epilogue) with its two
-gradients, and layer norm with its backward pass. They make the gradients
-that a Muon step reads: `dw` may be a view of the flat gradient buffer.
+gradients, on 16-bit tensors, on 8-bit ones and for the experts of a mixture,
+and layer norm and root-mean-square norm with their backward passes. They make
+the gradients that a Muon step reads: `dw` may be a view of the flat gradient
+buffer.
 
 Each function checks its tensors, allocates the outputs that are not given and
 the workspace through torch's caching allocator, and makes one C call
@@ -14,9 +16,16 @@ Matrices are [rows, features] with any row stride (the last dimension
 contiguous); leading dimensions of x, dy and the like are flattened only by
 the caller. Weights are [in, out] ("in_out", as the body's c_fc [d, 4d]) or
 [out, in] ("out_in").
+
+8-bit matrices are `Fp8` pairs (or any pair) of a torch.float8_e4m3fn or
+float8_e5m2 matrix whose rows start 16-byte aligned and float32 scales, one for
+each block of 128: [ceil(cols / 128), rows] for activations and gradients,
+[ceil(rows / 128), ceil(cols / 128)] for weights.
 """
 
 from __future__ import annotations
+
+from typing import NamedTuple
 
 import torch
 
@@ -24,6 +33,7 @@ from . import binding as B
 
 _TYPES = {torch.bfloat16: B.MUON_TYPE_BF16, torch.float16: B.MUON_TYPE_FP16, torch.float32: B.MUON_TYPE_FP32}
 _LAYOUTS = {"in_out": B.MUON_WEIGHT_IN_OUT, "out_in": B.MUON_WEIGHT_OUT_IN}
+_EIGHT = {torch.float8_e4m3fn: B.MUON_EIGHT_E4M3, torch.float8_e5m2: B.MUON_EIGHT_E5M2}
 ACTIVATIONS = {"none": B.MUON_ACT_NONE, "relu": B.MUON_ACT_RELU, "relu2": B.MUON_ACT_RELU2, "gelu": B.MUON_ACT_GELU,
                "gelu_tanh": B.MUON_ACT_GELU_TANH, "silu": B.MUON_ACT_SILU}
 
@@ -298,3 +308,375 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, add=None, dweight=None, d
     if s:
         _check(s, "layernorm_backward")
     return out, dweight, dbias
+
+
+class Fp8(NamedTuple):
+    """An 8-bit matrix and its scales."""
+    data: torch.Tensor
+    scale: torch.Tensor
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def _new_eight(rows, cols, dtype, scale_shape, device):
+    """A new 8-bit matrix (rows of whole 16 bytes) and its descriptor."""
+    ld = (cols + 15) // 16 * 16
+    data = torch.empty((rows, ld), dtype=dtype, device=device)
+    scale = torch.empty(scale_shape, dtype=torch.float32, device=device)
+    q = B.muon_eight(data.data_ptr(), scale.data_ptr(), ld, _EIGHT[dtype], 0)
+    return Fp8(data if ld == cols else data[:, :cols], scale), q
+
+
+def _eight(name, pair, dev, weight):
+    """(descriptor, rows, cols) of an 8-bit matrix argument."""
+    try:
+        t, scale = pair
+    except (TypeError, ValueError):
+        raise ValueError(f"{name}: expected a pair of an 8-bit matrix and its scales") from None
+    if t.dtype not in _EIGHT or weight and t.dtype is not torch.float8_e4m3fn:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.float8_e4m3fn" +
+                         ("" if weight else " or torch.float8_e5m2"))
+    ld = _matrix(name, t, t.dtype, dev)
+    rows, cols = t.shape
+    if rows <= 1:
+        ld = (cols + 15) // 16 * 16
+    if ld % 16 or t.data_ptr() % 16:
+        raise ValueError(f"{name}: rows must start 16-byte aligned (stride {ld})")
+    shape = (_blocks(rows), _blocks(cols)) if weight else (_blocks(cols), rows)
+    if scale.dtype is not torch.float32 or scale.get_device() != dev:
+        _same(f"{name}'s scales", scale, torch.float32, dev)
+    if scale.shape != shape or not scale.is_contiguous():
+        raise ValueError(f"{name}: scales {tuple(scale.shape)}, expected {list(shape)}, contiguous")
+    return B.muon_eight(t.data_ptr(), scale.data_ptr(), ld, _EIGHT[t.dtype], 0), rows, cols
+
+
+def _eight_type(dtype):
+    if dtype not in _EIGHT:
+        raise ValueError(f"8-bit type {dtype}, expected torch.float8_e4m3fn or torch.float8_e5m2")
+    return dtype
+
+
+def rmsnorm_forward(x, weight=None, residual=None, eps=1e-5, quantize=None, out=None, residual_out=None):
+    """(y, rstd) of root-mean-square norm over the rows of x (bf16, fp16 or fp32),
+    or with a residual (y, rstd, r) of r = x + residual, rounded to x's type: the
+    new residual stream, in `residual_out` if given (x or residual itself, for
+    one). weight and rstd are float32. With quantize (torch.float8_e4m3fn or
+    float8_e5m2) y is an Fp8 of the unrounded values, and x's type's y is written
+    too if `out` is given."""
+    dtype, device, dev = _first("x", x)
+    code = _norm_type("x", dtype)
+    ld_x = _matrix("x", x, dtype, dev)
+    rows, cols = x.shape
+    ld_a = ld_r = pa = pr = ld_y = py = 0
+    if residual is not None:
+        ld_a, pa = _matrix("residual", residual, dtype, dev, rows, cols), residual.data_ptr()
+        if residual_out is None:
+            residual_out = x.new_empty((rows, cols))
+            ld_r = cols
+        else:
+            ld_r = _matrix("residual_out", residual_out, dtype, dev, rows, cols)
+        pr = residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    y = q = None
+    if quantize is not None:
+        y, q = _new_eight(rows, cols, _eight_type(quantize), (_blocks(cols), rows), device)
+    elif out is None:
+        out = x.new_empty((rows, cols))
+    if out is not None:
+        ld_y, py = _matrix("out", out, dtype, dev, rows, cols), out.data_ptr()
+    if y is None:
+        y = out
+    rstd = torch.empty(rows, dtype=torch.float32, device=device)
+    d = B.muon_rmsnorm(rows, cols, ld_x, ld_a, ld_r, ld_y, 0, code, eps)
+    s = _on(dev, B.muon_rmsnorm_forward, d, x.data_ptr(), pa, 0 if weight is None else _vector("weight", weight, cols, dev),
+            pr, py, q, rstd.data_ptr())
+    if s:
+        _check(s, "rmsnorm_forward")
+    return (y, rstd) if residual is None else (y, rstd, residual_out)
+
+
+def rmsnorm_backward(dy, x, rstd, weight=None, add=None, dweight=None, accumulate=False, out=None):
+    """(dx, dweight): the gradient of x (what the norm was taken of: with a
+    residual, the r that the forward pass returned), plus `add`, and the float32
+    gradient of weight, written to (or with accumulate added to) the tensor given;
+    True allocates one, None leaves it out. `out` may be `add` itself, unless that
+    is dy or x too."""
+    dtype, device, dev = _first("dy", dy)
+    code = _norm_type("dy", dtype)
+    ld_y = _matrix("dy", dy, dtype, dev)
+    rows, cols = dy.shape
+    ld_x = _matrix("x", x, dtype, dev, rows, cols)
+    pr = _vector("rstd", rstd, rows, dev)
+    pw = 0 if weight is None else _vector("weight", weight, cols, dev)
+    ld_a, pa = (0, 0) if add is None else (_matrix("add", add, dtype, dev, rows, cols), add.data_ptr())
+    if dweight is True:
+        if accumulate:
+            raise ValueError("accumulate needs the tensor to add to")
+        dweight = torch.empty(cols, dtype=torch.float32, device=device)
+    pdw = 0 if dweight is None else _vector("dweight", dweight, cols, dev)
+    if out is None:
+        out = dy.new_empty((rows, cols))
+        ld_o = cols
+    else:
+        ld_o = _matrix("out", out, dtype, dev, rows, cols)
+    d = B.muon_rmsnorm(rows, cols, ld_x, ld_a, 0, ld_y, ld_o, code, 0.0)
+    nbytes = 0
+    if dweight is not None:
+        s, nbytes = B.muon_rmsnorm_workspace_bytes(d)
+        if s:
+            _check(s, "rmsnorm_backward")
+    ws, pws = _workspace(nbytes, device)
+    s = _on(dev, B.muon_rmsnorm_backward, d, dy.data_ptr(), x.data_ptr(), pw, pr, pa, out.data_ptr(), pdw,
+            int(accumulate), pws, nbytes)
+    if s:
+        _check(s, "rmsnorm_backward")
+    return out, dweight
+
+
+def quantize_fp8(x, dtype=torch.float8_e4m3fn):
+    """x [rows, cols] (bf16, fp16 or fp32; an activation or a gradient) as Fp8, a
+    scale for each 128 columns of a row."""
+    kind, device, dev = _first("x", x)
+    code = _norm_type("x", kind)
+    ld = _matrix("x", x, kind, dev)
+    rows, cols = x.shape
+    y, q = _new_eight(rows, cols, _eight_type(dtype), (_blocks(cols), rows), device)
+    s = _on(dev, B.muon_quantize, rows, cols, ld, code, x.data_ptr(), q)
+    if s:
+        _check(s, "quantize_fp8")
+    return y
+
+
+def quantize_fp8_weight(w, weight_layout="in_out", transpose=False):
+    """(w8, w8_t) of a weight (bf16, fp16 or fp32: a view of the flat parameters as
+    it is) in float8_e4m3fn, a scale for each 128 x 128: w8 [out, in] for
+    linear_fp8_forward and, with transpose, w8_t [in, out] for
+    linear_fp8_grad_input, else None."""
+    kind, device, dev = _first("w", w)
+    code = _norm_type("w", kind)
+    lay, fin, fout = _weight(w, weight_layout)
+    ld = _matrix("w", w, kind, dev)
+    rows, cols = w.shape
+    w8, q = _new_eight(fout, fin, torch.float8_e4m3fn, (_blocks(fout), _blocks(fin)), device)
+    w8_t = q_t = None
+    if transpose:
+        w8_t, q_t = _new_eight(fin, fout, torch.float8_e4m3fn, (_blocks(fin), _blocks(fout)), device)
+    if lay == B.MUON_WEIGHT_IN_OUT:
+        q, q_t = q_t, q
+    s = _on(dev, B.muon_quantize_weight, rows, cols, ld, code, w.data_ptr(), q, q_t)
+    if s:
+        _check(s, "quantize_fp8_weight")
+    return w8, w8_t
+
+
+def linear_fp8_forward(x, w, bias=None, residual=None, activation="none", save_preact=False, dtype=torch.bfloat16,
+                       out=None, preact_out=None):
+    """y = act(x w^T + bias) + residual in `dtype` (bf16 or fp16) of 8-bit x [tokens,
+    in] and w [out, in]; with save_preact (or preact_out) also z = x w^T + bias
+    rounded to it: returns y, or (y, z). `out` may be `residual` itself."""
+    _, device, dev = _first("x", x[0])
+    code = _linear_type("dtype", dtype)
+    act = _choice(ACTIVATIONS, activation, "activation")
+    a, n, fin = _eight("x", x, dev, False)
+    b, fout, k = _eight("w", w, dev, True)
+    if k != fin:
+        raise ValueError(f"w: {k} in features, expected {fin}")
+    z = preact_out
+    if z is None and save_preact:
+        z = torch.empty((n, fout), dtype=dtype, device=device)
+    if out is None:
+        out = torch.empty((n, fout), dtype=dtype, device=device)
+        ld_y = fout
+    else:
+        ld_y = _matrix("out", out, dtype, dev, n, fout)
+    e = None
+    if act or bias is not None or residual is not None or z is not None:
+        e = B.muon_epilogue(act, 0, None if bias is None else _vector("bias", bias, fout, dev))
+        if residual is not None:
+            e.ld_add = _matrix("residual", residual, dtype, dev, n, fout)
+            e.add = residual.data_ptr()
+        if z is not None:
+            e.ld_z = _matrix("preact_out", z, dtype, dev, n, fout)
+            e.z = z.data_ptr()
+    d = B.muon_linear(n, fin, fout, 0, 0, ld_y, code, B.MUON_WEIGHT_OUT_IN)
+    s = _on(dev, B.muon_linear_scaled_forward, d, a, b, e, out.data_ptr())
+    if s:
+        _check(s, "linear_fp8_forward")
+    return out if z is None else (out, z)
+
+
+def linear_fp8_grad_input(dy, w, preact=None, activation="none", add=None, dtype=torch.bfloat16, out=None):
+    """dx = (dy w^T) * act'(preact) + add in `dtype` (bf16 or fp16) of 8-bit dy
+    [tokens, out] and w [in, out], as linear_grad_input. `out` may be `add`
+    itself."""
+    _, device, dev = _first("dy", dy[0])
+    code = _linear_type("dtype", dtype)
+    act = _choice(ACTIVATIONS, activation, "activation")
+    a, n, fout = _eight("dy", dy, dev, False)
+    b, fin, k = _eight("w", w, dev, True)
+    if k != fout:
+        raise ValueError(f"w: {k} out features, expected {fout}")
+    if out is None:
+        out = torch.empty((n, fin), dtype=dtype, device=device)
+        ld_x = fin
+    else:
+        ld_x = _matrix("out", out, dtype, dev, n, fin)
+    e = _grad_epilogue("linear_fp8_grad_input", act, preact, add, dtype, dev, n, fin)
+    d = B.muon_linear(n, fin, fout, ld_x, 0, 0, code, B.MUON_WEIGHT_IN_OUT)
+    s = _on(dev, B.muon_linear_scaled_grad_input, d, a, b, e, out.data_ptr())
+    if s:
+        _check(s, "linear_fp8_grad_input")
+    return out
+
+
+def _grad_epilogue(what, act, preact, add, dtype, dev, n, fin):
+    """The epilogue of an input gradient, or None."""
+    if not act and add is None:
+        return None
+    e = B.muon_epilogue(act, 0)
+    if add is not None:
+        e.ld_add = _matrix("add", add, dtype, dev, n, fin)
+        e.add = add.data_ptr()
+    if act:
+        if preact is None:
+            raise ValueError(f"{what}: an activation needs its preact")
+        e.ld_z = _matrix("preact", preact, dtype, dev, n, fin)
+        e.z = preact.data_ptr()
+    return e
+
+
+def _experts(name, w, dtype, dev, layout, shape=None):
+    """(layout code, experts, in, out, row stride, expert stride) of the experts'
+    weights, [experts, in, out] or [experts, out, in]."""
+    lay = _choice(_LAYOUTS, layout, "weight_layout")
+    if w.dim() != 3 or shape is not None and tuple(w.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(w.shape)}, expected " +
+                         ("[experts, rows, cols]" if shape is None else str(list(shape))))
+    _same(name, w, dtype, dev)
+    n, a, b = w.shape
+    s0, s1, s2 = w.stride()
+    if s2 != 1 and b > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if a <= 1:
+        s1 = b
+    if n <= 1:
+        s0 = a * s1
+    if s1 < b or s0 < (a - 1) * s1 + b:
+        raise ValueError(f"{name}: rows overlap (strides {s0}, {s1}, length {b})")
+    return (lay, n, a, b, s1, s0) if lay == B.MUON_WEIGHT_IN_OUT else (lay, n, b, a, s1, s0)
+
+
+def _offsets(offsets, experts, dev):
+    """Address of the experts' row offsets, after their checks."""
+    _same("offsets", offsets, torch.int32, dev)
+    if experts >= 0 and offsets.shape != (experts + 1,) or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError(f"offsets: shape {tuple(offsets.shape)}, expected "
+                         f"[{'experts + 1' if experts < 0 else experts + 1}]")
+    if offsets.stride(0) != 1:
+        raise ValueError("offsets: must be contiguous")
+    return offsets.data_ptr()
+
+
+def _expert_vectors(name, t, experts, n, dev):
+    """Address of contiguous float32 vectors, one an expert."""
+    _same(name, t, torch.float32, dev)
+    if t.shape != (experts, n) or not t.is_contiguous():
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{experts}, {n}], contiguous")
+    return t.data_ptr()
+
+
+def grouped_linear_forward(x, w, offsets, bias=None, residual=None, activation="none", weight_layout="in_out",
+                           save_preact=False, out=None, preact_out=None):
+    """linear_forward of a mixture's experts on rows grouped by expert: rows
+    offsets[e] .. offsets[e + 1] - 1 of x [rows, in] go through w[e] and bias[e].
+    w: [experts, in, out] or [experts, out, in], bias [experts, out], offsets int32
+    [experts + 1], ascending, on the device, where they are read. Rows of no expert
+    (a padded batch's) are left as they are: unset, in an `out` that the call
+    allocates."""
+    dtype, device, dev = _first("x", x)
+    code = _linear_type("x", dtype)
+    act = _choice(ACTIVATIONS, activation, "activation")
+    lay, n_e, fin, fout, ld_w, step = _experts("w", w, dtype, dev, weight_layout)
+    po = _offsets(offsets, n_e, dev)
+    ld_x = _matrix("x", x, dtype, dev, -1, fin)
+    n = x.shape[0]
+    z = preact_out
+    if z is None and save_preact:
+        z = x.new_empty((n, fout))
+    if out is None:
+        out = x.new_empty((n, fout))
+        ld_y = fout
+    else:
+        ld_y = _matrix("out", out, dtype, dev, n, fout)
+    e = None
+    if act or bias is not None or residual is not None or z is not None:
+        e = B.muon_epilogue(act, 0, None if bias is None else _expert_vectors("bias", bias, n_e, fout, dev))
+        if residual is not None:
+            e.ld_add = _matrix("residual", residual, dtype, dev, n, fout)
+            e.add = residual.data_ptr()
+        if z is not None:
+            e.ld_z = _matrix("preact_out", z, dtype, dev, n, fout)
+            e.z = z.data_ptr()
+    d = B.muon_grouped(n, n_e, fin, fout, ld_x, ld_w, ld_y, step, code, lay)
+    s = _on(dev, B.muon_grouped_linear_forward, d, x.data_ptr(), w.data_ptr(), po, e, out.data_ptr())
+    if s:
+        _check(s, "grouped_linear_forward")
+    return out if z is None else (out, z)
+
+
+def grouped_linear_grad_input(dy, w, offsets, preact=None, activation="none", add=None, weight_layout="in_out",
+                              out=None):
+    """linear_grad_input of a mixture's experts, rows as grouped_linear_forward's."""
+    dtype, device, dev = _first("dy", dy)
+    code = _linear_type("dy", dtype)
+    act = _choice(ACTIVATIONS, activation, "activation")
+    lay, n_e, fin, fout, ld_w, step = _experts("w", w, dtype, dev, weight_layout)
+    po = _offsets(offsets, n_e, dev)
+    ld_y = _matrix("dy", dy, dtype, dev, -1, fout)
+    n = dy.shape[0]
+    if out is None:
+        out = dy.new_empty((n, fin))
+        ld_x = fin
+    else:
+        ld_x = _matrix("out", out, dtype, dev, n, fin)
+    e = _grad_epilogue("grouped_linear_grad_input", act, preact, add, dtype, dev, n, fin)
+    d = B.muon_grouped(n, n_e, fin, fout, ld_x, ld_w, ld_y, step, code, lay)
+    s = _on(dev, B.muon_grouped_linear_grad_input, d, dy.data_ptr(), w.data_ptr(), po, e, out.data_ptr())
+    if s:
+        _check(s, "grouped_linear_grad_input")
+    return out
+
+
+def grouped_linear_grad_weight(x, dy, offsets, dw=None, dbias=None, accumulate=False, weight_layout="in_out"):
+    """(dw, dbias): the float32 gradients of the experts' weights [experts, in, out]
+    (or [experts, out, in]; `count` matrices of a Muon table's entry, where dw is a
+    view of the flat gradient buffer) and biases [experts, out], written to (or with
+    accumulate added to) the tensors given. dbias=True allocates one; None leaves it
+    out. Zeros (or unchanged) for experts without rows."""
+    dtype, device, dev = _first("x", x)
+    code = _linear_type("x", dtype)
+    lay = _choice(_LAYOUTS, weight_layout, "weight_layout")
+    po = _offsets(offsets, -1, dev)
+    n_e = offsets.shape[0] - 1
+    ld_x = _matrix("x", x, dtype, dev)
+    n, fin = x.shape
+    ld_y = _matrix("dy", dy, dtype, dev, n)
+    fout = dy.shape[1]
+    shape = (n_e, fin, fout) if lay == B.MUON_WEIGHT_IN_OUT else (n_e, fout, fin)
+    if accumulate and (dw is None or dbias is True):
+        raise ValueError("accumulate needs the tensors to add to")
+    if dw is None:
+        dw = torch.empty(shape, dtype=torch.float32, device=device)
+    ld_w, step = _experts("dw", dw, torch.float32, dev, weight_layout, shape)[4:]
+    if dbias is True:
+        dbias = torch.empty((n_e, fout), dtype=torch.float32, device=device)
+    pb = 0 if dbias is None else _expert_vectors("dbias", dbias, n_e, fout, dev)
+    d = B.muon_grouped(n, n_e, fin, fout, ld_x, ld_w, ld_y, step, code, lay)
+    s = _on(dev, B.muon_grouped_linear_grad_weight, d, x.data_ptr(), dy.data_ptr(), po, dw.data_ptr(), pb,
+            int(accumulate))
+    if s:
+        _check(s, "grouped_linear_grad_weight")
+    return dw, dbias
