@@ -108,23 +108,24 @@ struct Operand {
         }
     }
 
-    // issue the next slice's loads to LDS address S
+    // issue the next slice's loads to LDS address S; the one after is STEP further
+    template <int STEP = 1>
     __device__ __forceinline__ void load(uint32_t S) {
         if constexpr (KC) {
             const uint32_t dead = kch < left ? 0u : OUT;  // chunks past the end of k
             const uint32_t so = left > 0 ? soff : 0u;
 #pragma unroll
             for (int q = 0; q < NLD; ++q) load_lds(r, S + lds_row + q * 4096, off[q] | dead, so);
-            soff += 2 * BK;
+            soff += 2 * BK * STEP;
         } else {
             r[2] = left >= BK ? range : left > 0 ? (uint32_t)(left - 1) * rowb + tail : 0u;
 #pragma unroll
             for (int q = 0; q < NLD; ++q) load_lds(r, S + lds_row + q * 4096, off[q], 0u);
-            const uint64_t base = (((uint64_t)r[1] << 32) | r[0]) + (uint64_t)BK * rowb;
+            const uint64_t base = (((uint64_t)r[1] << 32) | r[0]) + (uint64_t)(BK * STEP) * rowb;
             r[0] = (uint32_t)base;
             r[1] = (uint32_t)(base >> 32) & 0xffffu;
         }
-        left -= BK;
+        left -= BK * STEP;
     }
     // fragment block f of k16 step ks
     __device__ __forceinline__ typename V8<T>::type read(const char* S, int ks, int f) const {
@@ -357,8 +358,157 @@ __device__ __forceinline__ void tile_epilogue(const GemmArgs& g, char* smem, int
     }
 }
 
+// The same for a whole tile of a known MODE: what a block of 32 rows needs is decided
+// once for its passes, whose reads, activations and stores then go out together
+// (chunk by chunk, with every mode's branches in each, a 256 x 128 tile's epilogue took
+// 20000 clocks without any input or activation).
+template <int MODE, typename T, int TM, int TN, typename STAGE>
+__device__ __forceinline__ void whole_epilogue(const GemmArgs& g, char* smem, int i0, int j0, int lane, int wave,
+                                               STAGE&& stage) {
+    using U = std::conditional_t<MODE == EPI_GRAD_WEIGHT, float, T>;
+    constexpr int WM = TM / 2, WN = TN / 2;   // a wave's block
+    constexpr int FRI = WM / 32;
+    constexpr int SROW = kStagedRow<WN>;
+    constexpr int CPR = WN / 8;      // chunks of 8 per staged row
+    constexpr int RPI = 64 / CPR;    // rows per pass of the wave
+    constexpr int NP = 32 / RPI;     // passes per block
+    constexpr int PG = TM == 256 && NP > 2 ? 2 : NP;  // of them at a time, beside the tall tile's sums
+    const Epilogue& E = g.epi;
+    const int wi = wave >> 1, wj = wave & 1;
+    char* W = smem + wave * 32 * SROW;
+    const int ch = lane % CPR, rr = lane / CPR;
+    const int wrow = i0 + wi * WM, wcol = j0 + wj * WN;  // the wave's first row and column
+    const int col = wcol + ch * 8;
+    const bool inside = col < g.N;
+    const int ncol = g.N - col >= 8 ? 8 : g.N - col;  // of the lane's chunk: fewer at the edge
+    const bool edge = i0 + TM > g.M || j0 + TN > g.N;
+    const int act = E.act;
+    // what is read: on the way back through an activation z first, then add
+    const bool slope = MODE == EPI_GRAD_INPUT && act != ACT_NONE;
+    const U* const p1 = MODE == EPI_GRAD_WEIGHT ? (E.accumulate ? static_cast<const U*>(E.y) : nullptr)
+                                                : static_cast<const U*>(slope ? E.z : E.add);
+    const U* const p2 = slope ? static_cast<const U*>(E.add) : nullptr;
+    const int ld1 = MODE == EPI_GRAD_WEIGHT ? E.ld_y : slope ? E.ld_z : E.ld_add, ld2 = E.ld_add;
+    const int lane1 = rr * ld1 + ch * 8, lane2 = rr * ld2 + ch * 8;
+    auto row_of = [&](int fi, int it) { return wrow + 32 * fi + it * RPI; };
+    // the lane's chunk of pass `it`; lanes without a whole one have their row's first
+    // (rows of less than one read nothing ahead)
+    auto chunk = [&](const U* p, int ld, int ln, int fi, int it) {
+        if (!edge) return p + ((int64_t)row_of(fi, it) * ld + wcol) + ln;
+        const int row = row_of(fi, it) + rr;
+        return p + ((int64_t)(row < g.M ? row : g.M - 1) * ld + (inside && ncol == 8 ? col : 0));
+    };
+    typedef u32x4 Chunk[sizeof(U) / 2];
+    auto fetch = [&](const U* p, int ld, int ln, int fi, Chunk(&x)[NP]) {
+#pragma unroll
+        for (int it = 0; it < NP; ++it) {
+            const u32x4_mem* q = reinterpret_cast<const u32x4_mem*>(chunk(p, ld, ln, fi, it));
+#pragma unroll
+            for (int k = 0; k < (int)sizeof(U) / 2; ++k) x[it][k] = __builtin_nontemporal_load(q + k);
+        }
+    };
+    // the chunk's values, from what was fetched or, of fewer than 8, in place
+    auto widen = [&](const Chunk& x, const U* p, int ld, int fi, int it, float* t) {
+        if (edge && ncol < 8) {
+            const int row = row_of(fi, it) + rr;
+            float u[8];
+            load8(p + ((int64_t)(row < g.M ? row : g.M - 1) * ld + col), ncol, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = u[e];
+        } else if constexpr (sizeof(U) == 2) {
+            const typename V8<T>::type u = __builtin_bit_cast(typename V8<T>::type, x[0]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = (float)u[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = __uint_as_float(x[e / 4][e % 4]);
+        }
+    };
+    auto put = [&](U* p, int ld, int fi, int from, const float (&v)[8 * PG]) {
+        const int ln = rr * ld + ch * 8;
+#pragma unroll
+        for (int k = 0; k < PG; ++k) {
+            const int it = from + k;
+            float u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = v[8 * k + e];
+            if (!edge)
+                stream8(p + ((int64_t)row_of(fi, it) * ld + wcol) + ln, 8, u);
+            else if (inside && row_of(fi, it) + rr < g.M)
+                stream8(p + ((int64_t)(row_of(fi, it) + rr) * ld + col), ncol, u);
+        }
+    };
+    float bias[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (MODE == EPI_FORWARD && E.bias && inside) load8(E.bias + col, ncol, bias);
+    // inputs of this block and of the next one, which go out before this one's stores
+    Chunk a0[NP], a1[NP], b0[NP];
+    const bool ahead = p1 && g.N >= 8, second = p2 && g.N >= 8;
+    if (ahead) fetch(p1, ld1, lane1, 0, a0);
+#pragma unroll 1
+    for (int fi = 0; fi < FRI; ++fi) {
+        static_for<0, FRI>([&](auto f_c) {
+            constexpr int F = decltype(f_c)::value;
+            if (fi == F) {
+                stage(f_c, W);
+                asm volatile("" ::"n"(F));  // as in tile_epilogue
+            }
+        });
+        if (second) fetch(p2, ld2, lane2, fi, b0);
+        if (ahead && fi + 1 < FRI) fetch(p1, ld1, lane1, fi + 1, a1);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        static_for<0, NP / PG>([&](auto p_c) {
+            constexpr int from = decltype(p_c)::value * PG;
+            float v[8 * PG];
+#pragma unroll
+            for (int k = 0; k < PG; ++k) {
+                const f32x4* s = reinterpret_cast<const f32x4*>(W + ((from + k) * RPI + rr) * SROW + 32 * ch);
+                const f32x4 lo = s[0], up = s[1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[8 * k + e] = lo[e];
+                    v[8 * k + 4 + e] = up[e];
+                }
+            }
+            if constexpr (MODE == EPI_FORWARD) {
+#pragma unroll
+                for (int n = 0; n < 8 * PG; ++n) v[n] += bias[n & 7];
+                if (E.z) put(static_cast<U*>(E.z), E.ld_z, fi, from, v);
+                act_values(act, v);
+            }
+            if (p1) {
+                float t[8 * PG];
+#pragma unroll
+                for (int k = 0; k < PG; ++k) widen(a0[from + k], p1, ld1, fi, from + k, t + 8 * k);
+                if (slope) {
+                    act_slopes(act, t);
+#pragma unroll
+                    for (int n = 0; n < 8 * PG; ++n) v[n] *= t[n];
+                    if (p2) {
+#pragma unroll
+                        for (int k = 0; k < PG; ++k) widen(b0[from + k], p2, ld2, fi, from + k, t + 8 * k);
+                    }
+                }
+                if (!slope || p2) {
+#pragma unroll
+                    for (int n = 0; n < 8 * PG; ++n) v[n] += t[n];
+                }
+            }
+            put(static_cast<U*>(E.y), E.ld_y, fi, from, v);
+        });
+        if (p1) {
+#pragma unroll
+            for (int it = 0; it < NP; ++it)
+#pragma unroll
+                for (int k = 0; k < (int)sizeof(U) / 2; ++k) a0[it][k] = a1[it][k];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 // LDS of a tile's product
-template <typename T, int TM, int TN, bool AKC, bool BKC, bool RAW>
+template <typename T, int TM, int TN, bool AKC, bool BKC, bool RAW, int STAGES = 4, int KG = 1>
 struct GemmShape {
     using OA = std::conditional_t<RAW, RawOperand<T, TM, AKC>, Operand<T, TM, AKC>>;
     using OB = std::conditional_t<RAW, RawOperand<T, TN, BKC>, Operand<T, TN, BKC>>;
@@ -366,33 +516,43 @@ struct GemmShape {
     static constexpr int FRI = WM / 32, FRJ = WN / 32;
     // the tall tile: two A buffers and one B buffer, so that two workgroups fit
     // a CU; the square tiles, for products too small to fill the chip, whose
-    // time is load latency: a ring of four buffers of both
+    // time is load latency: a ring of four (STAGES) buffers of both
     static constexpr bool RING = TM <= 128;
     static constexpr int STAGE = OA::BYTES + OB::BYTES;
-    static constexpr int SMEM = RAW ? 2 * STAGE : RING ? 4 * STAGE : OA::BYTES + STAGE;
+    static constexpr int SMEM = RAW ? 2 * STAGE : RING ? KG * STAGES * STAGE : OA::BYTES + STAGE;
+    // the sums of the groups of waves but the first, behind the epilogue's staging
+    static constexpr int MEET = (4 * 32 * kStagedRow<WN> + 1023) / 1024 * 1024;
     static_assert(4 * 32 * kStagedRow<WN> <= SMEM, "epilogue staging");
+    static constexpr int MEET_SUMS = MEET + (KG - 1) * TM * TN * 4;
+    static_assert(KG == 1 || (RING && !RAW && MEET_SUMS + (KG - 1) * 1024 * FRI <= SMEM), "groups of waves");
 };
 
 // SUM: also the sums over k of the B (1) or A (2) operand's rows, for the bias
 // gradient: two-element dot products with 1 on the fragments in registers, in
 // the shadow of the matrix instructions. RAW: operands as RawOperand has them.
-// The tile (ti, tj)'s product over nk slices from s0 on, and its epilogue.
-template <typename T, int TM, int TN, bool AKC, bool BKC, int SUM, bool RAW>
+// The tile (ti, tj)'s product over nk slices from s0 on, and its epilogue. KG groups of
+// 4 waves take the slices in turn, each through a ring of its own, where a few tiles
+// leave most of the chip idle and a slice is the latency of its reads and products one
+// after the other; their sums meet in LDS, in the groups' order. MODE: the epilogue's,
+// where it is known (and the tile whole).
+template <typename T, int TM, int TN, bool AKC, bool BKC, int SUM, bool RAW, int STAGES = 4, int KG = 1,
+          int MODE = -1>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& g, char* smem, int ti, int tj, int piece, int s0, int nk) {
-    using Shape = GemmShape<T, TM, TN, AKC, BKC, RAW>;
+    using Shape = GemmShape<T, TM, TN, AKC, BKC, RAW, STAGES, KG>;
     using OA = typename Shape::OA;
     using OB = typename Shape::OB;
     constexpr int WM = Shape::WM, WN = Shape::WN, FRI = Shape::FRI, FRJ = Shape::FRJ, STAGE = Shape::STAGE;
     constexpr bool RING = Shape::RING;
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = KG > 1 ? threadIdx.x & 255 : threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int grp = KG > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8) : 0;
     const int wi = wave >> 1, wj = wave & 1;
     // a k-contiguous operand's rows go on to the next multiple of 8 (zeros), the
     // rows of the others likewise
     const int kp = (g.K + 7) & ~7, kmax = (AKC || BKC) && !RAW ? kp : g.K;
     const int i0 = ti * TM, j0 = tj * TN;
-    const int kb = s0 * BK;
-    int ke = kb + nk * BK;
+    const int kb = (s0 + grp) * BK;
+    int ke = s0 * BK + nk * BK;
     ke = ke < kmax ? ke : kmax;
 
     OA A;
@@ -457,7 +617,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, char* smem, int ti,
     using CM = std::integral_constant<int, FRI * FRJ>;
     using CH = std::integral_constant<int, FRI * FRJ / 2>;
 
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)smem;
+    char* const ring = smem + grp * STAGES * STAGE;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)ring;
     if constexpr (RAW) {
         if (nk > 0) {  // else there may be no row to read
             // two slices in LDS, the three after the current one in registers or
@@ -560,22 +721,23 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, char* smem, int ti,
             if (kt + 1 < nk) slice(smem + OA::BYTES, smem, SB, lds0);
         }
     } else {
+        static_assert((STAGES & (STAGES - 1)) == 0, "a ring's index");
         constexpr int NLD = OA::NLD + OB::NLD;
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            A.load(lds0 + k * STAGE);
-            B.load(lds0 + k * STAGE + OA::BYTES);
+        for (int k = 0; k < STAGES - 1; ++k) {
+            A.template load<KG>(lds0 + k * STAGE);
+            B.template load<KG>(lds0 + k * STAGE + OA::BYTES);
         }
-        wait_vm<2 * NLD>();
+        wait_vm<(STAGES - 2) * NLD>();
         __syncthreads();
-        read_b(smem + OA::BYTES, 0);
-        read_a(smem, 0);
+        read_b(ring + OA::BYTES, 0);
+        read_a(ring, 0);
         // S: this slice, N: the next, ldsF: the buffer of the one before,
         // which every wave had read before the last barrier
         auto slice = [&](const char* __restrict__ S, const char* __restrict__ N, uint32_t ldsF)
                          __attribute__((always_inline)) {
-            A.load(ldsF);
-            B.load(ldsF + OA::BYTES);
+            A.template load<KG>(ldsF);
+            B.template load<KG>(ldsF + OA::BYTES);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int ks = 0; ks < NKS - 1; ++ks) {
@@ -588,20 +750,59 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, char* smem, int ti,
             products(NKS - 1, 0, FRI / 2);
             add_sums(NKS - 1);
             __builtin_amdgcn_sched_barrier(0);
-            wait_vm<2 * NLD>();  // the next slice has landed
+            wait_vm<(STAGES - 2) * NLD>();  // the next slice has landed
             __syncthreads();
             read_b(N + OA::BYTES, 0);
             read_a(N, 0);
             products(NKS - 1, FRI / 2, FRI);
             interleave(std::integral_constant<int, RA + RB>{}, CH{});
         };
-        for (int kt = 0; kt < nk; ++kt)
-            slice(smem + (kt & 3) * STAGE, smem + ((kt + 1) & 3) * STAGE, lds0 + ((kt + 3) & 3) * STAGE);
+        const int turns = (nk + KG - 1) / KG;  // past the end, zeros are added
+        for (int kt = 0; kt < turns; ++kt)
+            slice(ring + (kt & (STAGES - 1)) * STAGE, ring + ((kt + 1) & (STAGES - 1)) * STAGE,
+                  lds0 + ((kt - 1) & (STAGES - 1)) * STAGE);
         wait_vm0();  // the loads past the end
     }
     __syncthreads();
+    if constexpr (KG > 1) {
+        char* const meet = smem + Shape::MEET;
+        auto place = [&](int group, int n) {
+            return reinterpret_cast<f32x4*>(meet + (((group - 1) * FRI * FRJ * 4 + n) * 256 + tid) * 16);
+        };
+        if (grp > 0) {
+            static_for<0, FRI * FRJ * 4>([&](auto n_c) {
+                constexpr int n = decltype(n_c)::value;
+                const f32x16& a = acc[n / (4 * FRJ)][n / 4 % FRJ];
+                *place(grp, n) = f32x4{a[4 * (n & 3)], a[4 * (n & 3) + 1], a[4 * (n & 3) + 2], a[4 * (n & 3) + 3]};
+            });
+        }
+        float* const meet_sums = reinterpret_cast<float*>(smem + Shape::MEET_SUMS);
+        if constexpr (SUM != 0) {
+            if (grp > 0)
+#pragma unroll
+                for (int f = 0; f < NSUM; ++f) meet_sums[((grp - 1) * NSUM + f) * 256 + tid] = sums[f];
+        }
+        __syncthreads();
+        if constexpr (SUM != 0) {
+            if (grp == 0)
+#pragma unroll
+                for (int f = 0; f < NSUM; ++f)
+#pragma unroll
+                    for (int k = 1; k < KG; ++k) sums[f] += meet_sums[((k - 1) * NSUM + f) * 256 + tid];
+        }
+        if (grp == 0) static_for<0, FRI * FRJ * 4>([&](auto n_c) {
+            constexpr int n = decltype(n_c)::value;
+            f32x16& a = acc[n / (4 * FRJ)][n / 4 % FRJ];
+#pragma unroll
+            for (int k = 1; k < KG; ++k) {
+                const f32x4 v = *place(k, n);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[4 * (n & 3) + e] += v[e];
+            }
+        });
+    }
 
-    tile_epilogue<T, TM, TN>(g, smem, i0, j0, piece, lane, wave, [&](auto f_c, char* W) {
+    auto stage = [&](auto f_c, char* W) {
         constexpr int F = decltype(f_c)::value;
         const int l32 = lane & 31, hi = lane >> 5;
 #pragma unroll
@@ -613,7 +814,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, char* smem, int ti,
                 for (int e = 0; e < 4; ++e) v[e] = acc[F][fj][4 * q + e];
                 *reinterpret_cast<f32x4*>(W + l32 * kStagedRow<WN> + 4 * (32 * fj + 8 * q + 4 * hi)) = v;
             }
-    });
+    };
+    if constexpr (MODE < 0)
+        tile_epilogue<T, TM, TN>(g, smem, i0, j0, piece, lane, wave, stage);
+    else if (grp == 0)
+        whole_epilogue<MODE, T, TM, TN>(g, smem, i0, j0, lane, wave, stage);
     if constexpr (SUM != 0) {
         const int l32 = lane & 31, hi = lane >> 5;
         const bool direct = piece < 0;
@@ -625,11 +830,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, char* smem, int ti,
 #pragma unroll
             for (int f = 0; f < NSUM; ++f) {
                 sums[f] += __shfl_xor(sums[f], 32, 64);
-                if (wj == 1 && hi == 0) half[wi * WM + 32 * f + l32] = sums[f];
+                if (grp == 0 && wj == 1 && hi == 0) half[wi * WM + 32 * f + l32] = sums[f];
             }
             __syncthreads();
         }
-        const bool mine = SUM == 1 ? ti == tj % g.tiles_m && wi == 0 : tj == ti % g.tiles_n && wj == 0;
+        const bool mine = grp == 0 && (SUM == 1 ? ti == tj % g.tiles_m && wi == 0 : tj == ti % g.tiles_n && wj == 0);
         if (mine) {
             const int at = (SUM == 1 ? wj * WN : wi * WM) + l32;
             const int n = (SUM == 1 ? j0 : i0) + at, end = SUM == 1 ? g.N : g.M;
@@ -664,13 +869,14 @@ __device__ __forceinline__ f32x4 mfma16<f16>(f16x8 a, f16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// The epilogue of few rows: a workgroup's 8 waves have left their sums [rows][TNS] in
-// LDS, `stride` bytes apart, which are added in wave order.
+// The epilogue of few rows, `rows` of them from row i0 on: a workgroup's 8 waves have left
+// their sums [rows][TNS] in LDS, `stride` bytes apart, which are added in wave order.
 template <typename T, int TNS>
-__device__ __forceinline__ void few_epilogue(const Epilogue& epi, int M, int N, const char* smem, int stride, int j0) {
+__device__ __forceinline__ void few_epilogue(const Epilogue& epi, int i0, int rows, int N, const char* smem, int stride,
+                                             int j0) {
     const int row = threadIdx.x / (TNS / 8), c = threadIdx.x % (TNS / 8) * 8;
     const int col = j0 + c, left = N - col;
-    if (row >= M || left <= 0) return;
+    if (row >= rows || left <= 0) return;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
@@ -686,10 +892,10 @@ __device__ __forceinline__ void few_epilogue(const Epilogue& epi, int M, int N, 
     if (epi.bias) load8(epi.bias + col, left, bias);
     u32x4 in = {0, 0, 0, 0}, in2 = in;
     if (left >= 8) {
-        in = first8<T>(epi, row, col, LaneAt());
-        if (has_second(epi)) in2 = second8<T>(epi, row, col, LaneAt());
+        in = first8<T>(epi, i0 + row, col, LaneAt());
+        if (has_second(epi)) in2 = second8<T>(epi, i0 + row, col, LaneAt());
     }
-    finish8<T>(epi, row, col, LaneAt(), left, v, bias, in, in2);
+    finish8<T>(epi, i0 + row, col, LaneAt(), left, v, bias, in, in2);
 }
 
 // LDS of a workgroup for few rows
@@ -824,7 +1030,7 @@ __device__ __forceinline__ void skinny_tile(const SkinnyArgs& g, char* smem, int
         for (int m = 0; m < MT; ++m)
             *reinterpret_cast<f32x4*>(own + (m * 16 + l16) * TNS + 16 * h + 4 * g16) = acc[h][m];
     __syncthreads();
-    few_epilogue<T, TNS>(g.epi, g.M, g.N, smem, R * STAGE, j0);
+    few_epilogue<T, TNS>(g.epi, 0, g.M, g.N, smem, R * STAGE, j0);
 }
 
 }  // namespace

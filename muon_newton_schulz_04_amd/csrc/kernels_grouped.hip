@@ -89,6 +89,30 @@ __device__ __forceinline__ bool find_block(const GroupedArgs& p, Block& out, F&&
     return false;
 }
 
+// The expert with the r-th most rows (of equal ones the first), and its rows; of more
+// than 64 experts, which are not ranked, the r-th.
+__device__ __forceinline__ int ranked(const GroupedArgs& p, int r, int& begin, int& end) {
+    const int lane = threadIdx.x & 63;
+    int e = r;
+    if (p.experts <= 64) {
+        const Group q = lane < p.experts ? group_of(p.offsets, p.rows, lane) : Group{0, -1};
+        const int n = q.end - q.begin;
+        int before = 0;
+        for (int k = 0; k < p.experts; ++k) {
+            const int m = __builtin_amdgcn_readlane(n, k);
+            before += m > n || (m == n && k < lane) ? 1 : 0;
+        }
+        e = __builtin_ctzll(__ballot(before == r));
+        begin = __builtin_amdgcn_readlane(q.begin, e);
+        end = __builtin_amdgcn_readlane(q.end, e);
+    } else {
+        const Group q = group_of(p.offsets, p.rows, e);
+        begin = __builtin_amdgcn_readfirstlane(q.begin);
+        end = __builtin_amdgcn_readfirstlane(q.end);
+    }
+    return e;
+}
+
 // The epilogue of one expert's rows, whose first is row `begin`.
 template <typename T>
 __device__ __forceinline__ Epilogue epilogue_of(const Epilogue& e, const Block& b, int n) {
@@ -101,10 +125,12 @@ __device__ __forceinline__ Epilogue epilogue_of(const Epilogue& e, const Block& 
     return r;
 }
 
-template <typename T, int TM, int TN, bool BKC, bool RAW>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ? 1 : 2, TM == 128 ? 1 : 2))) void
-k_grouped(const GroupedArgs p) {
-    __shared__ __attribute__((aligned(16))) char smem[GemmShape<T, TM, TN, true, BKC, RAW>::SMEM];
+// STAGES: buffers of the square tiles' rings. Two for 128 x 128, so that two
+// workgroups fit a CU, four for 64 x 64. KG: groups of waves that share the sum.
+template <typename T, int TM, int TN, int STAGES, int KG, bool BKC, bool RAW, int MODE>
+__global__ __launch_bounds__(256 * KG) __attribute__((amdgpu_waves_per_eu(KG > 2 ? KG : 2))) void k_grouped(
+    const GroupedArgs p) {
+    __shared__ __attribute__((aligned(16))) char smem[GemmShape<T, TM, TN, true, BKC, RAW, STAGES, KG>::SMEM];
     Block b;
     int tj = 0;
     const bool some = find_block<TM>(p, b, [&](int total) {
@@ -128,7 +154,7 @@ k_grouped(const GroupedArgs p) {
     g.K = p.K;
     g.slices = (p.K + BK - 1) / BK;
     g.epi = epilogue_of<T>(p.epi, b, p.N);
-    gemm_tile<T, TM, TN, true, BKC, 0, RAW>(g, smem, b.ti, tj, -1, 0, g.slices);
+    gemm_tile<T, TM, TN, true, BKC, 0, RAW, STAGES, KG, MODE>(g, smem, b.ti, tj, -1, 0, g.slices);
 }
 
 template <typename T, bool BKC, int MT>
@@ -159,14 +185,19 @@ __global__ __launch_bounds__(512) void k_grouped_few(const GroupedArgs p) {
     skinny_tile<T, BKC, MT>(g, smem, j0);
 }
 
-template <typename T, int TM, int TN, int SUM, bool RAW>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ? 1 : 2, TM == 128 ? 1 : 2))) void
-k_grouped_weight(const GroupedArgs p) {
-    __shared__ __attribute__((aligned(16))) char smem[GemmShape<T, TM, TN, false, false, RAW>::SMEM];
-    const int per = p.tiles_m * p.tiles_n;
-    const int l = per_xcd(blockIdx.x, gridDim.x), e = l / per;
-    const Group q = group_of(p.offsets, p.rows, e);
-    const int begin = __builtin_amdgcn_readfirstlane(q.begin), end = __builtin_amdgcn_readfirstlane(q.end);
+template <typename T, int TM, int TN, int STAGES, int KG, int SUM, bool RAW>
+__global__ __launch_bounds__(256 * KG) __attribute__((amdgpu_waves_per_eu(KG > 2 ? KG : 2))) void k_grouped_weight(
+    const GroupedArgs p) {
+    __shared__ __attribute__((aligned(16))) char smem[GemmShape<T, TM, TN, false, false, RAW, STAGES, KG>::SMEM];
+    // Each expert's tiles are shared by all XCDs, a contiguous run each, and the experts
+    // come by their rows, most first: their sums are unlike long, and one XCD with the
+    // longest, or a long one begun last, would keep the others waiting.
+    const int per = p.tiles_m * p.tiles_n, run = (per + 7) >> 3;
+    const int r = blockIdx.x / (8 * run), i = blockIdx.x - r * 8 * run;
+    const int l = ((i + r) & 7) * run + (i >> 3);
+    if (l >= per) return;
+    int begin, end;
+    const int e = ranked(p, r, begin, end);
     GemmArgs g{};
     g.a = static_cast<const T*>(p.a) + (int64_t)begin * p.ld_a;
     g.b = static_cast<const T*>(p.b) + (int64_t)begin * p.ld_b;
@@ -182,16 +213,31 @@ k_grouped_weight(const GroupedArgs p) {
     g.epi.y = static_cast<float*>(p.epi.y) + e * p.stride_w;
     if (SUM) g.sums = p.sums + (int64_t)e * (SUM == 1 ? p.N : p.M);
     int ti, tj;
-    tile_at(g, l - e * per, ti, tj);
-    gemm_tile<T, TM, TN, false, false, SUM, RAW>(g, smem, ti, tj, -1, 0, g.slices);
+    tile_at(g, l, ti, tj);
+    gemm_tile<T, TM, TN, false, false, SUM, RAW, STAGES, KG, EPI_GRAD_WEIGHT>(g, smem, ti, tj, -1, 0, g.slices);
 }
 
-template <typename T, int TM, int TN, bool RAW>
+template <typename T, int TM, int TN, int STAGES, int KG, bool RAW, int MODE>
 void rows_tile(const GroupedArgs& p, bool b_kc, unsigned grid, hipStream_t st) {
     if (b_kc)
-        k_grouped<T, TM, TN, true, RAW><<<grid, 256, 0, st>>>(p);
+        k_grouped<T, TM, TN, STAGES, KG, true, RAW, MODE><<<grid, 256 * KG, 0, st>>>(p);
     else
-        k_grouped<T, TM, TN, false, RAW><<<grid, 256, 0, st>>>(p);
+        k_grouped<T, TM, TN, STAGES, KG, false, RAW, MODE><<<grid, 256 * KG, 0, st>>>(p);
+}
+template <typename T, int MODE>
+void rows_mode(const GroupedArgs& p, TileKind tile, bool raw, bool b_kc, unsigned grid, hipStream_t st) {
+    if (raw)
+        rows_tile<T, 64, 64, 2, 1, true, MODE>(p, b_kc, grid, st);
+    else if (tile == TILE_TALL)
+        rows_tile<T, 256, 128, 2, 1, false, MODE>(p, b_kc, grid, st);
+    else if (tile == TILE_SQUARE)
+        rows_tile<T, 128, 128, 2, 1, false, MODE>(p, b_kc, grid, st);
+    else if (tile == TILE_SQUARE_GROUPS)
+        rows_tile<T, 128, 128, 2, 2, false, MODE>(p, b_kc, grid, st);
+    else if (tile == TILE_SMALL)
+        rows_tile<T, 64, 64, 4, 1, false, MODE>(p, b_kc, grid, st);
+    else
+        rows_tile<T, 64, 64, 4, 2, false, MODE>(p, b_kc, grid, st);
 }
 template <typename T, int MT>
 void few_tile(const GroupedArgs& p, bool b_kc, unsigned grid, hipStream_t st) {
@@ -201,52 +247,50 @@ void few_tile(const GroupedArgs& p, bool b_kc, unsigned grid, hipStream_t st) {
         k_grouped_few<T, false, MT><<<grid, 512, 0, st>>>(p);
 }
 template <typename T>
-hipError_t rows_t(const GroupedArgs& p, int tile, bool raw, bool b_kc, unsigned grid, hipStream_t st) {
-    if (tile == 16)
+hipError_t rows_t(const GroupedArgs& p, TileKind tile, bool raw, bool b_kc, unsigned grid, hipStream_t st) {
+    if (tile == TILE_FEW16)
         few_tile<T, 1>(p, b_kc, grid, st);
-    else if (tile == 32)
+    else if (tile == TILE_FEW32)
         few_tile<T, 2>(p, b_kc, grid, st);
-    else if (tile == 256)
-        rows_tile<T, 256, 128, false>(p, b_kc, grid, st);
-    else if (tile == 128)
-        rows_tile<T, 128, 128, false>(p, b_kc, grid, st);
-    else if (raw)
-        rows_tile<T, 64, 64, true>(p, b_kc, grid, st);
+    else if (p.epi.mode == EPI_FORWARD)
+        rows_mode<T, EPI_FORWARD>(p, tile, raw, b_kc, grid, st);
     else
-        rows_tile<T, 64, 64, false>(p, b_kc, grid, st);
+        rows_mode<T, EPI_GRAD_INPUT>(p, tile, raw, b_kc, grid, st);
     return hipGetLastError();
 }
 
-template <typename T, int TM, int TN, bool RAW>
+template <typename T, int TM, int TN, int STAGES, int KG, bool RAW>
 void weight_tile(const GroupedArgs& p, int sum, unsigned grid, hipStream_t st) {
     if (sum == 0)
-        k_grouped_weight<T, TM, TN, 0, RAW><<<grid, 256, 0, st>>>(p);
+        k_grouped_weight<T, TM, TN, STAGES, KG, 0, RAW><<<grid, 256 * KG, 0, st>>>(p);
     else if (sum == 1)
-        k_grouped_weight<T, TM, TN, 1, RAW><<<grid, 256, 0, st>>>(p);
+        k_grouped_weight<T, TM, TN, STAGES, KG, 1, RAW><<<grid, 256 * KG, 0, st>>>(p);
     else
-        k_grouped_weight<T, TM, TN, 2, RAW><<<grid, 256, 0, st>>>(p);
+        k_grouped_weight<T, TM, TN, STAGES, KG, 2, RAW><<<grid, 256 * KG, 0, st>>>(p);
 }
 template <typename T>
-hipError_t weight_t(const GroupedArgs& p, int tile, bool raw, int sum, unsigned grid, hipStream_t st) {
-    if (tile == 256)
-        weight_tile<T, 256, 128, false>(p, sum, grid, st);
-    else if (tile == 128)
-        weight_tile<T, 128, 128, false>(p, sum, grid, st);
-    else if (raw)
-        weight_tile<T, 64, 64, true>(p, sum, grid, st);
+hipError_t weight_t(const GroupedArgs& p, TileKind tile, bool raw, int sum, unsigned grid, hipStream_t st) {
+    if (raw)
+        weight_tile<T, 64, 64, 2, 1, true>(p, sum, grid, st);
+    else if (tile == TILE_TALL)
+        weight_tile<T, 256, 128, 2, 1, false>(p, sum, grid, st);
+    else if (tile == TILE_SQUARE)
+        weight_tile<T, 128, 128, 2, 1, false>(p, sum, grid, st);
+    else if (tile == TILE_SMALL)
+        weight_tile<T, 64, 64, 4, 1, false>(p, sum, grid, st);
     else
-        weight_tile<T, 64, 64, false>(p, sum, grid, st);
+        weight_tile<T, 64, 64, 2, 4, false>(p, sum, grid, st);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_grouped(const GroupedArgs& p, int tile, bool raw, bool b_kc, int dtype, unsigned grid,
+hipError_t launch_grouped(const GroupedArgs& p, TileKind tile, bool raw, bool b_kc, int dtype, unsigned grid,
                           hipStream_t st) {
     return dtype == 0 ? rows_t<bf16>(p, tile, raw, b_kc, grid, st) : rows_t<f16>(p, tile, raw, b_kc, grid, st);
 }
 
-hipError_t launch_grouped_weight(const GroupedArgs& p, int tile, bool raw, int dtype, int sum, unsigned grid,
+hipError_t launch_grouped_weight(const GroupedArgs& p, TileKind tile, bool raw, int dtype, int sum, unsigned grid,
                                  hipStream_t st) {
     return dtype == 0 ? weight_t<bf16>(p, tile, raw, sum, grid, st) : weight_t<f16>(p, tile, raw, sum, grid, st);
 }

@@ -42,19 +42,32 @@ __device__ __forceinline__ void clear_tail(char* S, int k, int tid) {
     }
 }
 
-template <typename T, int TM, int TN, int F>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TM == 128 ? 1 : 2, TM == 128 ? 1 : 2))) void
-k_scaled(const ScaledArgs p) {
+// 4 bytes per lane, global -> LDS: as load_lds.
+__device__ __forceinline__ void load_lds4(u32x4 r, uint32_t lds, uint32_t voff, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dword %0, %1, %2 offen lds"
+                 :
+                 : "v"(voff), "s"(r), "s"(soff), "s"(__builtin_amdgcn_readfirstlane(lds)));
+}
+
+// KG groups of 4 waves take the slices in turn, as in gemm_tile.
+template <typename T, int TM, int TN, int STAGES, int KG, int F, int MODE>
+__global__ __launch_bounds__(256 * KG) __attribute__((amdgpu_waves_per_eu(KG > 2 ? KG : 2))) void k_scaled(
+    const ScaledArgs p) {
     using OA = Operand<bf16, TM, true>;
     using OB = Operand<bf16, TN, true>;
     constexpr int WM = TM / 2, WN = TN / 2;   // a wave's block
     constexpr int FRI = WM / 16, FRJ = WN / 16;
     constexpr bool RING = TM <= 128;
-    constexpr int STAGE = OA::BYTES + OB::BYTES;
-    __shared__ __attribute__((aligned(16))) char smem[RING ? 4 * STAGE : OA::BYTES + STAGE];
+    // a ring's buffer: the slices of both operands, and each wave's scales of X's rows
+    constexpr int STAGE = OA::BYTES + OB::BYTES + (RING ? 1024 : 0);
+    constexpr int MEET = (4 * 32 * kStagedRow<WN> + 1023) / 1024 * 1024;  // the groups' sums, behind the staging
+    constexpr int SMEM = RING ? KG * STAGES * STAGE : OA::BYTES + STAGE;
+    static_assert(KG == 1 || (RING && MEET + (KG - 1) * TM * TN * 4 <= SMEM), "groups of waves");
+    __shared__ __attribute__((aligned(16))) char smem[SMEM];
     const GemmArgs& g = p.g;
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = KG > 1 ? threadIdx.x & 255 : threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int grp = KG > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8) : 0;
     const int wi = wave >> 1, wj = wave & 1;
     int ti, tj;
     tile_at(g, per_xcd(blockIdx.x, gridDim.x), ti, tj);
@@ -66,8 +79,8 @@ k_scaled(const ScaledArgs p) {
 
     OA A;
     OB B;
-    A.init(g.a, g.ld_a / 2, i0, g.M, kp, 0, kp, wave, lane, wi);
-    B.init(g.b, g.ld_b / 2, j0, g.N, kp, 0, kp, wave, lane, wj);
+    A.init(g.a, g.ld_a / 2, i0, g.M, kp, grp * BK, kp, wave, lane, wi);
+    B.init(g.b, g.ld_b / 2, j0, g.N, kp, grp * BK, kp, wave, lane, wj);
 
     f32x4 acc[FRI][FRJ];
 #pragma unroll
@@ -79,17 +92,21 @@ k_scaled(const ScaledArgs p) {
     // of columns
     const float* const sw = p.scale_w + (int64_t)(j0 >> 7) * nk;
     const int l16 = lane & 15, g16 = lane >> 4;
-    const int row = i0 + wi * WM + l16;
     float raw[FRI], sc[FRI];
+    // tall tile: to registers, a slice ahead, under the wait for the slice itself
     auto fetch_scales = [&](int kt) {
         const auto r = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<float*>(p.scale_x + (int64_t)(kt < nk ? kt : nk - 1) * g.M), 0, g.M * 4, 0x00020000);
 #pragma unroll
         for (int f = 0; f < FRI; ++f)
-            raw[f] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (row + 16 * f) * 4, 0, 0));
+            raw[f] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (i0 + wi * WM + l16 + 16 * f) * 4, 0, 0));
     };
+    // W's of 64 blocks at a time, one a lane (a scalar load for each slice is one
+    // latency for each slice)
+    float sw64 = sw[lane < nk ? lane : nk - 1];
     auto take_scales = [&](int kt) {
-        const float w = sw[kt < nk ? kt : nk - 1];
+        if (kt > 63 && (kt & 63) < KG) sw64 = sw[(kt & ~63) + lane < nk ? (kt & ~63) + lane : nk - 1];
+        const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw64), kt & 63));
 #pragma unroll
         for (int f = 0; f < FRI; ++f) sc[f] = raw[f] * w;
     };
@@ -134,7 +151,8 @@ k_scaled(const ScaledArgs p) {
             static_for<(PAIRS > DIST ? PAIRS - DIST : 0), PAIRS>([&](auto n_c) { collect(n_c); });
     };
 
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)smem;
+    char* const ring = smem + grp * STAGES * STAGE;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(LDS_AS char*)ring;
     if constexpr (!RING) {
         char* const SB = smem + 2 * OA::BYTES;
         fetch_scales(0);
@@ -180,40 +198,66 @@ k_scaled(const ScaledArgs p) {
             slice(kt, smem + o, smem + n, SB, lds0 + n);
         }
     } else {
-        constexpr int NLD = OA::NLD + OB::NLD;
-        fetch_scales(0);
-        take_scales(0);
+        // Scales go the way of the operands: into registers, the compiler's wait for
+        // them would be one for every load in flight (2048 x 6400 x 1600 43.7 us).
+        constexpr int NLD = OA::NLD + OB::NLD + 1;
+        const uint32_t at = lane < WM && i0 + wi * WM + lane < g.M ? 4u * (uint32_t)(i0 + wi * WM + lane) : OUT;
+        int next = grp;  // the next slice to load
+        auto load = [&](uint32_t buf) {
+            A.template load<KG>(buf);
+            B.template load<KG>(buf + OA::BYTES);
+            const float* s = p.scale_x + (int64_t)(next < nk ? next : nk - 1) * g.M;
+            load_lds4(rsrc(s, (uint32_t)g.M * 4u), buf + OA::BYTES + OB::BYTES + wave * 256, at, 0u);
+            next += KG;
+        };
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            A.load(lds0 + k * STAGE);
-            B.load(lds0 + k * STAGE + OA::BYTES);
-        }
-        for (int kt = 0; kt < nk; ++kt) {
-            char* const S = smem + (kt & 3) * STAGE;
-            wait_vm<2 * NLD>();  // this slice has landed
+        for (int k = 0; k < STAGES - 1; ++k) load(lds0 + k * STAGE);
+        const int turns = (nk + KG - 1) / KG;  // past the end, zeros are added
+        for (int t = 0; t < turns; ++t) {
+            const int kt = grp + KG * t;
+            char* const S = ring + (t & (STAGES - 1)) * STAGE;
+            wait_vm<(STAGES - 2) * NLD>();  // this slice has landed
             __syncthreads();
-            if (tail && kt + 1 == nk) {
-                clear_tail<TM>(S, g.K, tid);
-                clear_tail<TN>(S + OA::BYTES, g.K, tid);
+            if (tail && t + 1 == turns) {
+                if (kt + 1 == nk) {
+                    clear_tail<TM>(S, g.K, tid);
+                    clear_tail<TN>(S + OA::BYTES, g.K, tid);
+                }
                 __syncthreads();
             }
             // into the buffer of the slice before, which every wave had read
             // before the barrier
-            const uint32_t ldsF = lds0 + ((kt + 3) & 3) * STAGE;
-            fetch_scales(kt + 1);
-            A.load(ldsF);
-            B.load(ldsF + OA::BYTES);
+            load(lds0 + ((t - 1) & (STAGES - 1)) * STAGE);
             __builtin_amdgcn_sched_barrier(0);
             read_b(S + OA::BYTES);
             read_a(S, std::integral_constant<int, 0>{});
+            const float* own = reinterpret_cast<const float*>(S + OA::BYTES + OB::BYTES + wave * 256);
+#pragma unroll
+            for (int f = 0; f < FRI; ++f) raw[f] = own[16 * f + l16];
+            take_scales(kt);
             products(S, std::integral_constant<int, 0>{}, std::integral_constant<int, PAIRS>{});
-            take_scales(kt + 1);
         }
         wait_vm0();  // the loads past the end
     }
     __syncthreads();
+    if constexpr (KG > 1) {
+        auto place = [&](int group, int n) {
+            return reinterpret_cast<f32x4*>(smem + MEET + (((group - 1) * FRI * FRJ + n) * 256 + tid) * 16);
+        };
+        if (grp > 0) static_for<0, PAIRS>([&](auto n_c) {
+            constexpr int n = decltype(n_c)::value;
+            *place(grp, n) = acc[n / FRJ][n % FRJ];
+        });
+        __syncthreads();
+        if (grp > 0) return;
+        static_for<0, PAIRS>([&](auto n_c) {
+            constexpr int n = decltype(n_c)::value;
+#pragma unroll
+            for (int k = 1; k < KG; ++k) acc[n / FRJ][n % FRJ] += *place(k, n);
+        });
+    }
     // lane holds C[i][j .. j + 3] of a fragment, i = l16, j = 4 g16
-    tile_epilogue<T, TM, TN>(g, smem, i0, j0, -1, lane, wave, [&](auto f_c, char* W) {
+    whole_epilogue<MODE, T, TM, TN>(g, smem, i0, j0, lane, wave, [&](auto f_c, char* W) {
         constexpr int R = 2 * decltype(f_c)::value;
 #pragma unroll
         for (int a = 0; a < 2; ++a)
@@ -223,15 +267,9 @@ k_scaled(const ScaledArgs p) {
     });
 }
 
-// 4 bytes per lane, global -> LDS: as load_lds.
-__device__ __forceinline__ void load_lds4(u32x4 r, uint32_t lds, uint32_t voff, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dword %0, %1, %2 offen lds"
-                 :
-                 : "v"(voff), "s"(r), "s"(soff), "s"(__builtin_amdgcn_readfirstlane(lds)));
-}
-
-// Few rows of X (up to 16 MT tokens) against all of W, one launch: bound by reading W
-// once. A workgroup of 8 waves takes 16 columns and all of K; the waves take its
+// Few rows of X, in blocks of 16 MT, against all of W: bound by reading W once (a block
+// each, and it is in cache for the next one). A workgroup of 8 waves takes a block's 16
+// columns and all of K; the waves take its
 // blocks in turn, each through a ring of its own in LDS (a wave waits for its own
 // loads, X's scales among them). Their sums meet in LDS, in wave order.
 template <typename T, int MT, int F>
@@ -244,7 +282,10 @@ __global__ __launch_bounds__(512) void k_scaled_few(const ScaledArgs p) {
     const GemmArgs& g = p.g;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int j0 = per_xcd(blockIdx.x, gridDim.x) * 16;
+    // the row blocks of 16 columns follow one another, for the same XCD
+    const int l = per_xcd(blockIdx.x, gridDim.x);
+    const int j0 = l / g.tiles_m * 16, i0 = (l - l / g.tiles_m * g.tiles_m) * 16 * MT;
+    const int here = g.M - i0 < 16 * MT ? g.M - i0 : 16 * MT;  // rows
     const int kp = (g.K + 15) & ~15;
     char* const ring = smem + wave * R * STAGE;
     const uint32_t lring = (uint32_t)(uintptr_t)(LDS_AS char*)ring;
@@ -258,11 +299,10 @@ __global__ __launch_bounds__(512) void k_scaled_few(const ScaledArgs p) {
         offw[q] = r8 + 8 * q < rows ? (uint32_t)(r8 + 8 * q) * rowb + (uint32_t)c8 * 16u : OUT;
 #pragma unroll
     for (int q = 0; q < XB / 1024; ++q)
-        offx[q] = r8 + 8 * q < g.M ? (uint32_t)(r8 + 8 * q) * rowa + (uint32_t)c8 * 16u : OUT;
-    const uint32_t offs = lane < g.M && lane < 16 * MT ? 4u * (uint32_t)lane : OUT;
+        offx[q] = r8 + 8 * q < here ? (uint32_t)(r8 + 8 * q) * rowa + (uint32_t)c8 * 16u : OUT;
+    const uint32_t offs = lane < here ? 4u * (uint32_t)lane : OUT;
     const u32x4 rw = rsrc(static_cast<const char*>(g.b) + (int64_t)j0 * rowb, (uint32_t)(rows - 1) * rowb + (uint32_t)kp);
-    const u32x4 rx = rsrc(g.a, (uint32_t)(g.M - 1) * rowa + (uint32_t)kp);
-    const u32x4 rs = rsrc(p.scale_x, (uint32_t)g.M * 4u * (uint32_t)g.slices);
+    const u32x4 rx = rsrc(static_cast<const char*>(g.a) + (int64_t)i0 * rowa, (uint32_t)(here - 1) * rowa + (uint32_t)kp);
     const float* const sw = p.scale_w + (int64_t)(j0 >> 7) * g.slices;
     auto load = [&](int slice, uint32_t dst) {
         const int k0 = slice * 128;
@@ -271,8 +311,8 @@ __global__ __launch_bounds__(512) void k_scaled_few(const ScaledArgs p) {
         for (int q = 0; q < WB / 1024; ++q) load_lds(rw, dst + q * 1024, offw[q] | dead, so);
 #pragma unroll
         for (int q = 0; q < XB / 1024; ++q) load_lds(rx, dst + WB + q * 1024, offx[q] | dead, so);
-        const bool some = slice < g.slices;
-        load_lds4(rs, dst + WB + XB, some ? offs : OUT, some ? (uint32_t)(slice * g.M) * 4u : 0u);
+        const float* sx = p.scale_x + (int64_t)(slice < g.slices ? slice : g.slices - 1) * g.M + i0;
+        load_lds4(rsrc(sx, 4u * (uint32_t)here), dst + WB + XB, offs, 0u);
     };
     f32x4 acc[MT];
 #pragma unroll
@@ -284,10 +324,18 @@ __global__ __launch_bounds__(512) void k_scaled_few(const ScaledArgs p) {
         return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)up[0], (int)up[1], (int)up[2], (int)up[3]};
     };
     const int mine = (g.slices - wave + 7) / 8;  // slices wave, wave + 8, ...
+    int at = 0;
+    // W's scales of the wave's next 64 slices, one a lane, which come before its loads
+    auto scales64 = [&](int i) {
+        const int b = wave + 8 * (i + lane);
+        return sw[b < g.slices ? b : g.slices - 1];
+    };
+    float sw64 = scales64(0);
+    asm volatile("" : "+v"(sw64));
 #pragma unroll
     for (int k = 0; k < R - 1; ++k) load(wave + 8 * k, lring + k * STAGE);
-    int at = 0;
     for (int i = 0; i < mine; ++i) {
+        if ((i & 63) == 0 && i) sw64 = scales64(i);
         // the buffer read last turn takes the slice R - 1 ahead: its reads have
         // returned (their products were issued), and none moves across here
         int to = at + R - 1;
@@ -304,7 +352,7 @@ __global__ __launch_bounds__(512) void k_scaled_few(const ScaledArgs p) {
             const unsigned __int128 mask = ((unsigned __int128)1 << (8 * (g.K & 15))) - 1;
             *q = __builtin_bit_cast(u32x4, __builtin_bit_cast(unsigned __int128, *q) & mask);
         }
-        const float w = sw[slice];
+        const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sw64), i & 63));
         const i32x8 wf = frag(S);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -321,28 +369,39 @@ __global__ __launch_bounds__(512) void k_scaled_few(const ScaledArgs p) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) *reinterpret_cast<f32x4*>(own + (m * 16 + l16) * 16 + 4 * g16) = acc[m];
     __syncthreads();
-    few_epilogue<T, 16>(g.epi, g.M, g.N, smem, R * STAGE, j0);
+    few_epilogue<T, 16>(g.epi, i0, here, g.N, smem, R * STAGE, j0);
 }
 
-template <typename T, int F>
-hipError_t scaled_t(const ScaledArgs& p, int tile, hipStream_t st) {
-    const unsigned grid = (unsigned)(p.g.tiles_m * p.g.tiles_n);
-    if (tile == 0 && p.g.M <= 16)
-        k_scaled_few<T, 1, F><<<grid, 512, 0, st>>>(p);
-    else if (tile == 0)
-        k_scaled_few<T, 2, F><<<grid, 512, 0, st>>>(p);
-    else if (tile == 256)
-        k_scaled<T, 256, 128, F><<<grid, 256, 0, st>>>(p);
-    else if (tile == 128)
-        k_scaled<T, 128, 128, F><<<grid, 256, 0, st>>>(p);
+template <typename T, int F, int MODE>
+void scaled_tiles(const ScaledArgs& p, TileKind tile, unsigned grid, hipStream_t st) {
+    if (tile == TILE_TALL)
+        k_scaled<T, 256, 128, 2, 1, F, MODE><<<grid, 256, 0, st>>>(p);
+    else if (tile == TILE_SQUARE)
+        k_scaled<T, 128, 128, 2, 1, F, MODE><<<grid, 256, 0, st>>>(p);
+    else if (tile == TILE_SQUARE_GROUPS)
+        k_scaled<T, 128, 128, 2, 2, F, MODE><<<grid, 512, 0, st>>>(p);
+    else if (tile == TILE_SMALL)
+        k_scaled<T, 64, 64, 4, 1, F, MODE><<<grid, 256, 0, st>>>(p);
     else
-        k_scaled<T, 64, 64, F><<<grid, 256, 0, st>>>(p);
+        k_scaled<T, 64, 64, 2, 4, F, MODE><<<grid, 1024, 0, st>>>(p);
+}
+template <typename T, int F>
+hipError_t scaled_t(const ScaledArgs& p, TileKind tile, hipStream_t st) {
+    const unsigned grid = (unsigned)(p.g.tiles_m * p.g.tiles_n);
+    if (tile == TILE_FEW16)
+        k_scaled_few<T, 1, F><<<grid, 512, 0, st>>>(p);
+    else if (tile == TILE_FEW32)
+        k_scaled_few<T, 2, F><<<grid, 512, 0, st>>>(p);
+    else if (p.g.epi.mode == EPI_FORWARD)
+        scaled_tiles<T, F, EPI_FORWARD>(p, tile, grid, st);
+    else
+        scaled_tiles<T, F, EPI_GRAD_INPUT>(p, tile, grid, st);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_scaled(const ScaledArgs& p, int tile, int dtype, int format, hipStream_t st) {
+hipError_t launch_scaled(const ScaledArgs& p, TileKind tile, int dtype, int format, hipStream_t st) {
     if (dtype == 0)
         return format == EIGHT_E4M3 ? scaled_t<bf16, EIGHT_E4M3>(p, tile, st) : scaled_t<bf16, EIGHT_E5M2>(p, tile, st);
     return format == EIGHT_E4M3 ? scaled_t<f16, EIGHT_E4M3>(p, tile, st) : scaled_t<f16, EIGHT_E5M2>(p, tile, st);

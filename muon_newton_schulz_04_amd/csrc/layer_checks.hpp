@@ -167,5 +167,21 @@ inline Epilogue epilogue_args(bool fwd, const muon_epilogue& e, const Outputs& o
     return E;
 }
 
+// What a product takes on one kind of tile, in microseconds: all but its slices, a
+// slice's worth of a workgroup alone on its CU and of a CU that holds all it can, and
+// each further round of workgroups.
+struct TileCost {
+    TileKind kind;
+    int rows, cols;
+    double fixed, alone, beside, next;
+    int places;  // workgroups that the chip holds: 512, or 256 for those that fill their CU
+};
+
+inline double tile_price(const TileCost& c, double tiles, double slices) {
+    const double full = std::floor(tiles / c.places), rest = tiles - full * c.places;
+    const double more = rest > 256 ? c.alone + (c.beside - c.alone) * (rest - 256) / 256 : rest > 0 ? c.alone : 0;
+    return c.fixed + c.next * std::ceil(tiles / c.places - 1) + slices * (full * c.beside + more);
+}
+
 }  // namespace checks
 }  // namespace muon

@@ -173,12 +173,13 @@ __device__ __forceinline__ float act_slope(float z) {
     }
 }
 
-// One uniform branch for a chunk of 8, not one an element.
+// One uniform branch for all the values (8, a chunk, or more), not one an element.
 #define MUON_ACT_CASE(A, F)                                 \
     case A:                                                 \
-        _Pragma("unroll") for (int e = 0; e < 8; ++e) v[e] = F<A>(v[e]); \
+        _Pragma("unroll") for (int e = 0; e < N; ++e) v[e] = F<A>(v[e]); \
         break;
-__device__ __forceinline__ void act_values(int act, float (&v)[8]) {
+template <int N>
+__device__ __forceinline__ void act_values(int act, float (&v)[N]) {
     switch (act) {
         MUON_ACT_CASE(ACT_RELU, act_value)
         MUON_ACT_CASE(ACT_RELU2, act_value)
@@ -187,7 +188,8 @@ __device__ __forceinline__ void act_values(int act, float (&v)[8]) {
         MUON_ACT_CASE(ACT_SILU, act_value)
     }
 }
-__device__ __forceinline__ void act_slopes(int act, float (&v)[8]) {
+template <int N>
+__device__ __forceinline__ void act_slopes(int act, float (&v)[N]) {
     switch (act) {
         MUON_ACT_CASE(ACT_RELU, act_slope)
         MUON_ACT_CASE(ACT_RELU2, act_slope)

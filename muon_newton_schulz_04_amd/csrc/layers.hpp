@@ -110,6 +110,12 @@ struct NormSums {
     int32_t cols, blocks, accumulate;
 };
 
+// The tiles of the 8-bit and the grouped products: 256 x 128, 128 x 128 and 64 x 64, the
+// latter two also with groups of waves that share a tile's sum (two; four for the 8-bit
+// product's and the weight gradient's 64 x 64), and blocks of 16 or 32 rows of the
+// kernels for few rows.
+enum TileKind { TILE_TALL, TILE_SQUARE, TILE_SQUARE_GROUPS, TILE_SMALL, TILE_SMALL_GROUPS, TILE_FEW16, TILE_FEW32 };
+
 // A linear layer of each of `experts` over rows grouped by expert. Forward and input
 // gradient: A [rows, K] k-contiguous, B an expert's weight; weight gradient: A
 // [rows, M], B [rows, N], the sum over the expert's rows.
@@ -124,11 +130,9 @@ struct GroupedArgs {
     int32_t tiles_m, tiles_n;  // of an expert's output (tiles_m: weight gradient)
     Epilogue epi;
 };
-// tile: rows of a tile (256 x 128, 128 x 128, 64 x 64), or of a block of the kernel for
-// few rows (16, 32)
-hipError_t launch_grouped(const GroupedArgs& p, int tile, bool raw, bool b_kc, int dtype, unsigned grid,
+hipError_t launch_grouped(const GroupedArgs& p, TileKind tile, bool raw, bool b_kc, int dtype, unsigned grid,
                           hipStream_t st);
-hipError_t launch_grouped_weight(const GroupedArgs& p, int tile, bool raw, int dtype, int sum, unsigned grid,
+hipError_t launch_grouped_weight(const GroupedArgs& p, TileKind tile, bool raw, int dtype, int sum, unsigned grid,
                                  hipStream_t st);
 
 // 8-bit floating point with a float32 scale for each block of 128: what a format's
@@ -199,9 +203,7 @@ struct ScaledArgs {
     const float* scale_x;  // [slices][M]
     const float* scale_w;  // [N's blocks][slices]
 };
-// tile: rows of a tile (256 x 128, 128 x 128, 64 x 64), or 0 for up to kSkinnyRows rows
-// against columns in groups of 16
-hipError_t launch_scaled(const ScaledArgs& p, int tile, int dtype, int format, hipStream_t st);
+hipError_t launch_scaled(const ScaledArgs& p, TileKind tile, int dtype, int format, hipStream_t st);
 
 int norm_backward_blocks(int64_t rows, int64_t cols, int dtype);
 hipError_t launch_norm_forward(const NormForward& n, int dtype, hipStream_t st);

@@ -50,22 +50,69 @@ Tensor rows_of(const muon_grouped& d, const void* p, int64_t cols, int64_t ld) {
 // them through registers.
 bool whole_chunks(const void* p, int64_t ld, int64_t cols) { return aligned16(p, ld, 2) && cols % 8 == 0; }
 
-// rows of a tile for `rows` rows of `experts` groups
-int rows_tile(int64_t rows, int64_t experts, int64_t N) {
-    const int64_t each = (rows + experts - 1) / experts;
-    if (rows <= 16) return 16;
-    if (each <= 16) return 32;
-    const int64_t cols = (N + 127) / 128;
-    if (each >= 384 && rows / 256 * cols >= 400) return 256;
-    if (each >= 96 && rows / 128 * cols >= 200) return 128;
-    return 64;
+// The tiles of the forward pass and the input gradient, by prices fitted to times
+// measured over 24 shapes and every tile (rows, experts, in, out; bf16, us, small, small
+// in groups, square, square in groups, tall): 48, 16, 768, 1536 8.9, 11.8, 13.0, 12.0,
+// 17.5; 2, 16, 6400, 1600 29, 21, 64, 47, 84 (blocks of 16 rows 13.2); 4099, 8, 1536,
+// 768 25, 31, 22, 19, 28; 4096, 8, 1600, 1600 45, 59, 28, 38, 30; 32768, 16, 1600, 1600
+// 301, 381, 184, 253, 161.
+constexpr TileCost kRowTiles[] = {{muon::TILE_TALL, 256, 128, 6.0, 0.82, 1.65, 5.0, 512},
+                                  {muon::TILE_SQUARE, 128, 128, 5.0, 0.65, 0.95, 3.0, 512},
+                                  {muon::TILE_SQUARE_GROUPS, 128, 128, 5.5, 0.52, 0.75, 3.0, 256},
+                                  {muon::TILE_SMALL, 64, 64, 4.0, 0.26, 0.48, 1.0, 512},
+                                  {muon::TILE_SMALL_GROUPS, 64, 64, 5.0, 0.18, 0.33, 2.0, 256}};
+// The weight gradient's (32768, 16, 1600, 1600 in 351, -, 253, -, 227; 4099, 8, 1536, 768
+// 39, -, 31, -, 40).
+constexpr TileCost kWeightTiles[] = {{muon::TILE_TALL, 256, 128, 8.0, 1.0, 2.0, 8.0, 512},
+                                     {muon::TILE_SQUARE, 128, 128, 6.5, 0.7, 1.1, 5.0, 512},
+                                     {muon::TILE_SMALL, 64, 64, 4.5, 0.28, 0.55, 2.0, 512},
+                                     {muon::TILE_SMALL_GROUPS, 64, 64, 6.5, 0.1, 0.16, 4.0, 256}};
+
+int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct GroupedPlan {
+    muon::TileKind tile;
+    int rows, cols;
+};
+
+// How many blocks of `tall` rows the groups are, as far as the host can tell: half a
+// block more for each group that has rows.
+double expected_blocks(int64_t rows, int64_t experts, int64_t tall) {
+    const double some = (double)(rows < experts ? rows : experts), n = (double)rows / (double)tall + 0.5 * some;
+    return std::ceil(n > some ? n : some);
 }
 
-int weight_tile(int64_t rows, int64_t experts, int64_t M, int64_t N) {
-    const int64_t cols = (N + 127) / 128;
-    if (experts * ((M + 255) / 256) * cols >= 400 && M > 128) return 256;
-    if (experts * ((M + 127) / 128) * cols >= 200) return 128;
-    return 64;
+GroupedPlan rows_plan(int64_t rows, int64_t experts, int64_t N, int64_t K, bool b_kc) {
+    const double slices = (double)up_div(K, muon::kGemmSlice);
+    GroupedPlan best{};
+    double least = 1e300;
+    for (const TileCost& c : kRowTiles) {
+        const double t = tile_price(c, expected_blocks(rows, experts, c.rows) * (double)up_div(N, c.cols), slices);
+        if (t >= least) continue;
+        least = t;
+        best = {c.kind, c.rows, c.cols};
+    }
+    // blocks of few rows: rounds of 256 workgroups, each a wait of its own
+    const bool one = rows <= 16 * experts;
+    const int cols = b_kc ? 16 : 32, tall = one ? 16 : 32;
+    const double wgs = expected_blocks(rows, experts, tall) * (double)up_div(N, cols);
+    const double t = 4.0 + std::ceil(wgs / 256) * (b_kc ? 2.2 + 0.038 * slices : 2.6 + 0.08 * slices);
+    if (t < least) best = {one ? muon::TILE_FEW16 : muon::TILE_FEW32, tall, cols};
+    return best;
+}
+
+GroupedPlan weight_plan(int64_t rows, int64_t experts, int64_t M, int64_t N) {
+    // the longest of the sums, where some experts have half as much again as the mean
+    const double slices = 1.0 + 1.5 * (double)rows / (double)experts / muon::kGemmSlice;
+    GroupedPlan best{};
+    double least = 1e300;
+    for (const TileCost& c : kWeightTiles) {
+        const double t = tile_price(c, (double)(experts * up_div(M, c.rows) * up_div(N, c.cols)), slices);
+        if (t >= least) continue;
+        least = t;
+        best = {c.kind, c.rows, c.cols};
+    }
+    return best;
 }
 
 muon_status too_large() { return fail(MUON_E_SHAPE, "grouped linear: output too large"); }
@@ -97,8 +144,7 @@ muon_status run_grouped(const muon_grouped* d, bool fwd, const void* a, const vo
     const int64_t wc = d->weight_layout == MUON_WEIGHT_IN_OUT ? d->out_features : d->in_features;
     const int64_t ld_w = stride_of(d->ld_w, wc), step = weight_step(*d);
     const bool raw = !whole_chunks(a, A.ld, K) || !whole_chunks(w, ld_w, wc) || step % 8 != 0;
-    const int tile = raw ? 64 : rows_tile(d->rows, d->experts, N);
-    const int tile_n = tile <= 32 ? (b_kc ? 16 : 32) : tile == 64 ? 64 : 128;
+    const GroupedPlan plan = raw ? GroupedPlan{muon::TILE_SMALL, 64, 64} : rows_plan(d->rows, d->experts, N, K, b_kc);
     muon::GroupedArgs p{};
     p.a = a;
     p.b = w;
@@ -110,13 +156,15 @@ muon_status run_grouped(const muon_grouped* d, bool fwd, const void* a, const vo
     p.experts = (int)d->experts;
     p.N = (int)N;
     p.K = (int)K;
-    p.tiles_n = (int)((N + tile_n - 1) / tile_n);
+    p.tiles_n = (int)up_div(N, plan.cols);
     p.epi = epilogue_args(fwd, *e, o);
     // every expert with rows may end inside a tile
-    const int64_t most = (d->rows < d->experts ? d->rows : d->experts) + d->rows / tile, grid = most * p.tiles_n;
+    const int64_t most = (d->rows < d->experts ? d->rows : d->experts) + d->rows / plan.rows;
+    const int64_t grid = most * p.tiles_n;
     if (grid >= (int64_t)1 << 22) return too_large();
     TRY(check_device());
-    return hip_status(muon::launch_grouped(p, tile, raw, b_kc, d->dtype, (unsigned)grid, static_cast<hipStream_t>(stream)),
+    return hip_status(muon::launch_grouped(p, plan.tile, raw, b_kc, d->dtype, (unsigned)grid,
+                                           static_cast<hipStream_t>(stream)),
                       "grouped product kernel");
 }
 
@@ -153,8 +201,7 @@ muon_status muon_grouped_linear_grad_weight(const muon_grouped* d, const void* x
         TRY(check_disjoint(Bi, {X, Y, Of}));
         const Tensor &A = io ? X : Y, &B = io ? Y : X;
         const bool raw = d->rows > 0 && (!whole_chunks(A.p, A.ld, A.cols) || !whole_chunks(B.p, B.ld, B.cols));
-        const int tile = raw ? 64 : weight_tile(d->rows, d->experts, A.cols, B.cols);
-        const int tile_n = tile == 64 ? 64 : 128;
+        const GroupedPlan plan = raw ? GroupedPlan{muon::TILE_SMALL, 64, 64} : weight_plan(d->rows, d->experts, A.cols, B.cols);
         muon::GroupedArgs p{};
         p.a = A.p;
         p.b = B.p;
@@ -167,18 +214,19 @@ muon_status muon_grouped_linear_grad_weight(const muon_grouped* d, const void* x
         p.experts = (int)d->experts;
         p.M = (int)A.cols;
         p.N = (int)B.cols;
-        p.tiles_m = (int)((A.cols + tile - 1) / tile);
-        p.tiles_n = (int)((B.cols + tile_n - 1) / tile_n);
+        p.tiles_m = (int)up_div(A.cols, plan.rows);
+        p.tiles_n = (int)up_div(B.cols, plan.cols);
         p.epi.mode = muon::EPI_GRAD_WEIGHT;
         p.epi.y = dw;
         p.epi.ld_y = (int)stride_of(d->ld_w, io ? d->out_features : d->in_features);
         p.epi.accumulate = accumulate != 0;
-        const int64_t grid = d->experts * p.tiles_m * p.tiles_n;
+        // an expert's tiles in runs of one length for each of the 8 XCDs
+        const int64_t grid = d->experts * (((int64_t)p.tiles_m * p.tiles_n + 7) / 8 * 8);
         if (grid >= (int64_t)1 << 22) return too_large();
         TRY(check_device());
         // dy is the second operand of an [in, out] gradient, else the first
         const int sum = !dbias ? 0 : io ? 1 : 2;
-        return hip_status(muon::launch_grouped_weight(p, tile, raw, d->dtype, sum, (unsigned)grid,
+        return hip_status(muon::launch_grouped_weight(p, plan.tile, raw, d->dtype, sum, (unsigned)grid,
                                                       static_cast<hipStream_t>(stream)),
                           "grouped weight gradient kernel");
     });

@@ -61,11 +61,35 @@ size_t rms_workspace(const muon_rmsnorm& d) {
     return up256((size_t)muon::rms_backward_blocks(d.rows, d.cols, d.dtype) * (size_t)d.cols * 4);
 }
 
-// How an 8-bit product is cut: rows of its tile, 0 for the kernel for few rows.
-int scaled_tile(int64_t M, int64_t N) {
-    if (M <= muon::kSkinnyRows) return 0;
-    const int64_t tall = ((M + 255) / 256) * ((N + 127) / 128), square = ((M + 127) / 128) * ((N + 127) / 128);
-    return tall >= 384 ? 256 : square >= 200 ? 128 : 64;
+// The tile of an 8-bit product, by prices fitted to times measured over 22 shapes and
+// every tile (bf16 output; us, small, small in groups, square, square in groups, tall):
+// 512 x 6400 x 1600 32, 19, 54, 39, 60; 1024 x 1600 x 1600 10.9, 14.5, 14.4, 13.4, 21.7;
+// 2048 x 6400 x 1600 64, 68, 54, 39, 60; 4096 x 1600 x 1600 31, 44, 18.4, 26, 22; 4096 x
+// 1600 x 6400 123, 173, 70, 92, 59.
+constexpr TileCost kScaledTiles[] = {{muon::TILE_TALL, 256, 128, 6.0, 1.15, 2.3, 5.0, 512},
+                                     {muon::TILE_SQUARE, 128, 128, 5.5, 0.8, 1.15, 3.0, 512},
+                                     {muon::TILE_SQUARE_GROUPS, 128, 128, 6.0, 0.62, 1.0, 3.0, 256},
+                                     {muon::TILE_SMALL, 64, 64, 4.5, 0.42, 0.55, 1.0, 512},
+                                     {muon::TILE_SMALL_GROUPS, 64, 64, 6.0, 0.23, 0.33, 2.0, 256}};
+
+struct ScaledPlan {
+    muon::TileKind tile;
+    int64_t tiles_m, tiles_n;
+};
+ScaledPlan scaled_plan(int64_t M, int64_t N, int64_t K) {
+    if (M <= 16) return {muon::TILE_FEW16, 1, (N + 15) / 16};
+    const int64_t blocks = (M + 31) / 32, few = blocks * ((N + 15) / 16);
+    if (blocks == 1 || few <= 256) return {muon::TILE_FEW32, blocks, (N + 15) / 16};
+    ScaledPlan best{};
+    double least = 1e300;
+    for (const TileCost& c : kScaledTiles) {
+        const int64_t m = (M + c.rows - 1) / c.rows, n = (N + c.cols - 1) / c.cols;
+        const double t = tile_price(c, (double)(m * n), (double)blocks_of(K));
+        if (t >= least) continue;
+        least = t;
+        best = {c.kind, m, n};
+    }
+    return best;
 }
 
 // forward (X [tokens, in], W [out, in]) and grad input (dY [tokens, out], W [in, out])
@@ -107,7 +131,7 @@ muon_status run_scaled(const muon_linear* d, bool fwd, const muon_eight* a, cons
     TRY(check_add(Y, R));
     if (fwd) TRY(check_disjoint(Z, {A, SA, W, SW, R, Bi}));
     TRY(check_device());
-    const int tile = scaled_tile(M, N);
+    const ScaledPlan plan = scaled_plan(M, N, K);
     muon::ScaledArgs p{};
     muon::GemmArgs& g = p.g;
     g.a = a->data;
@@ -117,14 +141,13 @@ muon_status run_scaled(const muon_linear* d, bool fwd, const muon_eight* a, cons
     g.M = (int)M;
     g.N = (int)N;
     g.K = (int)K;
-    g.tiles_m = tile ? (int)((M + tile - 1) / tile) : 1;
-    const int tile_n = tile == 0 ? 16 : tile == 64 ? 64 : 128;
-    g.tiles_n = (int)((N + tile_n - 1) / tile_n);
+    g.tiles_m = (int)plan.tiles_m;
+    g.tiles_n = (int)plan.tiles_n;
     g.slices = (int)blocks_of(K);
     g.epi = epilogue_args(fwd, *e, o);
     p.scale_x = a->scale;
     p.scale_w = w->scale;
-    return hip_status(muon::launch_scaled(p, tile, d->dtype, a->format, static_cast<hipStream_t>(stream)),
+    return hip_status(muon::launch_scaled(p, plan.tile, d->dtype, a->format, static_cast<hipStream_t>(stream)),
                       "8-bit product kernel");
 }
 
