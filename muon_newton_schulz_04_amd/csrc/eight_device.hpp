@@ -67,20 +67,21 @@ struct NearScale : BlockScale<F> {
     __device__ __forceinline__ float operator()(float v) const { return v * inv; }
 };
 
-// v kLargest / amax rounded once: 16-bit values divided by one another often
-// fall on the border between two 8-bit values, where an error of the quotient's
-// last bit takes the wrong one. kLargest is 7/8 of a power of two: a = 7 v / 8 is
-// exact for 16-bit v, t = a / amax is corrected by its exact remainder, and the
-// power of two is exact again.
-template <int F>
+// v kLargest / amax rounded once: values divided by one another often fall on the
+// border between two 8-bit values, where an error of the quotient's last bit takes the
+// wrong one. kLargest is 7/8 of a power of two: a = 7 v / 8, exact for 16-bit v and
+// with the rest of its rounding in `low` for 32-bit ones (WIDE), t = a / amax is
+// corrected by its exact remainder, and the power of two is exact again.
+template <int F, bool WIDE>
 struct ExactScale : BlockScale<F> {
     float rcp;
     __device__ __forceinline__ explicit ExactScale(uint32_t bits) : BlockScale<F>(bits) { rcp = 1.f / this->amax; }
     __device__ __forceinline__ float operator()(float v) const {
         constexpr float P = F == EIGHT_E4M3 ? 512.f : 65536.f;
-        const float a = 0.875f * v;
-        const float t = a * rcp;
-        return fmaf(fmaf(-t, this->amax, a), rcp, t) * P;
+        const float a = 0.875f * v, t = a * rcp;
+        float rest = fmaf(-t, this->amax, a);
+        if constexpr (WIDE) rest += fmaf(0.875f, v, -a);
+        return fmaf(rest, rcp, t) * P;
     }
 };
 

@@ -16,6 +16,8 @@ namespace muon {
 
 namespace {
 
+// (Four segments a wave, their loads all on the way before the first is used: 2051 x 6400
+// bf16 11.3 us, against 9.3.)
 template <typename T, int F>
 __global__ __launch_bounds__(256) void k_quantize(const Quantize a) {
     const int lane = threadIdx.x & 63;
@@ -29,7 +31,7 @@ __global__ __launch_bounds__(256) void k_quantize(const Quantize a) {
     uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) m = umax(m, magnitude(v[e]));
-    const ExactScale<F> s(max16(m));
+    const ExactScale<F, sizeof(T) == 4> s(max16(m));
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = e < left ? s(v[e]) : 0.f;
     // rows go on with zeros to the next multiple of 16
@@ -61,7 +63,7 @@ __global__ __launch_bounds__(256) void k_quantize_weight(const QuantizeWeight a)
     m = umax(m, (uint32_t)__shfl_xor((int)m, 32, 64));
     if ((tid & 63) == 0) red[tid >> 6] = m;
     __syncthreads();
-    const ExactScale<F> s(umax(umax(red[0], red[1]), umax(red[2], red[3])));
+    const ExactScale<F, sizeof(T) == 4> s(umax(umax(red[0], red[1]), umax(red[2], red[3])));
     // values past an edge are 0, and stay 0 beside a NaN
 #pragma unroll
     for (int j = 0; j < 8; ++j)
