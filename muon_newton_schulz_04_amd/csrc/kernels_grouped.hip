@@ -65,7 +65,10 @@ __device__ __forceinline__ bool find_block(const GroupedArgs& p, Block& out, F&&
         const int e = e0 + lane;
         q = e < p.experts ? group_of(p.offsets, p.rows, e) : Group{0, 0};
         run = wave_prefix((q.end - q.begin + TM - 1) / TM);
+        // offsets that repeat rows may count more blocks than there are workgroups for, and
+        // their sum would pass 32 bits
         total += __builtin_amdgcn_readlane(run, 63);
+        total = total < p.tiles_m ? total : p.tiles_m;
     }
     int t = at(total);
     if (t < 0) return false;

@@ -127,7 +127,7 @@ struct GroupedArgs {
     float* sums;             // bias gradients [experts][], or null
     int32_t ld_a, ld_b;
     int32_t rows, experts, M, N, K;
-    int32_t tiles_m, tiles_n;  // of an expert's output (tiles_m: weight gradient)
+    int32_t tiles_m, tiles_n;  // of an expert's output; tiles_m of rows: the most blocks of all experts
     Epilogue epi;
 };
 hipError_t launch_grouped(const GroupedArgs& p, TileKind tile, bool raw, bool b_kc, int dtype, unsigned grid,

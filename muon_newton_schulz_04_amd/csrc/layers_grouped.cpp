@@ -162,6 +162,7 @@ muon_status run_grouped(const muon_grouped* d, bool fwd, const void* a, const vo
     const int64_t most = (d->rows < d->experts ? d->rows : d->experts) + d->rows / plan.rows;
     const int64_t grid = most * p.tiles_n;
     if (grid >= (int64_t)1 << 22) return too_large();
+    p.tiles_m = (int)most;
     TRY(check_device());
     return hip_status(muon::launch_grouped(p, plan.tile, raw, b_kc, d->dtype, (unsigned)grid,
                                            static_cast<hipStream_t>(stream)),

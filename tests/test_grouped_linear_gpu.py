@@ -145,6 +145,22 @@ def test_offsets_of_any_value_stay_inside():
             close(y[10:20], a @ b, sum_tol(a, b), t)
 
 
+def test_offsets_that_repeat_all_rows():
+    """Every other of 65536 experts claims all 2^20 rows: blocks of 16 rows for them
+    number 2^31, more than 32 bits hold, and the grid has workgroups for 2^17. Nothing
+    beside the tensors is written, and the call ends."""
+    t = torch.bfloat16
+    e, n, i, o = 65536, 1 << 20, 8, 8
+    off = torch.zeros(e + 1, dtype=torch.int32, device="cuda")
+    off[1::2] = n
+    x = torch.ones(n, i, dtype=t, device="cuda")
+    w = torch.ones(e, i, o, dtype=t, device="cuda")
+    buf = torch.full((n + 16, o), 7.0, dtype=t, device="cuda")
+    L.grouped_linear_forward(x, w, off, out=buf[8:8 + n])
+    assert (buf[:8] == 7).all() and (buf[8 + n:] == 7).all()
+    assert ((buf[8:8 + n] == 8) | (buf[8:8 + n] == 7)).all() and (buf[8] == 8).all()
+
+
 def test_no_rows():
     w = torch.zeros(3, 16, 24, dtype=torch.bfloat16, device="cuda")
     off = torch.zeros(4, dtype=torch.int32, device="cuda")
