@@ -58,15 +58,6 @@ __device__ __forceinline__ u32x2 pack8(const float (&v)[8]) {
     return u32x2{pack4<F>(v[0], v[1], v[2], v[3]), pack4<F>(v[4], v[5], v[6], v[7])};
 }
 
-// v / scale to within float32's rounding of v times the reciprocal: for values
-// that are themselves sums of float32 roundings.
-template <int F>
-struct NearScale : BlockScale<F> {
-    float inv;
-    __device__ __forceinline__ explicit NearScale(uint32_t bits) : BlockScale<F>(bits) { inv = kLargest<F> / this->amax; }
-    __device__ __forceinline__ float operator()(float v) const { return v * inv; }
-};
-
 // v kLargest / amax rounded once: values divided by one another often fall on the
 // border between two 8-bit values, where an error of the quotient's last bit takes the
 // wrong one. kLargest is 7/8 of a power of two: a = 7 v / 8, exact for 16-bit v and

@@ -17,6 +17,12 @@
 //  * The weight's gradient: each wave keeps the sums of dy xhat of its own columns
 //    in registers over all the rows it goes through, a workgroup writes one
 //    partial row, and a second kernel adds the partial rows in order.
+//
+// Measured, inputs in turn that no cache holds (a copy of 2 GiB reaches 4.9 TB/s on the
+// same box): 16384 x 1600 bf16, residual, 8-bit output 37.4 us a call (184 MB, 4.9 TB/s);
+// its backward with the residual's gradient 45 (210 MB; the pass 40, the join of 768
+// partial rows 4). One row takes 4 us, the call 13 on the host. Nontemporal
+// loads of x and the residual: no difference.
 
 #include "eight_device.hpp"
 #include "norm_device.hpp"
@@ -25,7 +31,8 @@ namespace muon {
 
 namespace {
 
-constexpr int kBlockCols = 8192;  // longest rows that live in registers
+// The longest rows that live in registers: 32 elements a lane of 4 waves.
+constexpr int kBlockCols = 8192;
 
 // What a lane does with its chunk of 8 outputs t from column c on, `left` of which
 // exist (the others are 0): y, and the 8-bit form with its scale. All 16 lanes of
@@ -37,7 +44,9 @@ __device__ __forceinline__ void emit(const RmsForward& n, int64_t row, int c, in
         uint32_t m = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = umax(m, magnitude(t[e]));
-        const NearScale<F> s(max16(m));
+        // (times a rounded reciprocal 36.4 us, not 37.4, and twice as many of 16384 x 1600
+        // values, 3 or 4, on the other side of a border between two 8-bit values)
+        const ExactScale<F, true> s(max16(m));
         // rows go on with zeros to the next multiple of 16
         if (left > -8 && (left > 0 || (c & 8))) {
             float u[8];
@@ -444,10 +453,15 @@ hipError_t backward_t(const RmsBackward& n, hipStream_t st) {
 
 }  // namespace
 
+// Workgroups of the backward pass, each with a partial row: two or three a CU, and at
+// least 8 rows each, so that a row's next one is on the way while it is summed. A call in
+// us, in 256, 512, 768 and 1024 workgroups: 16384 x 1600 bf16 66, 49, 45, 46; 16384 x
+// 1001 bf16 75, 47, 40, 51; 16384 x 1600 float32 90, 80, 84, 91; 8192 x 6400 bf16 (8 waves
+// a workgroup) 95, 83, 95, 89.
 int rms_backward_blocks(int64_t rows, int64_t cols, int dtype) {
     if (rows == 0) return 0;
     const int64_t b = cols <= kBlockCols ? rows / 8 : rows / 64;
-    const int64_t most = cols > kBlockCols ? 64 : cols > 4096 ? 256 : dtype != 2 && cols % 8 == 0 ? 768 : 512;
+    const int64_t most = cols > kBlockCols ? 64 : cols > 4096 || dtype == 2 ? 512 : 768;
     return (int)(b < 1 ? 1 : b < most ? b : most);
 }
 
