@@ -495,12 +495,18 @@ muon_status muon_grouped_linear_forward(const muon_grouped* d, const void* x, co
 muon_status muon_grouped_linear_grad_input(const muon_grouped* d, const void* dy, const void* w,
                                            const int32_t* offsets, const muon_epilogue* e, void* dx, void* stream);
 
+/* Bytes of device workspace (256-byte aligned) that the weight gradient needs: often 0,
+ * and NULL is then accepted; where few experts of few features have many rows, room for
+ * the sums of pieces of them. Of x and dy only the alignment is looked at. Host-only. */
+muon_status muon_grouped_linear_workspace_bytes(const muon_grouped* d, const void* x, const void* dy,
+                                                size_t* out_bytes);
+
 /* dW_e (+)= the product of X and dY over the expert's rows, float32, and dbias_e (+)=
  * the sum of dY over them, or NULL: zeros (or unchanged, when accumulating) for an
  * expert without rows. */
 muon_status muon_grouped_linear_grad_weight(const muon_grouped* d, const void* x, const void* dy,
                                             const int32_t* offsets, float* dw, float* dbias, int32_t accumulate,
-                                            void* stream);
+                                            void* workspace, size_t ws_bytes, void* stream);
 
 /* Detail of the last failed layer operator call on this thread ("" if none). */
 const char* muon_op_last_error(void);

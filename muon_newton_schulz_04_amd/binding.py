@@ -257,8 +257,10 @@ _SIGS = {
                                                    ctypes.POINTER(muon_epilogue), _P, _P]),
     "muon_grouped_linear_grad_input": (ctypes.c_int, [ctypes.POINTER(muon_grouped), _P, _P, _P,
                                                       ctypes.POINTER(muon_epilogue), _P, _P]),
+    "muon_grouped_linear_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(muon_grouped), _P, _P,
+                                                           ctypes.POINTER(ctypes.c_size_t)]),
     "muon_grouped_linear_grad_weight": (ctypes.c_int, [ctypes.POINTER(muon_grouped), _P, _P, _P, _P, _P,
-                                                       ctypes.c_int32, _P]),
+                                                       ctypes.c_int32, _P, ctypes.c_size_t, _P]),
     "muon_op_last_error": (ctypes.c_char_p, []),
     "muon_lr_wsd": (ctypes.c_float, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
     "muon_lr_cooldown_floor": (ctypes.c_float, [ctypes.c_int64, ctypes.c_int64, ctypes.c_float, ctypes.c_float]),
@@ -492,10 +494,17 @@ def muon_grouped_linear_grad_input(d: muon_grouped, dy_ptr: int, w_ptr: int, off
     return load().muon_grouped_linear_grad_input(d, dy_ptr, w_ptr, offsets_ptr, e, dx_ptr, stream_ptr)
 
 
+def muon_grouped_linear_workspace_bytes(d: muon_grouped, x_ptr: int, dy_ptr: int) -> tuple:
+    out = ctypes.c_size_t(0)
+    s = load().muon_grouped_linear_workspace_bytes(d, x_ptr, dy_ptr, out)
+    return s, out.value
+
+
 def muon_grouped_linear_grad_weight(d: muon_grouped, x_ptr: int, dy_ptr: int, offsets_ptr: int, dw_ptr: int,
-                                    dbias_ptr: int, accumulate: int, stream_ptr: int) -> int:
+                                    dbias_ptr: int, accumulate: int, workspace_ptr: int, ws_bytes: int,
+                                    stream_ptr: int) -> int:
     return load().muon_grouped_linear_grad_weight(d, x_ptr, dy_ptr, offsets_ptr, dw_ptr, dbias_ptr, accumulate,
-                                                  stream_ptr)
+                                                  workspace_ptr, ws_bytes, stream_ptr)
 
 
 def muon_op_last_error() -> str:

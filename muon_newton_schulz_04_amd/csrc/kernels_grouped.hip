@@ -15,7 +15,17 @@
 //    Few rows an expert go through the kernel for few rows, whose list is of blocks
 //    of 16 or 32 rows.
 //  * Weight gradient: an expert's rows are the sum's index; an expert without rows
-//    gets zeros (or keeps what it has, when accumulating).
+//    gets zeros (or keeps what it has, when accumulating). Few tiles of long sums are
+//    cut into pieces of the experts' rows, whose sums a second kernel adds in order
+//    (32768 rows of 2 experts, 2048 -> 800: 270 us whole in the best of the tiles, 167
+//    in 4 pieces; 128 -> 128 101 and 20 in 32).
+//
+// Measured, 32768 rows of 16 experts, 1600 -> 1600, bf16, inputs that no cache holds:
+// forward 181 us (the linear layer on one weight of that size 182, a library's 209; with
+// inputs in cache 158), weight gradient added to what is there 235 (stored 215, of equal
+// groups 205; the linear layer's one gradient 190): 16 times the float32 output and the
+// ends of 16 sums. The matrix unit is busy 47% and 38% of the clocks. Two rows of two
+// experts, 1600 -> 6400, 9.7 us a call: 41 MB of weights and one launch.
 
 #include "gemm_device.hpp"
 
@@ -188,6 +198,12 @@ __global__ __launch_bounds__(512) void k_grouped_few(const GroupedArgs p) {
     skinny_tile<T, BKC, MT>(g, smem, j0);
 }
 
+// Rows of each piece of an expert's (the last may be shorter): whole slices, and a
+// number that the kernel and the join both come to.
+__device__ __forceinline__ int piece_rows(int rows, int pieces) {
+    return ((rows + BK - 1) / BK + pieces - 1) / pieces * BK;
+}
+
 template <typename T, int TM, int TN, int STAGES, int KG, int SUM, bool RAW>
 __global__ __launch_bounds__(256 * KG) __attribute__((amdgpu_waves_per_eu(KG > 2 ? KG : 2))) void k_grouped_weight(
     const GroupedArgs p) {
@@ -200,8 +216,22 @@ __global__ __launch_bounds__(256 * KG) __attribute__((amdgpu_waves_per_eu(KG > 2
     const int l = ((i + r) & 7) * run + (i >> 3);
     if (l >= per) return;
     int begin, end;
-    const int e = ranked(p, r, begin, end);
+    const int turn = r / p.pieces, piece = r - turn * p.pieces;
+    const int e = ranked(p, turn, begin, end);
     GemmArgs g{};
+    g.epi = p.epi;
+    if (p.pieces > 1) {
+        const int rows = piece_rows(end - begin, p.pieces);
+        begin += piece * rows;
+        end = end - begin < rows ? end : begin + rows;
+        if (begin >= end) return;  // no such piece, which the join knows
+        const int64_t at = (int64_t)piece * p.experts + e;
+        g.epi.y = p.part + at * p.M * p.ld_part;
+        if (SUM) g.sums = p.part_sums + at * (SUM == 1 ? p.N : p.M);
+    } else {
+        g.epi.y = static_cast<float*>(p.epi.y) + e * p.stride_w;
+        if (SUM) g.sums = p.sums + (int64_t)e * (SUM == 1 ? p.N : p.M);
+    }
     g.a = static_cast<const T*>(p.a) + (int64_t)begin * p.ld_a;
     g.b = static_cast<const T*>(p.b) + (int64_t)begin * p.ld_b;
     g.ld_a = p.ld_a;
@@ -212,12 +242,39 @@ __global__ __launch_bounds__(256 * KG) __attribute__((amdgpu_waves_per_eu(KG > 2
     g.tiles_m = p.tiles_m;
     g.tiles_n = p.tiles_n;
     g.slices = (g.K + BK - 1) / BK;
-    g.epi = p.epi;
-    g.epi.y = static_cast<float*>(p.epi.y) + e * p.stride_w;
-    if (SUM) g.sums = p.sums + (int64_t)e * (SUM == 1 ? p.N : p.M);
     int ti, tj;
     tile_at(g, l, ti, tj);
     gemm_tile<T, TM, TN, false, false, SUM, RAW, STAGES, KG, EPI_GRAD_WEIGHT>(g, smem, ti, tj, -1, 0, g.slices);
+}
+
+// One expert's gradient (blockIdx.y) from its pieces, an element a thread, and behind it
+// the bias's: the loads of 8 pieces are on the way at once, and small gradients still
+// make enough workgroups.
+__global__ __launch_bounds__(256) void k_grouped_join(const GroupedArgs p, const int sums) {
+    const int e = blockIdx.y;
+    const uint32_t total = (uint32_t)p.M * (uint32_t)p.N, i = blockIdx.x * 256u + threadIdx.x;
+    if (i >= total + (uint32_t)sums) return;
+    const Group q = group_of(p.offsets, p.rows, e);
+    const int rows = q.end - q.begin, tall = piece_rows(rows, p.pieces);
+    const int live = rows ? (rows + tall - 1) / tall : 0;
+    const float* from;
+    float* to;
+    int64_t step;
+    if (i < total) {
+        const uint32_t m = i / (uint32_t)p.N, n = i - m * (uint32_t)p.N;
+        step = (int64_t)p.experts * p.M * p.ld_part;
+        from = p.part + ((int64_t)e * p.M + m) * p.ld_part + n;
+        to = static_cast<float*>(p.epi.y) + e * p.stride_w + (int64_t)m * p.epi.ld_y + n;
+    } else {
+        step = (int64_t)p.experts * sums;
+        from = p.part_sums + (int64_t)e * sums + (i - total);
+        to = p.sums + (int64_t)e * sums + (i - total);
+    }
+    const float old = p.epi.accumulate ? *to : 0.f;
+    float s = 0.f;
+#pragma unroll 8
+    for (int t = 0; t < live; ++t) s += from[t * step];
+    *to = p.epi.accumulate ? old + s : s;
 }
 
 template <typename T, int TM, int TN, int STAGES, int KG, bool RAW, int MODE>
@@ -279,10 +336,8 @@ hipError_t weight_t(const GroupedArgs& p, TileKind tile, bool raw, int sum, unsi
         weight_tile<T, 256, 128, 2, 1, false>(p, sum, grid, st);
     else if (tile == TILE_SQUARE)
         weight_tile<T, 128, 128, 2, 1, false>(p, sum, grid, st);
-    else if (tile == TILE_SMALL)
-        weight_tile<T, 64, 64, 4, 1, false>(p, sum, grid, st);
     else
-        weight_tile<T, 64, 64, 2, 4, false>(p, sum, grid, st);
+        weight_tile<T, 64, 64, 4, 1, false>(p, sum, grid, st);
     return hipGetLastError();
 }
 
@@ -291,6 +346,12 @@ hipError_t weight_t(const GroupedArgs& p, TileKind tile, bool raw, int sum, unsi
 hipError_t launch_grouped(const GroupedArgs& p, TileKind tile, bool raw, bool b_kc, int dtype, unsigned grid,
                           hipStream_t st) {
     return dtype == 0 ? rows_t<bf16>(p, tile, raw, b_kc, grid, st) : rows_t<f16>(p, tile, raw, b_kc, grid, st);
+}
+
+hipError_t launch_grouped_join(const GroupedArgs& p, int sums, hipStream_t st) {
+    const dim3 grid((unsigned)(((int64_t)p.M * p.N + sums + 255) / 256), (unsigned)p.experts);
+    k_grouped_join<<<grid, 256, 0, st>>>(p, sums);
+    return hipGetLastError();
 }
 
 hipError_t launch_grouped_weight(const GroupedArgs& p, TileKind tile, bool raw, int dtype, int sum, unsigned grid,

@@ -125,6 +125,11 @@ struct GroupedArgs {
     const int32_t* offsets;  // [experts + 1]
     int64_t stride_w;        // elements from one expert's weight (or its gradient) to the next
     float* sums;             // bias gradients [experts][], or null
+    // weight gradient in pieces of each expert's rows: their sums [pieces][experts][M][ld_part]
+    // and bias sums [pieces][experts][] (pieces 1: none, the tiles write dw and sums)
+    float* part;
+    float* part_sums;
+    int32_t pieces, ld_part;
     int32_t ld_a, ld_b;
     int32_t rows, experts, M, N, K;
     int32_t tiles_m, tiles_n;  // of an expert's output; tiles_m of rows: the most blocks of all experts
@@ -134,6 +139,8 @@ hipError_t launch_grouped(const GroupedArgs& p, TileKind tile, bool raw, bool b_
                           hipStream_t st);
 hipError_t launch_grouped_weight(const GroupedArgs& p, TileKind tile, bool raw, int dtype, int sum, unsigned grid,
                                  hipStream_t st);
+// dw (+)= the pieces' sums, in order. sums: bias gradients an expert has (0 without)
+hipError_t launch_grouped_join(const GroupedArgs& p, int sums, hipStream_t st);
 
 // 8-bit floating point with a float32 scale for each block of 128: what a format's
 // kernels are called by.

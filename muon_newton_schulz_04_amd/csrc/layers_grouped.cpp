@@ -61,18 +61,21 @@ constexpr TileCost kRowTiles[] = {{muon::TILE_TALL, 256, 128, 6.0, 0.82, 1.65, 5
                                   {muon::TILE_SQUARE_GROUPS, 128, 128, 5.5, 0.52, 0.75, 3.0, 256},
                                   {muon::TILE_SMALL, 64, 64, 4.0, 0.26, 0.48, 1.0, 512},
                                   {muon::TILE_SMALL_GROUPS, 64, 64, 5.0, 0.18, 0.33, 2.0, 256}};
-// The weight gradient's (32768, 16, 1600, 1600 in 351, -, 253, -, 227; 4099, 8, 1536, 768
-// 39, -, 31, -, 40).
-constexpr TileCost kWeightTiles[] = {{muon::TILE_TALL, 256, 128, 8.0, 1.0, 2.0, 8.0, 512},
-                                     {muon::TILE_SQUARE, 128, 128, 6.5, 0.7, 1.1, 5.0, 512},
-                                     {muon::TILE_SMALL, 64, 64, 4.5, 0.28, 0.55, 2.0, 512},
-                                     {muon::TILE_SMALL_GROUPS, 64, 64, 6.5, 0.1, 0.16, 4.0, 256}};
+// The weight gradient's, over 18 shapes, 3 tiles and 1 to 32 pieces of each expert's rows;
+// rows, experts, in, out; us whole and in the best of the pieces (small, square, tall):
+// 32768, 16, 1600, 1600 351, 253, 227; 32768, 2, 2048, 800 269 and 260, 293 and 174, 394
+// and 167; 32768, 4, 768, 768 92 and 92, 166 and 87, 209 and 95; 32768, 4, 256, 128 60 and
+// 19, 121 and 22, 164 and 25; 4099, 8, 1536, 768 40, 36, 39.
+constexpr TileCost kWeightTiles[] = {{muon::TILE_TALL, 256, 128, 10.0, 0.83, 1.47, 0.0, 512},
+                                     {muon::TILE_SQUARE, 128, 128, 8.0, 0.64, 0.85, 0.0, 512},
+                                     {muon::TILE_SMALL, 64, 64, 8.0, 0.23, 0.31, 0.65, 512}};
 
 int64_t up_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct GroupedPlan {
     muon::TileKind tile;
     int rows, cols;
+    int pieces = 1;  // of each expert's rows (weight gradient)
 };
 
 // How many blocks of `tall` rows the groups are, as far as the host can tell: half a
@@ -101,18 +104,57 @@ GroupedPlan rows_plan(int64_t rows, int64_t experts, int64_t N, int64_t K, bool 
     return best;
 }
 
-GroupedPlan weight_plan(int64_t rows, int64_t experts, int64_t M, int64_t N) {
+// The workgroups of a weight gradient: an expert's tiles, in runs of one length for each
+// of the 8 XCDs, for each piece of its rows.
+int64_t weight_grid(const GroupedPlan& p, int64_t experts, int64_t M, int64_t N) {
+    return experts * p.pieces * (up_div(up_div(M, p.rows) * up_div(N, p.cols), 8) * 8);
+}
+
+// Few tiles of long sums leave CUs idle: then each expert's rows are cut into pieces,
+// whose sums meet in a second kernel (its launch, and each piece's sums once written
+// and read).
+GroupedPlan weight_plan(int64_t rows, int64_t experts, int64_t M, int64_t N, bool raw) {
     // the longest of the sums, where some experts have half as much again as the mean
-    const double slices = 1.0 + 1.5 * (double)rows / (double)experts / muon::kGemmSlice;
+    const double all = 1.5 * (double)rows / (double)experts / muon::kGemmSlice;
+    const double out = (double)experts * (double)M * (double)N;
     GroupedPlan best{};
     double least = 1e300;
-    for (const TileCost& c : kWeightTiles) {
-        const double t = tile_price(c, (double)(experts * up_div(M, c.rows) * up_div(N, c.cols)), slices);
-        if (t >= least) continue;
-        least = t;
-        best = {c.kind, c.rows, c.cols};
-    }
+    for (int pieces = 1; pieces == 1 || (pieces <= 64 && all >= 8.0 * pieces); pieces *= 2)
+        for (const TileCost& c : kWeightTiles) {
+            if (raw && c.kind != muon::TILE_SMALL) continue;
+            const GroupedPlan p{c.kind, c.rows, c.cols, pieces};
+            if (pieces > 1 && (weight_grid(p, experts, M, N) >= (int64_t)1 << 22 || M * N >= (int64_t)1 << 31)) continue;
+            double t = tile_price(c, (double)(experts * pieces * up_div(M, c.rows) * up_div(N, c.cols)), 1.0 + all / pieces);
+            if (pieces > 1) t += 3.3 + out * (2 * pieces + 1) * 4e-6 / 4.9;
+            if (t >= least) continue;
+            least = t;
+            best = p;
+        }
     return best;
+}
+
+struct WeightLayout {
+    bool io, raw;  // weight_layout; operands read as they are
+    int64_t M, N;  // an expert's gradient
+    GroupedPlan plan;
+    int64_t ld_part;
+    size_t part, need;  // bytes of the pieces' sums, with those of their bias sums
+};
+WeightLayout weight_layout(const muon_grouped& d, const void* x, const void* dy) {
+    WeightLayout w{};
+    w.io = d.weight_layout == MUON_WEIGHT_IN_OUT;
+    w.M = w.io ? d.in_features : d.out_features;
+    w.N = w.io ? d.out_features : d.in_features;
+    const int64_t ld_x = stride_of(d.ld_x, d.in_features), ld_y = stride_of(d.ld_y, d.out_features);
+    w.raw = d.rows > 0 && (!whole_chunks(x, ld_x, d.in_features) || !whole_chunks(dy, ld_y, d.out_features));
+    w.plan = weight_plan(d.rows, d.experts, w.M, w.N, w.raw);
+    w.ld_part = (w.N + 3) / 4 * 4;
+    if (w.plan.pieces > 1) {
+        const size_t each = (size_t)w.plan.pieces * (size_t)d.experts;
+        w.part = up256(each * (size_t)(w.M * w.ld_part) * 4);
+        w.need = w.part + up256(each * (size_t)d.out_features * 4);
+    }
+    return w;
 }
 
 muon_status too_large() { return fail(MUON_E_SHAPE, "grouped linear: output too large"); }
@@ -183,13 +225,24 @@ muon_status muon_grouped_linear_grad_input(const muon_grouped* d, const void* dy
     return guarded([&]() { return run_grouped(d, false, dy, w, offsets, e, dx, stream); });
 }
 
+muon_status muon_grouped_linear_workspace_bytes(const muon_grouped* d, const void* x, const void* dy,
+                                                size_t* out_bytes) {
+    return guarded([&]() -> muon_status {
+        if (!out_bytes) return fail(MUON_E_INVALID_ARG, "null out_bytes");
+        TRY(check_grouped(d));
+        *out_bytes = weight_layout(*d, x, dy).need;
+        return MUON_OK;
+    });
+}
+
 muon_status muon_grouped_linear_grad_weight(const muon_grouped* d, const void* x, const void* dy,
                                             const int32_t* offsets, float* dw, float* dbias, int32_t accumulate,
-                                            void* stream) {
+                                            void* workspace, size_t ws_bytes, void* stream) {
     return guarded([&]() -> muon_status {
         TRY(check_grouped(d));
         if (!dw || !offsets || (d->rows > 0 && (!x || !dy))) return fail(MUON_E_INVALID_ARG, "null tensor");
-        const bool io = d->weight_layout == MUON_WEIGHT_IN_OUT;
+        const WeightLayout lay = weight_layout(*d, x, dy);
+        const bool io = lay.io;
         const Tensor X = rows_of(*d, x, d->in_features, d->ld_x), Y = rows_of(*d, dy, d->out_features, d->ld_y);
         const Tensor W = weights_of(*d, dw, 4), Bi{dbias, 1, d->experts * d->out_features, d->experts * d->out_features, 4};
         const Tensor Of{offsets, 1, d->experts + 1, d->experts + 1, 4};
@@ -201,8 +254,12 @@ muon_status muon_grouped_linear_grad_weight(const muon_grouped* d, const void* x
         TRY(check_disjoint(W, {X, Y, Bi, Of}));
         TRY(check_disjoint(Bi, {X, Y, Of}));
         const Tensor &A = io ? X : Y, &B = io ? Y : X;
-        const bool raw = d->rows > 0 && (!whole_chunks(A.p, A.ld, A.cols) || !whole_chunks(B.p, B.ld, B.cols));
-        const GroupedPlan plan = raw ? GroupedPlan{muon::TILE_SMALL, 64, 64} : weight_plan(d->rows, d->experts, A.cols, B.cols);
+        const GroupedPlan& plan = lay.plan;
+        const int64_t grid = weight_grid(plan, d->experts, lay.M, lay.N);
+        if (grid >= (int64_t)1 << 22) return too_large();
+        TRY(check_workspace(workspace, ws_bytes, lay.need));
+        const Tensor K{workspace, 1, (int64_t)lay.need, (int64_t)lay.need, 1};
+        TRY(check_disjoint(K, {X, Y, W, Bi, Of}));
         muon::GroupedArgs p{};
         p.a = A.p;
         p.b = B.p;
@@ -220,16 +277,27 @@ muon_status muon_grouped_linear_grad_weight(const muon_grouped* d, const void* x
         p.epi.mode = muon::EPI_GRAD_WEIGHT;
         p.epi.y = dw;
         p.epi.ld_y = (int)stride_of(d->ld_w, io ? d->out_features : d->in_features);
-        p.epi.accumulate = accumulate != 0;
-        // an expert's tiles in runs of one length for each of the 8 XCDs
-        const int64_t grid = d->experts * (((int64_t)p.tiles_m * p.tiles_n + 7) / 8 * 8);
-        if (grid >= (int64_t)1 << 22) return too_large();
+        const bool cut = plan.pieces > 1;
+        p.epi.accumulate = accumulate != 0 && !cut;
+        p.pieces = plan.pieces;
+        p.ld_part = (int)lay.ld_part;
+        const int ld_w = p.epi.ld_y;
+        if (cut) {
+            p.part = static_cast<float*>(workspace);
+            p.part_sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + lay.part);
+            p.epi.ld_y = p.ld_part;
+        }
         TRY(check_device());
         // dy is the second operand of an [in, out] gradient, else the first
         const int sum = !dbias ? 0 : io ? 1 : 2;
-        return hip_status(muon::launch_grouped_weight(p, plan.tile, raw, d->dtype, sum, (unsigned)grid,
-                                                      static_cast<hipStream_t>(stream)),
-                          "grouped weight gradient kernel");
+        hipStream_t st = static_cast<hipStream_t>(stream);
+        TRY(hip_status(muon::launch_grouped_weight(p, plan.tile, lay.raw, d->dtype, sum, (unsigned)grid, st),
+                       "grouped weight gradient kernel"));
+        if (!cut) return MUON_OK;
+        p.epi.accumulate = accumulate != 0;
+        p.epi.ld_y = ld_w;
+        return hip_status(muon::launch_grouped_join(p, dbias ? (int)d->out_features : 0, st),
+                          "grouped weight gradient sums");
     });
 }
 

@@ -61,8 +61,10 @@ size_t rms_workspace(const muon_rmsnorm& d) {
     return up256((size_t)muon::rms_backward_blocks(d.rows, d.cols, d.dtype) * (size_t)d.cols * 4);
 }
 
-// The tile of an 8-bit product, by prices fitted to times measured over 22 shapes and
-// every tile (bf16 output; us, small, small in groups, square, square in groups, tall):
+// The tile of an 8-bit product: blocks of few rows while there are no more of them than
+// CUs (64 rows, 6400 -> 1600 6.7 us, in 64 x 64 tiles 13.6; 1600 -> 6400, which has more,
+// 13.6 and 7.2), else by prices fitted to times measured over 22 shapes and every tile
+// (bf16 output; us, small, small in groups, square, square in groups, tall):
 // 512 x 6400 x 1600 32, 19, 54, 39, 60; 1024 x 1600 x 1600 10.9, 14.5, 14.4, 13.4, 21.7;
 // 2048 x 6400 x 1600 64, 68, 54, 39, 60; 4096 x 1600 x 1600 31, 44, 18.4, 26, 22; 4096 x
 // 1600 x 6400 123, 173, 70, 92, 59.

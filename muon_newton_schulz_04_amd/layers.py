@@ -686,8 +686,13 @@ def grouped_linear_grad_weight(x, dy, offsets, dw=None, dbias=None, accumulate=F
         dbias = torch.empty((n_e, fout), dtype=torch.float32, device=device)
     pb = 0 if dbias is None else _expert_vectors("dbias", dbias, n_e, fout, dev)
     d = B.muon_grouped(n, n_e, fin, fout, ld_x, ld_w, ld_y, step, code, lay)
-    s = _on(dev, B.muon_grouped_linear_grad_weight, d, x.data_ptr(), dy.data_ptr(), po, dw.data_ptr(), pb,
-            int(accumulate))
+    px, py, pd = x.data_ptr(), dy.data_ptr(), dw.data_ptr()
+    s = _on(dev, B.muon_grouped_linear_grad_weight, d, px, py, po, pd, pb, int(accumulate), 0, 0)
+    if s == B.MUON_E_WORKSPACE:
+        s, nbytes = B.muon_grouped_linear_workspace_bytes(d, px, py)
+        _check(s, "grouped_linear_grad_weight")
+        ws, pws = _workspace(nbytes, device)
+        s = _on(dev, B.muon_grouped_linear_grad_weight, d, px, py, po, pd, pb, int(accumulate), pws, nbytes)
     if s:
         _check(s, "grouped_linear_grad_weight")
     return dw, dbias

@@ -279,7 +279,7 @@ static void grouped(void) {
     int32_t* const off = AT(9);
     EXPECT(muon_grouped_linear_forward(&d, AT(1), AT(2), off, NULL, AT(3), NULL) == reached);
     EXPECT(muon_grouped_linear_grad_input(&d, AT(1), AT(2), off, NULL, AT(3), NULL) == reached);
-    EXPECT(muon_grouped_linear_grad_weight(&d, AT(1), AT(2), off, AT(3), AT(4), 0, NULL) == reached);
+    EXPECT(muon_grouped_linear_grad_weight(&d, AT(1), AT(2), off, AT(3), AT(4), 0, NULL, 0, NULL) == reached);
     for (int k = 0; k < 15; ++k) {
         muon_grouped b = d;
         muon_status want = MUON_E_SHAPE;
@@ -302,7 +302,7 @@ static void grouped(void) {
         if (k == 14) b.ld_w = 130, b.stride_w = 96 * 128;
         EXPECT(muon_grouped_linear_forward(&b, AT(1), AT(2), off, NULL, AT(3), NULL) == want);
         EXPECT(muon_grouped_linear_grad_input(&b, AT(1), AT(2), off, NULL, AT(3), NULL) == want);
-        EXPECT(muon_grouped_linear_grad_weight(&b, AT(1), AT(2), off, AT(3), NULL, 0, NULL) == want);
+        EXPECT(muon_grouped_linear_grad_weight(&b, AT(1), AT(2), off, AT(3), NULL, 0, NULL, 0, NULL) == want);
     }
     EXPECT(muon_grouped_linear_forward(NULL, AT(1), AT(2), off, NULL, AT(3), NULL) == BAD_ARG);
     EXPECT(muon_grouped_linear_forward(&d, NULL, AT(2), off, NULL, AT(3), NULL) == BAD_ARG);
@@ -332,17 +332,39 @@ static void grouped(void) {
     EXPECT(muon_grouped_linear_grad_input(&d, AT(1), AT(2), off, &e, AT(3), NULL) == BAD_ARG);
     e.z = AT(5);
     EXPECT(muon_grouped_linear_grad_input(&d, AT(1), AT(2), off, &e, AT(3), NULL) == reached);
-    EXPECT(muon_grouped_linear_grad_weight(&d, AT(1), AT(2), off, NULL, NULL, 0, NULL) == BAD_ARG);
-    EXPECT(muon_grouped_linear_grad_weight(&d, AT(1), AT(2), off, AT(3), AT(3), 0, NULL) == BAD_ARG);
-    EXPECT(muon_grouped_linear_grad_weight(&d, AT(1), AT(2), off, AT(2), NULL, 0, NULL) == BAD_ARG);
-    EXPECT(muon_grouped_linear_grad_weight(&d, AT(1), AT(2), off, AT(3), (float*)AT(9), 0, NULL) == BAD_ARG);
-    EXPECT(muon_grouped_linear_grad_weight(&d, AT(1), AT(2), off, (float*)((char*)AT(3) + 2), NULL, 0, NULL) ==
+    EXPECT(muon_grouped_linear_grad_weight(&d, AT(1), AT(2), off, NULL, NULL, 0, NULL, 0, NULL) == BAD_ARG);
+    EXPECT(muon_grouped_linear_grad_weight(&d, AT(1), AT(2), off, AT(3), AT(3), 0, NULL, 0, NULL) == BAD_ARG);
+    EXPECT(muon_grouped_linear_grad_weight(&d, AT(1), AT(2), off, AT(2), NULL, 0, NULL, 0, NULL) == BAD_ARG);
+    EXPECT(muon_grouped_linear_grad_weight(&d, AT(1), AT(2), off, AT(3), (float*)AT(9), 0, NULL, 0, NULL) == BAD_ARG);
+    EXPECT(muon_grouped_linear_grad_weight(&d, AT(1), AT(2), off, (float*)((char*)AT(3) + 2), NULL, 0, NULL, 0, NULL) ==
            MUON_E_LAYOUT);
+    /* many rows of few features: pieces of the rows, whose sums need a workspace */
+    size_t n = 7;
+    EXPECT(muon_grouped_linear_workspace_bytes(&d, AT(1), AT(2), &n) == MUON_OK && n == 0);
+    EXPECT(muon_grouped_linear_workspace_bytes(&d, AT(1), AT(2), NULL) == BAD_ARG);
+    EXPECT(muon_grouped_linear_workspace_bytes(NULL, AT(1), AT(2), &n) == BAD_ARG);
+    d.rows = 100000;
+    for (int odd = 0; odd < 2; ++odd) {
+        void* x = (char*)AT(1) + 2 * odd;
+        char* const ws = AT(100);
+        EXPECT(muon_grouped_linear_workspace_bytes(&d, x, AT(2), &n) == MUON_OK && n >= 2 * 4 * 96 * 128 * 4);
+        EXPECT(muon_grouped_linear_grad_weight(&d, x, AT(2), off, AT(3), AT(4), 1, NULL, 0, NULL) == MUON_E_WORKSPACE);
+        EXPECT(muon_grouped_linear_grad_weight(&d, x, AT(2), off, AT(3), AT(4), 1, ws, n - 1, NULL) ==
+               MUON_E_WORKSPACE);
+        EXPECT(muon_grouped_linear_grad_weight(&d, x, AT(2), off, AT(3), AT(4), 1, ws + 16, n, NULL) ==
+               MUON_E_WORKSPACE);
+        EXPECT(muon_grouped_linear_grad_weight(&d, x, AT(2), off, AT(3), AT(4), 1, ws, n, NULL) == reached);
+        EXPECT(muon_grouped_linear_grad_weight(&d, x, AT(2), off, (float*)(ws + n - 256), AT(4), 1, ws, n, NULL) ==
+               BAD_ARG);
+        EXPECT(muon_grouped_linear_grad_weight(&d, x, AT(2), off, AT(3), (float*)ws, 1, ws, n, NULL) == BAD_ARG);
+        EXPECT(muon_grouped_linear_grad_weight(&d, x, ws, off, AT(3), AT(4), 1, ws, n, NULL) == BAD_ARG);
+        EXPECT(muon_grouped_linear_grad_weight(&d, x, AT(2), (int32_t*)ws, AT(3), AT(4), 1, ws, n, NULL) == BAD_ARG);
+    }
     d.rows = 0;
     EXPECT(muon_grouped_linear_forward(&d, NULL, NULL, NULL, NULL, NULL, NULL) == MUON_OK);
     EXPECT(muon_grouped_linear_grad_input(&d, NULL, NULL, NULL, NULL, NULL, NULL) == MUON_OK);
-    EXPECT(muon_grouped_linear_grad_weight(&d, NULL, NULL, off, AT(3), NULL, 0, NULL) == reached);
-    EXPECT(muon_grouped_linear_grad_weight(&d, NULL, NULL, NULL, AT(3), NULL, 0, NULL) == BAD_ARG);
+    EXPECT(muon_grouped_linear_grad_weight(&d, NULL, NULL, off, AT(3), NULL, 0, NULL, 0, NULL) == reached);
+    EXPECT(muon_grouped_linear_grad_weight(&d, NULL, NULL, NULL, AT(3), NULL, 0, NULL, 0, NULL) == BAD_ARG);
     const int64_t sizes[] = {8, 33, 128, 1600, 50304, (int64_t)1 << 21};
     const int64_t rows[] = {1, 17, 1000, 131072, ((int64_t)1 << 24) - 1};
     const int64_t experts[] = {1, 3, 64, 1000, 65536};
@@ -363,7 +385,9 @@ static void grouped(void) {
                         muon_status s = muon_grouped_linear_forward(&d, p, w, off, NULL, y, NULL);
                         EXPECT(s == reached || s == MUON_E_SHAPE || (huge && s == BAD_ARG));
                         if (rows[r] <= 131072 && experts[x] <= 64 && sizes[b] <= 1600) EXPECT(s == reached);
-                        s = muon_grouped_linear_grad_weight(&d, p, y, off, w, NULL, 0, NULL);
+                        size_t n = 0;
+                        EXPECT(muon_grouped_linear_workspace_bytes(&d, p, y, &n) == MUON_OK);
+                        s = muon_grouped_linear_grad_weight(&d, p, y, off, w, NULL, 0, AT(1 << 24), n, NULL);
                         EXPECT(s == reached || s == MUON_E_SHAPE || (huge && s == BAD_ARG));
                         if (experts[x] <= 64 && sizes[a] <= 1600 && sizes[b] <= 1600) EXPECT(s == reached);
                     }

@@ -14,4 +14,5 @@ hipError_t launch_grouped(const GroupedArgs&, TileKind, bool, bool, int, unsigne
 hipError_t launch_grouped_weight(const GroupedArgs&, TileKind, bool, int, int, unsigned, hipStream_t) {
     return hipSuccess;
 }
+hipError_t launch_grouped_join(const GroupedArgs&, int, hipStream_t) { return hipSuccess; }
 }  // namespace muon

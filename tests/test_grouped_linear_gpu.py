@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from eight import T, U, act64, act_tol, close, cpu64, gen, rand, slope64, sum_tol
+from muon_newton_schulz_04_amd import binding as B
 from muon_newton_schulz_04_amd import layers as L
 
 pytestmark = pytest.mark.gpu
@@ -159,6 +160,54 @@ def test_offsets_that_repeat_all_rows():
     L.grouped_linear_forward(x, w, off, out=buf[8:8 + n])
     assert (buf[:8] == 7).all() and (buf[8 + n:] == 7).all()
     assert ((buf[8:8 + n] == 8) | (buf[8:8 + n] == 7)).all() and (buf[8] == 8).all()
+
+
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+@pytest.mark.parametrize("at", [0, 1])
+def test_pieces_of_many_rows(at, layout):
+    """Few experts of few features whose rows are summed in pieces: the C call on a
+    workspace full of NaN with guard bytes behind it, rows 16-byte aligned or not, experts
+    with fewer slices of rows than pieces or none, a gradient with gaps, adding to it."""
+    g = gen(at)
+    t, i, o = torch.bfloat16, 72, 136
+    counts = [9001, 0, 100, 3000]
+    n, e = 12200, len(counts)  # 99 rows behind the last expert's
+    x, dy = rand(g, (n, i + 8), t)[:, at:at + i], rand(g, (n, o + 8), t, std=0.1)[:, at:at + o]
+    off = torch.tensor([0] + counts).cumsum(0).int().cuda()
+    r, c = (i, o) if layout == "in_out" else (o, i)
+    lay = B.MUON_WEIGHT_IN_OUT if layout == "in_out" else B.MUON_WEIGHT_OUT_IN
+    step = (r + 1) * (c + 5)
+    d = B.muon_grouped(n, e, i, o, i + 8, c + 5, o + 8, step, 0, lay)
+    s, need = B.muon_grouped_linear_workspace_bytes(d, x.data_ptr(), dy.data_ptr())
+    assert s == 0 and need >= 2 * e * r * c * 4
+    want, dbias = [], []
+    for k in range(e):
+        rows = slice(int(off[k]), int(off[k + 1]))
+        a, b = (cpu64(x[rows]).t(), cpu64(dy[rows])) if layout == "in_out" else (cpu64(dy[rows]).t(), cpu64(x[rows]))
+        want.append((a @ b, sum_tol(a, b)))
+        ones = torch.ones(1, counts[k], dtype=torch.float64)
+        dbias.append((cpu64(dy[rows]).sum(0), sum_tol(ones, cpu64(dy[rows]))[0]))
+    results = []
+    for accumulate in (0, 1):
+        buf = torch.full((e * step,), 3.0, device="cuda")
+        db = torch.full((e * o,), 5.0, device="cuda")
+        ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+        assert ws.data_ptr() % 256 == 0
+        s = B.muon_grouped_linear_grad_weight(d, x.data_ptr(), dy.data_ptr(), off.data_ptr(), buf.data_ptr(),
+                                              db.data_ptr(), accumulate, ws.data_ptr(), need,
+                                              torch.cuda.current_stream().cuda_stream)
+        assert s == 0, B.muon_op_last_error()
+        assert (ws[need:] == 0xFF).all()
+        full = buf.view(e, r + 1, c + 5)
+        assert (full[:, r] == 3).all() and (full[:, :, c:] == 3).all()
+        for k in range(e):
+            more = accumulate * U * (want[k][0].abs() + 3)
+            close(full[k, :r, :c], want[k][0] + 3 * accumulate, want[k][1] + more, torch.float32)
+            more = accumulate * U * (dbias[k][0].abs() + 5)
+            close(db[k * o:k * o + o], dbias[k][0] + 5 * accumulate, dbias[k][1] + more, torch.float32)
+        results.append((full.clone(), db.clone()))
+    dw, db = L.grouped_linear_grad_weight(x, dy, off, dbias=True, weight_layout=layout)
+    assert torch.equal(dw, results[0][0][:, :r, :c]) and torch.equal(db.flatten(), results[0][1])
 
 
 def test_no_rows():

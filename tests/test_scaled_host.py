@@ -71,14 +71,15 @@ KINDS = ["tall", "square", "square groups", "small", "small groups", "few 16", "
 
 
 def plans(tmp_path, lines):
-    """The kind of tile that the entry points' sources take for each line."""
+    """The kind of tile that the entry points' sources take for each line, and the pieces."""
     exe = str(tmp_path / "scaled_plan")
     srcs = [os.path.join(NATIVE, s) for s in ("scaled_plan.cpp", "layer_stubs.cpp", "scaled_stubs.cpp")]
     subprocess.run(["g++", "-std=c++17", "-O1", *INC, *srcs, os.path.join(CSRC, "layers.cpp"), "-o", exe,
                     f"-L{ROCM}/lib", "-lamdhip64", f"-Wl,-rpath,{ROCM}/lib"], check=True)
     text = "".join(" ".join(str(v) for v in line) + "\n" for line in lines)
     out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.split("\n")
-    return [KINDS[int(o.split()[0])] for o in out if o]
+    got = [[int(v) for v in o.split()] for o in out if o]
+    return [KINDS[k] + (f" in {p}" if p > 1 else "") for k, p in got]
 
 
 @pytest.mark.skipif(not _have_toolchain(), reason="g++ / ROCm HIP runtime not available")
@@ -91,7 +92,9 @@ def test_every_tile_is_taken_by_a_tested_size(tmp_path):
     assert {c[-1] for c in EIGHT} == set(KINDS)
     for op in ("forward", "grad input"):
         assert {c[-1] for c in GROUPED if c[0] == op} == set(KINDS)
-    assert {c[-1] for c in GROUPED if c[0] == "grad weight"} == {"tall", "square", "small", "small groups"}
+    weight = {c[-1] for c in GROUPED if c[0] == "grad weight"}
+    assert {c.split(" in ")[0] for c in weight} == {"tall", "square", "small"}
+    assert {c.split(" in ")[0] for c in weight if " in " in c} == {"tall", "square", "small"}
 
 
 @pytest.mark.skipif(not _have_hipcc(), reason="hipcc not available")

@@ -49,8 +49,12 @@ GROUPED = [
     ("grad input", [3000, 41, 0, 5200], 3208, 264, 0, "tall"),
     ("grad weight", [60, 0, 90, 11], 200, 136, 0, "small"),
     ("grad weight", [60, 0, 90, 11], 136, 200, 1, "small"),
-    ("grad weight", [3000, 0, 200], 200, 136, 0, "small groups"),
-    ("grad weight", [3000, 0, 200], 136, 200, 1, "small groups"),
+    ("grad weight", [9000, 0, 5000], 200, 136, 0, "small in 8"),
+    ("grad weight", [9000, 77, 5000], 136, 200, 1, "small in 8"),
+    ("grad weight", [18000, 6000], 1032, 520, 0, "square in 4"),
+    ("grad weight", [18000, 6000], 520, 1032, 1, "square in 4"),
+    ("grad weight", [0, 16000, 9000], 1544, 808, 0, "tall in 2"),
+    ("grad weight", [0, 16000, 9000], 808, 1544, 1, "tall in 2"),
     ("grad weight", [500, 0, 90, 311], 808, 1032, 0, "square"),
     ("grad weight", [500, 0, 90, 311], 1032, 808, 1, "square"),
     ("grad weight", [1500, 0, 890, 3011, 700], 1608, 1544, 0, "tall"),
