@@ -24,7 +24,7 @@
 // forward 181 us (the linear layer on one weight of that size 182, a library's 209; with
 // inputs in cache 158), weight gradient added to what is there 235 (stored 215, of equal
 // groups 205; the linear layer's one gradient 190): 16 times the float32 output and the
-// ends of 16 sums. The matrix unit is busy 47% and 38% of the clocks. Two rows of two
+// ends of 16 sums. The matrix unit is busy 46% and 38% of the clocks. Two rows of two
 // experts, 1600 -> 6400, 9.7 us a call: 41 MB of weights and one launch.
 
 #include "gemm_device.hpp"

@@ -44,8 +44,8 @@ __device__ __forceinline__ void emit(const RmsForward& n, int64_t row, int c, in
         uint32_t m = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = umax(m, magnitude(t[e]));
-        // (times a rounded reciprocal 36.4 us, not 37.4, and twice as many of 16384 x 1600
-        // values, 3 or 4, on the other side of a border between two 8-bit values)
+        // (times a rounded reciprocal 36.4 us, not 37.4, but 2 more of 16384 x 1600 values
+        // on the wrong side of a border between two 8-bit values)
         const ExactScale<F, true> s(max16(m));
         // rows go on with zeros to the next multiple of 16
         if (left > -8 && (left > 0 || (c & 8))) {
