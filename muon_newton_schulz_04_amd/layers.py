@@ -355,6 +355,9 @@ def _eight(name, pair, dev, weight):
     p = t.data_ptr()
     if ld % 16 or p % 16:
         raise ValueError(f"{name}: rows must start 16-byte aligned (stride {ld})")
+    end = t.storage_offset() + (rows - 1) * ld + (cols + 15) // 16 * 16
+    if cols % 16 and rows and t.untyped_storage().nbytes() < end:
+        raise ValueError(f"{name}: the last row's bytes up to the next multiple of 16 are read too, and lie outside")
     shape = (_blocks(rows), _blocks(cols)) if weight else (_blocks(cols), rows)
     if scale.dtype is not torch.float32 or scale.get_device() != dev:
         _same(f"{name}'s scales", scale, torch.float32, dev)
@@ -402,8 +405,8 @@ def rmsnorm_forward(x, weight=None, residual=None, eps=1e-5, quantize=None, out=
         y = out
     rstd = torch.empty(rows, dtype=torch.float32, device=device)
     d = B.muon_rmsnorm(rows, cols, ld_x, ld_a, ld_r, ld_y, 0, code, eps)
-    s = _on(dev, B.muon_rmsnorm_forward, d, x.data_ptr(), pa, 0 if weight is None else _vector("weight", weight, cols, dev),
-            pr, py, q, rstd.data_ptr())
+    pw = 0 if weight is None else _vector("weight", weight, cols, dev)
+    s = _on(dev, B.muon_rmsnorm_forward, d, x.data_ptr(), pa, pw, pr, py, q, rstd.data_ptr())
     if s:
         _check(s, "rmsnorm_forward")
     return (y, rstd) if residual is None else (y, rstd, residual_out)

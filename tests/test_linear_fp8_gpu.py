@@ -171,3 +171,31 @@ def test_refusals():
         L.quantize_fp8(torch.zeros(2, 2, device="cuda"), dtype=torch.float16)
     with pytest.raises(ValueError, match="residual"):
         L.rmsnorm_forward(torch.zeros(2, 8, device="cuda"), residual_out=torch.zeros(2, 8, device="cuda"))
+
+
+def test_last_row_goes_on_to_the_next_16():
+    """The kernel reads whole chunks of 16 bytes: a matrix whose storage ends before is
+    refused, and one whose storage just holds them is not."""
+    g = gen(6)
+    w = eight(g, 24, 40, weight=True)
+    for rows in (1, 5):
+        x, s = eight(g, rows, 40)
+        want = L.linear_fp8_forward((x, s), w)
+        flat = torch.zeros(rows * 48, dtype=torch.uint8, device="cuda").view(x.dtype)
+        full = flat.as_strided((rows, 40), (48, 1))
+        full.view(torch.uint8).copy_(x.view(torch.uint8))
+        assert torch.equal(L.linear_fp8_forward((full, s), w), want)
+        short = flat[:rows * 48 - 8].clone().as_strided((rows, 40), (48, 1))
+        with pytest.raises(ValueError, match="next multiple of 16"):
+            L.linear_fp8_forward((short, s), w)
+        with pytest.raises(ValueError, match="next multiple of 16"):
+            L.linear_fp8_grad_input((short, s), w)
+
+
+def test_no_tokens():
+    g = gen(7)
+    w = eight(g, 24, 40, weight=True)
+    x, s = L.quantize_fp8(torch.zeros(0, 40, dtype=torch.bfloat16, device="cuda"))
+    y, z = L.linear_fp8_forward((x, s), w, save_preact=True)
+    assert y.shape == (0, 24) and z.shape == (0, 24)
+    assert L.linear_fp8_grad_input((x, s), w).shape == (0, 24)

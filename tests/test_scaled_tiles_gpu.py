@@ -51,6 +51,7 @@ GROUPED = [
     ("grad weight", [60, 0, 90, 11], 136, 200, 1, "small"),
     ("grad weight", [9000, 0, 5000], 200, 136, 0, "small in 8"),
     ("grad weight", [9000, 77, 5000], 136, 200, 1, "small in 8"),
+    ("grad weight", [1500] * 45 + [0, 7, 70] + [1500] * 30, 24, 16, 0, "small in 4"),
     ("grad weight", [18000, 6000], 1032, 520, 0, "square in 4"),
     ("grad weight", [18000, 6000], 520, 1032, 1, "square in 4"),
     ("grad weight", [0, 16000, 9000], 1544, 808, 0, "tall in 2"),
