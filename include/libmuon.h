@@ -473,7 +473,10 @@ muon_status muon_linear_scaled_grad_input(const muon_linear* d, const muon_eight
  * that are in range and ascending: rows are then of unspecified values, and nothing
  * outside the tensors is read or written. Rows before the first and behind the last
  * expert's are not read and left as they are. rows < 2^24, experts at most 2^16,
- * features from 8 to 2^21. */
+ * features from 8 to 2^21. An output of fewer than 2^24 tiles of 64 x 64 is taken, and
+ * larger ones may be refused (MUON_E_SHAPE): of rows, counted as rows / 64 rounded down
+ * and one for each expert (each row, of fewer rows); of weight gradients, an expert's as
+ * the next multiple of 8. */
 typedef struct muon_grouped {
     int64_t rows;
     int64_t experts;

@@ -78,6 +78,21 @@ struct GroupedPlan {
     int pieces = 1;  // of each expert's rows (weight gradient)
 };
 
+// Workgroups of the forward pass and the input gradient: every expert with rows may end
+// inside a tile.
+int64_t most_blocks(int64_t rows, int64_t experts, int64_t tall) {
+    return (rows < experts ? rows : experts) + rows / tall;
+}
+int64_t rows_grid(const GroupedPlan& p, int64_t rows, int64_t experts, int64_t N) {
+    return most_blocks(rows, experts, p.rows) * up_div(N, p.cols);
+}
+
+// A launch has fewer than 2^32 threads.
+bool fits(int64_t grid, muon::TileKind tile) {
+    const bool two = tile != muon::TILE_TALL && tile != muon::TILE_SQUARE && tile != muon::TILE_SMALL;
+    return grid < (int64_t)1 << (two ? 23 : 24);
+}
+
 // How many blocks of `tall` rows the groups are, as far as the host can tell: half a
 // block more for each group that has rows.
 double expected_blocks(int64_t rows, int64_t experts, int64_t tall) {
@@ -85,23 +100,26 @@ double expected_blocks(int64_t rows, int64_t experts, int64_t tall) {
     return std::ceil(n > some ? n : some);
 }
 
+// rows 0: no tile's workgroups fit one launch
 GroupedPlan rows_plan(int64_t rows, int64_t experts, int64_t N, int64_t K, bool b_kc) {
     const double slices = (double)up_div(K, muon::kGemmSlice);
     GroupedPlan best{};
     double least = 1e300;
     for (const TileCost& c : kRowTiles) {
+        const GroupedPlan p{c.kind, c.rows, c.cols};
+        if (!fits(rows_grid(p, rows, experts, N), c.kind)) continue;
         const double t = tile_price(c, expected_blocks(rows, experts, c.rows) * (double)up_div(N, c.cols), slices);
         if (t >= least) continue;
         least = t;
-        best = {c.kind, c.rows, c.cols};
+        best = p;
     }
     // blocks of few rows: rounds of 256 workgroups, each a wait of its own
     const bool one = rows <= 16 * experts;
     const int cols = b_kc ? 16 : 32, tall = one ? 16 : 32;
     const double wgs = expected_blocks(rows, experts, tall) * (double)up_div(N, cols);
     const double t = 4.0 + std::ceil(wgs / 256) * (b_kc ? 2.2 + 0.038 * slices : 2.6 + 0.08 * slices);
-    if (t < least) best = {one ? muon::TILE_FEW16 : muon::TILE_FEW32, tall, cols};
-    return best;
+    const GroupedPlan few{one ? muon::TILE_FEW16 : muon::TILE_FEW32, tall, cols};
+    return t < least && fits(rows_grid(few, rows, experts, N), few.tile) ? few : best;
 }
 
 // The workgroups of a weight gradient: an expert's tiles, in runs of one length for each
@@ -112,7 +130,7 @@ int64_t weight_grid(const GroupedPlan& p, int64_t experts, int64_t M, int64_t N)
 
 // Few tiles of long sums leave CUs idle: then each expert's rows are cut into pieces,
 // whose sums meet in a second kernel (its launch, and each piece's sums once written
-// and read).
+// and read). rows 0: no tile's workgroups fit one launch.
 GroupedPlan weight_plan(int64_t rows, int64_t experts, int64_t M, int64_t N, bool raw) {
     // the longest of the sums, where some experts have half as much again as the mean
     const double all = 1.5 * (double)rows / (double)experts / muon::kGemmSlice;
@@ -123,7 +141,9 @@ GroupedPlan weight_plan(int64_t rows, int64_t experts, int64_t M, int64_t N, boo
         for (const TileCost& c : kWeightTiles) {
             if (raw && c.kind != muon::TILE_SMALL) continue;
             const GroupedPlan p{c.kind, c.rows, c.cols, pieces};
-            if (pieces > 1 && (weight_grid(p, experts, M, N) >= (int64_t)1 << 22 || M * N >= (int64_t)1 << 31)) continue;
+            const int64_t grid = weight_grid(p, experts, M, N);
+            if (!fits(grid, c.kind)) continue;
+            if (pieces > 1 && (grid >= (int64_t)1 << 22 || M * N >= (int64_t)1 << 31)) continue;
             double t = tile_price(c, (double)(experts * pieces * up_div(M, c.rows) * up_div(N, c.cols)), 1.0 + all / pieces);
             if (pieces > 1) t += 3.3 + out * (2 * pieces + 1) * 4e-6 / 4.9;
             if (t >= least) continue;
@@ -187,6 +207,7 @@ muon_status run_grouped(const muon_grouped* d, bool fwd, const void* a, const vo
     const int64_t ld_w = stride_of(d->ld_w, wc), step = weight_step(*d);
     const bool raw = !whole_chunks(a, A.ld, K) || !whole_chunks(w, ld_w, wc) || step % 8 != 0;
     const GroupedPlan plan = raw ? GroupedPlan{muon::TILE_SMALL, 64, 64} : rows_plan(d->rows, d->experts, N, K, b_kc);
+    if (plan.rows == 0 || !fits(rows_grid(plan, d->rows, d->experts, N), plan.tile)) return too_large();
     muon::GroupedArgs p{};
     p.a = a;
     p.b = w;
@@ -200,11 +221,8 @@ muon_status run_grouped(const muon_grouped* d, bool fwd, const void* a, const vo
     p.K = (int)K;
     p.tiles_n = (int)up_div(N, plan.cols);
     p.epi = epilogue_args(fwd, *e, o);
-    // every expert with rows may end inside a tile
-    const int64_t most = (d->rows < d->experts ? d->rows : d->experts) + d->rows / plan.rows;
-    const int64_t grid = most * p.tiles_n;
-    if (grid >= (int64_t)1 << 22) return too_large();
-    p.tiles_m = (int)most;
+    p.tiles_m = (int)most_blocks(d->rows, d->experts, plan.rows);
+    const int64_t grid = rows_grid(plan, d->rows, d->experts, N);
     TRY(check_device());
     return hip_status(muon::launch_grouped(p, plan.tile, raw, b_kc, d->dtype, (unsigned)grid,
                                            static_cast<hipStream_t>(stream)),
@@ -255,8 +273,8 @@ muon_status muon_grouped_linear_grad_weight(const muon_grouped* d, const void* x
         TRY(check_disjoint(Bi, {X, Y, Of}));
         const Tensor &A = io ? X : Y, &B = io ? Y : X;
         const GroupedPlan& plan = lay.plan;
+        if (plan.rows == 0) return too_large();
         const int64_t grid = weight_grid(plan, d->experts, lay.M, lay.N);
-        if (grid >= (int64_t)1 << 22) return too_large();
         TRY(check_workspace(workspace, ws_bytes, lay.need));
         const Tensor K{workspace, 1, (int64_t)lay.need, (int64_t)lay.need, 1};
         TRY(check_disjoint(K, {X, Y, W, Bi, Of}));
