@@ -440,13 +440,15 @@ muon_status muon_rmsnorm_backward(const muon_rmsnorm* d, const void* dy, const v
                                   void* workspace, size_t ws_bytes, void* stream);
 
 /* x [rows, cols] (row stride ld_x, any of the three types) to 8 bits, activations' or
- * gradients' blocks. */
+ * gradients' blocks. rows < 2^24, cols and strides at most 2^21, and rows times cols,
+ * as the next multiple of 512, at most 2^35 - 2^11. */
 muon_status muon_quantize(int64_t rows, int64_t cols, int64_t ld_x, int32_t dtype, const void* x, const muon_eight* q,
                           void* stream);
 
 /* A weight [rows, cols] (any of the three types; muon_step's params as they are) to
  * 8 bits, weights' blocks: q in its own order, q_t the other one [cols, rows], with
- * the same values and scales; either NULL. */
+ * the same values and scales; either NULL. rows, cols and strides at most 2^21, and
+ * fewer than 2^23 blocks. */
 muon_status muon_quantize_weight(int64_t rows, int64_t cols, int64_t ld_w, int32_t dtype, const void* w,
                                  const muon_eight* q, const muon_eight* q_t, void* stream);
 

@@ -251,7 +251,8 @@ muon_status muon_quantize(int64_t rows, int64_t cols, int64_t ld_x, int32_t dtyp
         TRY(check_eight(*q, cols, false));
         const int size = size_of(dtype);
         TRY(check_align(x, size, "x"));
-        if (rows * ((cols + 511) / 512) >= (int64_t)1 << 26)
+        // four segments of 512 columns a workgroup of 256 threads, fewer than 2^32 a launch
+        if (rows * ((cols + 511) / 512) > ((int64_t)1 << 26) - 4)
             return fail(MUON_E_SHAPE, "quantize: rows times cols too large");
         const Tensor X{x, rows, cols, stride_of(ld_x, cols), size}, Q = data_of(*q, rows, cols),
                      S = scales_of(*q, blocks_of(cols), rows);
