@@ -490,7 +490,9 @@ def linear_fp8_forward(x, w, bias=None, residual=None, activation="none", save_p
                        out=None, preact_out=None):
     """y = act(x w^T + bias) + residual in `dtype` (bf16 or fp16) of 8-bit x [tokens,
     in] and w [out, in]; with save_preact (or preact_out) also z = x w^T + bias
-    rounded to it: returns y, or (y, z). `out` may be `residual` itself."""
+    rounded to it: returns y, or (y, z). `out` may be `residual` itself. Each 8
+    products of consecutive k are summed to 13 bits below the largest of them, the
+    rest in float32."""
     _, device, dev = _first("x", x[0])
     code = _linear_type("dtype", dtype)
     act = _choice(ACTIVATIONS, activation, "activation")
