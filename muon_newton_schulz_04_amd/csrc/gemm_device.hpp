@@ -523,8 +523,7 @@ struct GemmShape {
     // the sums of the groups of waves but the first, behind the epilogue's staging
     static constexpr int MEET = (4 * 32 * kStagedRow<WN> + 1023) / 1024 * 1024;
     static_assert(4 * 32 * kStagedRow<WN> <= SMEM, "epilogue staging");
-    static constexpr int MEET_SUMS = MEET + (KG - 1) * TM * TN * 4;
-    static_assert(KG == 1 || (RING && !RAW && MEET_SUMS + (KG - 1) * 1024 * FRI <= SMEM), "groups of waves");
+    static_assert(KG == 1 || (RING && !RAW && MEET + (KG - 1) * TM * TN * 4 <= SMEM), "groups of waves");
 };
 
 // SUM: also the sums over k of the B (1) or A (2) operand's rows, for the bias
@@ -543,6 +542,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, char* smem, int ti,
     using OB = typename Shape::OB;
     constexpr int WM = Shape::WM, WN = Shape::WN, FRI = Shape::FRI, FRJ = Shape::FRJ, STAGE = Shape::STAGE;
     constexpr bool RING = Shape::RING;
+    static_assert(KG == 1 || SUM == 0, "the groups' sums over k do not meet");
     const int tid = KG > 1 ? threadIdx.x & 255 : threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int grp = KG > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8) : 0;
@@ -776,20 +776,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, char* smem, int ti,
                 *place(grp, n) = f32x4{a[4 * (n & 3)], a[4 * (n & 3) + 1], a[4 * (n & 3) + 2], a[4 * (n & 3) + 3]};
             });
         }
-        float* const meet_sums = reinterpret_cast<float*>(smem + Shape::MEET_SUMS);
-        if constexpr (SUM != 0) {
-            if (grp > 0)
-#pragma unroll
-                for (int f = 0; f < NSUM; ++f) meet_sums[((grp - 1) * NSUM + f) * 256 + tid] = sums[f];
-        }
         __syncthreads();
-        if constexpr (SUM != 0) {
-            if (grp == 0)
-#pragma unroll
-                for (int f = 0; f < NSUM; ++f)
-#pragma unroll
-                    for (int k = 1; k < KG; ++k) sums[f] += meet_sums[((k - 1) * NSUM + f) * 256 + tid];
-        }
         if (grp == 0) static_for<0, FRI * FRJ * 4>([&](auto n_c) {
             constexpr int n = decltype(n_c)::value;
             f32x16& a = acc[n / (4 * FRJ)][n / 4 % FRJ];
@@ -830,11 +817,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, char* smem, int ti,
 #pragma unroll
             for (int f = 0; f < NSUM; ++f) {
                 sums[f] += __shfl_xor(sums[f], 32, 64);
-                if (grp == 0 && wj == 1 && hi == 0) half[wi * WM + 32 * f + l32] = sums[f];
+                if (wj == 1 && hi == 0) half[wi * WM + 32 * f + l32] = sums[f];
             }
             __syncthreads();
         }
-        const bool mine = grp == 0 && (SUM == 1 ? ti == tj % g.tiles_m && wi == 0 : tj == ti % g.tiles_n && wj == 0);
+        const bool mine = SUM == 1 ? ti == tj % g.tiles_m && wi == 0 : tj == ti % g.tiles_n && wj == 0;
         if (mine) {
             const int at = (SUM == 1 ? wj * WN : wi * WM) + l32;
             const int n = (SUM == 1 ? j0 : i0) + at, end = SUM == 1 ? g.N : g.M;

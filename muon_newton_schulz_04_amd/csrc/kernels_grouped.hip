@@ -141,7 +141,7 @@ __device__ __forceinline__ Epilogue epilogue_of(const Epilogue& e, const Block& 
 // STAGES: buffers of the square tiles' rings. Two for 128 x 128, so that two
 // workgroups fit a CU, four for 64 x 64. KG: groups of waves that share the sum.
 template <typename T, int TM, int TN, int STAGES, int KG, bool BKC, bool RAW, int MODE>
-__global__ __launch_bounds__(256 * KG) __attribute__((amdgpu_waves_per_eu(KG > 2 ? KG : 2))) void k_grouped(
+__global__ __launch_bounds__(256 * KG) __attribute__((amdgpu_waves_per_eu(2))) void k_grouped(
     const GroupedArgs p) {
     __shared__ __attribute__((aligned(16))) char smem[GemmShape<T, TM, TN, true, BKC, RAW, STAGES, KG>::SMEM];
     Block b;
@@ -204,10 +204,9 @@ __device__ __forceinline__ int piece_rows(int rows, int pieces) {
     return ((rows + BK - 1) / BK + pieces - 1) / pieces * BK;
 }
 
-template <typename T, int TM, int TN, int STAGES, int KG, int SUM, bool RAW>
-__global__ __launch_bounds__(256 * KG) __attribute__((amdgpu_waves_per_eu(KG > 2 ? KG : 2))) void k_grouped_weight(
-    const GroupedArgs p) {
-    __shared__ __attribute__((aligned(16))) char smem[GemmShape<T, TM, TN, false, false, RAW, STAGES, KG>::SMEM];
+template <typename T, int TM, int TN, int STAGES, int SUM, bool RAW>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_grouped_weight(const GroupedArgs p) {
+    __shared__ __attribute__((aligned(16))) char smem[GemmShape<T, TM, TN, false, false, RAW, STAGES>::SMEM];
     // Each expert's tiles are shared by all XCDs, a contiguous run each, and the experts
     // come by their rows, most first: their sums are unlike long, and one XCD with the
     // longest, or a long one begun last, would keep the others waiting.
@@ -244,7 +243,7 @@ __global__ __launch_bounds__(256 * KG) __attribute__((amdgpu_waves_per_eu(KG > 2
     g.slices = (g.K + BK - 1) / BK;
     int ti, tj;
     tile_at(g, l, ti, tj);
-    gemm_tile<T, TM, TN, false, false, SUM, RAW, STAGES, KG, EPI_GRAD_WEIGHT>(g, smem, ti, tj, -1, 0, g.slices);
+    gemm_tile<T, TM, TN, false, false, SUM, RAW, STAGES, 1, EPI_GRAD_WEIGHT>(g, smem, ti, tj, -1, 0, g.slices);
 }
 
 // One expert's gradient (blockIdx.y) from its pieces, an element a thread, and behind it
@@ -319,25 +318,25 @@ hipError_t rows_t(const GroupedArgs& p, TileKind tile, bool raw, bool b_kc, unsi
     return hipGetLastError();
 }
 
-template <typename T, int TM, int TN, int STAGES, int KG, bool RAW>
+template <typename T, int TM, int TN, int STAGES, bool RAW>
 void weight_tile(const GroupedArgs& p, int sum, unsigned grid, hipStream_t st) {
     if (sum == 0)
-        k_grouped_weight<T, TM, TN, STAGES, KG, 0, RAW><<<grid, 256 * KG, 0, st>>>(p);
+        k_grouped_weight<T, TM, TN, STAGES, 0, RAW><<<grid, 256, 0, st>>>(p);
     else if (sum == 1)
-        k_grouped_weight<T, TM, TN, STAGES, KG, 1, RAW><<<grid, 256 * KG, 0, st>>>(p);
+        k_grouped_weight<T, TM, TN, STAGES, 1, RAW><<<grid, 256, 0, st>>>(p);
     else
-        k_grouped_weight<T, TM, TN, STAGES, KG, 2, RAW><<<grid, 256 * KG, 0, st>>>(p);
+        k_grouped_weight<T, TM, TN, STAGES, 2, RAW><<<grid, 256, 0, st>>>(p);
 }
 template <typename T>
 hipError_t weight_t(const GroupedArgs& p, TileKind tile, bool raw, int sum, unsigned grid, hipStream_t st) {
     if (raw)
-        weight_tile<T, 64, 64, 2, 1, true>(p, sum, grid, st);
+        weight_tile<T, 64, 64, 2, true>(p, sum, grid, st);
     else if (tile == TILE_TALL)
-        weight_tile<T, 256, 128, 2, 1, false>(p, sum, grid, st);
+        weight_tile<T, 256, 128, 2, false>(p, sum, grid, st);
     else if (tile == TILE_SQUARE)
-        weight_tile<T, 128, 128, 2, 1, false>(p, sum, grid, st);
+        weight_tile<T, 128, 128, 2, false>(p, sum, grid, st);
     else
-        weight_tile<T, 64, 64, 4, 1, false>(p, sum, grid, st);
+        weight_tile<T, 64, 64, 4, false>(p, sum, grid, st);
     return hipGetLastError();
 }
 

@@ -112,7 +112,7 @@ struct NormSums {
 
 // The tiles of the 8-bit and the grouped products: 256 x 128, 128 x 128 and 64 x 64, the
 // latter two also with groups of waves that share a tile's sum (two; four for the 8-bit
-// product's and the weight gradient's 64 x 64), and blocks of 16 or 32 rows of the
+// product's 64 x 64; none for the weight gradient), and blocks of 16 or 32 rows of the
 // kernels for few rows.
 enum TileKind { TILE_TALL, TILE_SQUARE, TILE_SQUARE_GROUPS, TILE_SMALL, TILE_SMALL_GROUPS, TILE_FEW16, TILE_FEW32 };
 
