@@ -32,9 +32,8 @@ __global__ __launch_bounds__(256) void k_quantize(const Quantize a) {
     uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) m = umax(m, magnitude(v[e]));
-    const ExactScale<F, sizeof(T) == 4> s(max16(m));
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < left ? s(v[e]) : 0.f;
+    const ScaleOf<F, T> s(max16(m));
+    s.scale8(v, left);
     // rows go on with zeros to the next multiple of 16
     if (left > 0 || (left > -8 && (c & 8)))
         *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.q) + row * a.ld_q + c) = pack8<F>(v);
@@ -64,12 +63,10 @@ __global__ __launch_bounds__(256) void k_quantize_weight(const QuantizeWeight a)
     m = umax(m, (uint32_t)__shfl_xor((int)m, 32, 64));
     if ((tid & 63) == 0) red[tid >> 6] = m;
     __syncthreads();
-    const ExactScale<F, sizeof(T) == 4> s(umax(umax(red[0], red[1]), umax(red[2], red[3])));
+    const ScaleOf<F, T> s(umax(umax(red[0], red[1]), umax(red[2], red[3])));
     // values past an edge are 0, and stay 0 beside a NaN
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[j][e] = j < down && e < left ? s(v[j][e]) : 0.f;
+    for (int j = 0; j < 8; ++j) s.scale8(v[j], j < down ? left : 0);
     const int rb = blockIdx.y, cb = blockIdx.x;
     if (a.q) {
         // rows go on with zeros to the next multiple of 16

@@ -19,7 +19,7 @@
 //    partial row, and a second kernel adds the partial rows in order.
 //
 // Measured, inputs in turn that no cache holds (a copy of 2 GiB reaches 4.9 TB/s on the
-// same box): 16384 x 1600 bf16, residual, 8-bit output 37.4 us a call (184 MB, 4.9 TB/s);
+// same box): 16384 x 1600 bf16, residual, 8-bit output 37.1 us a call (184 MB, 5.0 TB/s);
 // its backward with the residual's gradient 45 (210 MB; the pass 40, the join of 768
 // partial rows 4). One row takes 4 us, the call 13 on the host. Nontemporal
 // loads of x and the residual: no difference.
@@ -44,14 +44,13 @@ __device__ __forceinline__ void emit(const RmsForward& n, int64_t row, int c, in
         uint32_t m = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = umax(m, magnitude(t[e]));
-        // (times a rounded reciprocal 36.4 us, not 37.4, but 2 more of 16384 x 1600 values
-        // on the wrong side of a border between two 8-bit values)
-        const ExactScale<F, true> s(max16(m));
+        const ScaleOf<F, float> s(max16(m));
         // rows go on with zeros to the next multiple of 16
         if (left > -8 && (left > 0 || (c & 8))) {
             float u[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = e < left ? s(t[e]) : 0.f;
+            for (int e = 0; e < 8; ++e) u[e] = t[e];
+            s.scale8(u, left);
             const u32x2 q = pack8<F>(u);
             __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(n.q) + row * n.ld_q + c));
         }
