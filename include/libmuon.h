@@ -425,7 +425,8 @@ typedef struct muon_eight {
  * residual stream (residual and sum come together; sum may be the very tensor of x
  * or residual, same address and stride). y: in dtype, or NULL; q: in 8 bits, from
  * the unrounded values, or NULL (one of the two is given, or both). weight [cols] or
- * NULL (1); rstd [rows] is written. Squares beyond float32 make y 0. */
+ * NULL (1); rstd [rows] is written. Squares beyond float32 make y 0; with eps 0, a row
+ * whose squares all vanish in float32 (zeros among them) has no finite y. */
 muon_status muon_rmsnorm_forward(const muon_rmsnorm* d, const void* x, const void* residual, const float* weight,
                                  void* sum, void* y, const muon_eight* q, float* rstd, void* stream);
 

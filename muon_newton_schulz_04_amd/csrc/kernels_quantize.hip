@@ -1,7 +1,7 @@
 // Matrices to 8-bit floating point with a float32 scale for each block of 128, on
 // gfx950. Bound by HBM: each element is read once and written once (a weight in
 // both orders twice, from one read). 2051 x 6400 bf16 9.1 us a call (39 MB), 1600 x 6400
-// float32 in both orders 12.8 (61 MB, 4.8 TB/s; a copy of 2 GiB 4.9).
+// float32 in both orders 12.5 (61 MB, 4.9 TB/s; a copy of 2 GiB 4.9).
 //
 //  * Rows (activations, gradients): a block is 128 columns of a row, 16
 //    neighbouring lanes of a wave; a wave takes 512 columns of a row at a time.
@@ -43,7 +43,10 @@ __global__ __launch_bounds__(256) void k_quantize(const Quantize a) {
 template <typename T>
 __global__ __launch_bounds__(256) void k_quantize_weight(const QuantizeWeight a) {
     constexpr int F = EIGHT_E4M3;
-    constexpr int PITCH = 136;  // bytes of a row in LDS: the 16 lanes of a column group write to 16 bank pairs
+    // Bytes of a row in LDS. Neighbouring lanes write 8 rows apart, 272 banks, so that 16 of
+    // them begin at 4 of the 64 (any pitch of whole 8 bytes puts them on 4 at most): 74% of
+    // the LDS-active clocks are conflicts, 1 us of a CU's, beside the wait for HBM.
+    constexpr int PITCH = 136;
     __shared__ __attribute__((aligned(16))) uint8_t turn[128 * PITCH];
     __shared__ uint32_t red[4];
     const int tid = threadIdx.x;

@@ -26,8 +26,9 @@
 // What bounds it: 8192^3 492 us (2.23 PFLOP/s; a library product with one scale for a
 // whole matrix, which adds nothing per block, 2.55 to 2.88). The matrix unit is busy 51% of
 // the clocks, the vector unit 41%: the scales' fmas cost 15 to 20% (without them 2.52
-// PFLOP/s), LDS reads and the barriers the rest. 16384 x 1600 -> 6400 with bias, GELU and
-// kept pre-activation 219 us: 13 blocks of K a tile, then 64 KB of activations each, two
+// PFLOP/s), the barriers and LDS reads the rest: a slice begins with its first fragments'
+// reads, while none of the wave's products runs. 16384 x 1600 -> 6400 with bias, GELU and
+// kept pre-activation 219 to 228 us, by the box: 13 blocks of K a tile, then 64 KB of activations each, two
 // outputs; the matrix unit is busy 33%. The library's bare product takes 196.
 // Tried: 32 x 32 x 64 instructions (half the reads, but 16 registers a block sum: 802 us
 // for 8192^3 against 525 then); a 256 x 256 tile of 128 x 128 a wave (more than the 256
@@ -292,7 +293,8 @@ __global__ __launch_bounds__(256 * KG) __attribute__((amdgpu_waves_per_eu(KG > 2
 // block's 16 columns and all of K; the waves take its slices in turn, each through a
 // ring of its own in LDS (a wave waits for its own loads, X's scales among them). Their
 // sums meet in LDS, in wave order. One row, 1600 -> 6400: 7.8 us, of which the 10 MB of
-// W are 2; a launch and two latencies are the rest.
+// W are 2. The rest is a launch, and two rounds of workgroups (400 of them, and 136 KB of
+// LDS lets one run on a CU) that each wait for W's scales, then for their first slice.
 template <typename T, int MT, int F>
 __global__ __launch_bounds__(512) void k_scaled_few(const ScaledArgs p) {
     constexpr int WB = 2048, XB = MT * 2048;      // bytes of a slice of W, of X
